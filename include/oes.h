@@ -389,6 +389,181 @@ oes_status oes_layers_ffn(oes_layers *p, int32_t layer, const void *x, const int
                           const float *w, int32_t n, int32_t k, void *y, void *workspace,
                           int64_t workspace_bytes, void *compute_stream);
 
+/* ------------------------------------------------------------------ the layer around the step */
+/*
+ * The operators a decoder layer runs before its expert step: projections with
+ * 4-bit weights, rotary positions, attention over a paged key / value cache,
+ * and keeping that cache within its share of HBM (FreeToken architecture
+ * walk-through §4: KV pools next to the expert cache, VRAM moving between the
+ * two; §6: quantised linear kernels).  All of them only enqueue kernels on
+ * `stream` - no allocation, no memset node, no sync - and may be captured into
+ * a HIP graph.  Device pointers belong to the device of the call (the current
+ * one).  Work that shares a workspace, an output or a cache must be ordered by
+ * the caller (one stream, or events); two captured graphs that may run at the
+ * same time need a workspace each.
+ */
+
+/* y[t, r] = sum_k W[r, k] * x[t, k] for n rows of x: a product with 4-bit
+ * weights and group scales, in the layout of one matrix of the expert banks of
+ * `format` with out = N rows and in = K columns:
+ *   OES_Q4_0     w0 codes [N, K/2], w1 fp16 [N, K/32], w2 unused (NULL)
+ *   OES_NVFP4    w0 codes [N, K/2], w1 e4m3 [N, K/16], w2 fp16 [N]
+ *   OES_MXFP4_T  w0 blocks [K/32, N, 16], w1 e8m0 [K/32, N], w2 bias bf16 [N] or
+ *                NULL (none)
+ * Other formats: OES_ERR_UNSUPPORTED.  x is bf16 with rows x_stride elements
+ * apart, y bf16 with rows y_stride elements apart.  Sums are fp32; the weights
+ * are used exactly (no rounding on the way); y is rounded to nearest even once.
+ * K a positive multiple of 32 up to 2^20, N >= 1, n >= 0; w0, w1 and the rows of
+ * x 16-byte aligned, w2 and y 2-byte aligned, x_stride >= K, y_stride >= N.  y
+ * must not overlap an input.  Async. */
+oes_status oes_linear(int32_t format, const void *w0, const void *w1, const void *w2, int32_t N, int32_t K,
+                      const void *x, int64_t x_stride, void *y, int64_t y_stride, int32_t n, void *stream);
+
+/* A paged key / value cache of one layer, in caller-owned device memory.  Entry
+ * j of sequence b stands in row j % page_size of page
+ * table[b * table_stride + j / page_size]; the head_dim values of head h of row r
+ * of page p start k_page * p + k_row * r + k_head * h elements after k (and the
+ * same with v_*), so pages may be head-major or row-major.
+ *   elem       OES_ELEM_BF16, or OES_ELEM_E4M3 with value = code * k_scale (v_scale)
+ *   len        int32 [batch]: entries of each sequence, the new tokens of a
+ *              step included
+ *   status     int32 device word or NULL: a kernel that meets a table entry
+ *              outside [0, num_pages), a length outside [0, max_pages *
+ *              page_size] or a q_start that is no ascending sequence within the
+ *              rows stores OES_ERR_ARG there (nothing else ever writes it).
+ *              Such an entry is treated as masked and is not written; lengths
+ *              and row ranges are clamped.
+ * Limits: head_dim a multiple of 16 in [16, 256], page_size >= 1, kv_heads in
+ * [1, 1024], batch >= 0, max_pages >= 1, max_pages * page_size <= 2^30; k, v and
+ * their strides keep every head row 16-byte aligned; k_scale, v_scale finite
+ * and positive (1 for bf16).  The struct is read during the call only. */
+typedef struct {
+  void *k, *v;
+  const int32_t *table;
+  const int32_t *len;
+  int32_t *status;
+  int64_t k_page, k_row, k_head;   /* strides in elements */
+  int64_t v_page, v_row, v_head;
+  int64_t table_stride;
+  int32_t elem, num_pages, page_size, kv_heads, head_dim, batch, max_pages;
+  float k_scale, v_scale;
+} oes_kv;
+
+/* Element offsets of head 0 of entry j of sequence b in k and v, from a host
+ * copy of the page table, by the routine that the kernels use; OES_ERR_ARG for
+ * an entry outside the table or a page outside the cache.  Host code, for
+ * tests. */
+oes_status oes_debug_kv_entry(const oes_kv *kv, const int32_t *host_table, int32_t b, int32_t j, int64_t *k_off,
+                              int64_t *v_off);
+
+/* Rotary frequencies (host code): freq[i], i < rot_dim / 2, is the angle in
+ * radians per position of pair i, and *mscale the factor on the rotated values.
+ *   OES_ROPE_NONE    f_i = base^(-2 i / rot_dim)
+ *   OES_ROPE_LINEAR  f_i / factor (positions interpolated)
+ *   OES_ROPE_NTK     f_i of the base  base * factor^(rot_dim / (rot_dim - 2))
+ *   OES_ROPE_YARN    f_i / factor for pairs that turn less than once over
+ *                    trained_len positions, f_i for those that turn 32 times or
+ *                    more, a linear ramp over the pair index between the two
+ *                    (bounds rounded outwards); *mscale = 0.1 ln(factor) + 1
+ * Errors: OES_ERR_ARG for rot_dim odd, < 2 (< 4 for NTK) or > 256, base <= 1,
+ * factor < 1, trained_len < 1 (YARN), an unknown scaling, NULL. */
+enum { OES_ROPE_NONE = 0, OES_ROPE_LINEAR = 1, OES_ROPE_NTK = 2, OES_ROPE_YARN = 3 };
+oes_status oes_rope_freqs(int32_t scaling, int32_t rot_dim, double base, double factor, int32_t trained_len,
+                          double *freq, float *mscale);
+
+/* Rotary positions: in every head, pair i of the first rot_dim values is turned
+ * by the angle a = pos[t] * freq[i]:
+ *   y0 = mscale * (x0 cos a - x1 sin a),  y1 = mscale * (x0 sin a + x1 cos a)
+ * where pair i is (i, i + rot_dim / 2) for OES_ROPE_HALF and (2 i, 2 i + 1) for
+ * OES_ROPE_INTERLEAVED; values behind rot_dim are copied.  The angle is formed
+ * and reduced in fp64 (positions of any size keep their accuracy), sine,
+ * cosine and products are fp32, y is rounded to bf16 once.
+ *   x, y   bf16 [n, heads, head_dim]: token t, head h at t * row + h * head
+ *          elements; y may be x (then with the same strides), otherwise they
+ *          must not overlap
+ *   freq   double [rot_dim / 2] device, pos int32 [n] device
+ * head_dim as for oes_kv, rot_dim even in [2, head_dim], heads in [1, 4096]; rows
+ * 16-byte aligned.  Async. */
+enum { OES_ROPE_HALF = 0, OES_ROPE_INTERLEAVED = 1 };
+oes_status oes_rope(const void *x, int64_t x_row, int64_t x_head, void *y, int64_t y_row, int64_t y_head, int32_t n,
+                    int32_t heads, int32_t head_dim, int32_t rot_dim, int32_t layout, const double *freq,
+                    float mscale, const int32_t *pos, void *stream);
+
+/* oes_rope on the q and k rows of a step's new tokens, with k (rotated) and v
+ * written into the cache in the same launch.  Rows [q_start[b], q_start[b + 1])
+ * (int32 [batch + 1] device, ascending, at most n) are the new tokens of
+ * sequence b; the i-th of its q_len becomes entry len[b] - q_len + i (none
+ * before entry 0).  q_out may be q; rows from q_start[batch] on are left as
+ * they are, in q_out and in the cache.  An e4m3 cache stores
+ * value / scale, clamped to +-448 and rounded to nearest even (NaN stays NaN).
+ * Two tokens must not share an entry (pages that several sequences share are
+ * read-only).  q, q_out bf16 [n, q_heads, head_dim], k, v bf16 [n, kv_heads,
+ * head_dim], strides as in oes_rope.  Async. */
+oes_status oes_rope_append(const oes_kv *kv, const void *q, int64_t q_row, int64_t q_head, void *q_out,
+                           int64_t qo_row, int64_t qo_head, int32_t q_heads, const void *k, int64_t k_row,
+                           int64_t k_head, const void *v, int64_t v_row, int64_t v_head, int32_t n,
+                           const int32_t *q_start, int32_t rot_dim, int32_t layout, const double *freq,
+                           float mscale, const int32_t *pos, void *stream);
+
+/* Attention of a chunk of new tokens over the paged cache (prompts, chunks of
+ * them and single decoded tokens alike, ragged in one call).  Row t is new
+ * token i of sequence b (q_start as in oes_rope_append; the chunk's own keys and
+ * values are already in the cache) and sees entries j with
+ *   j <= at and, for window > 0, j > at - window,   at = len[b] - q_len + i.
+ *   out[t, h] = sum_j p_j v_j,  p = softmax_j(scale * q[t, h] . k_j)
+ *   lse[t, h] = ln sum_j exp(scale * q[t, h] . k_j)     (natural log)
+ * Query head h reads head h / (q_heads / kv_heads) of the cache.  A row that
+ * sees nothing gets out = 0 and lse = -inf.  Rows from q_start[batch] on are
+ * left as they were.  Entries that a row does not see do not reach it, whatever
+ * they hold (infinities and NaN included).  Scores, softmax statistics and sums
+ * are fp32; the probabilities are rounded to bf16 for the product with v; out is
+ * rounded to bf16 once.
+ *   q, out  bf16 [n, q_heads, head_dim] with row and head strides (elements,
+ *           16-byte aligned rows); lse fp32 [n, q_heads] or NULL
+ *   q_heads a multiple of kv_heads, q_heads / kv_heads <= 128; scale finite,
+ *   positive; window >= 0 (0: none)
+ *   workspace: device, 16-byte aligned, >= oes_attn_workspace bytes for the
+ *   same kv sizes, q_heads and n (the splits of a long cache are summed through
+ *   it, in a fixed order).  Async. */
+oes_status oes_attn_workspace(const oes_kv *kv, int32_t q_heads, int32_t n, int64_t *bytes);
+oes_status oes_attn(const oes_kv *kv, const void *q, int64_t q_row, int64_t q_head, void *out, int64_t o_row,
+                    int64_t o_head, float *lse, int32_t q_heads, int32_t n, const int32_t *q_start, float scale,
+                    int32_t window, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* The attention weight that each cache entry receives from a step's new tokens,
+ * added to what it has received before:
+ *   acc[b, g, j] += sum over the rows t of sequence b that see entry j, and the
+ *                   query heads h that read cache head g, of
+ *                   exp(scale * q[t, h] . k_j - lse[t, h])
+ * with q, q_start, scale and window as in oes_attn and lse as it returned it (a
+ * row with lse = -inf adds nothing).  acc fp32 [batch, kv_heads, acc_stride],
+ * acc_stride >= max_pages * page_size; values from len[b] on are left as they are.
+ * Sums run in a fixed order (no atomics).  Async. */
+oes_status oes_attn_weigh(const oes_kv *kv, const void *q, int64_t q_row, int64_t q_head, const float *lse,
+                          int32_t q_heads, int32_t n, const int32_t *q_start, float scale, int32_t window,
+                          float *acc, int64_t acc_stride, void *stream);
+
+/* Eviction by accumulated attention weight: every (sequence, cache head) of more
+ * than `budget` entries keeps its `first` first and `last` last entries and, of
+ * the others, those with the largest acc, up to budget in all (equal ones: the
+ * lower index stays; -0 counts as 0 and NaN as less than any number).  The kept
+ * entries close up in place, in their order: k, v and acc of entry
+ * kept[b, g, i] move to entry i.  Keys keep the rotation of the position they
+ * were written at, so the next token's position is unchanged by an eviction.
+ *   kept     int32 [batch, kv_heads, budget] out: the old index of entry i,
+ *            -1 for i >= new_len[b]
+ *   new_len  int32 [batch] out: min(len, budget); may be kv->len itself
+ * What stands in entries from new_len on is left as it was.  A sequence of at
+ * most budget entries is left untouched (kept counts up).  Pages of a sequence
+ * that is cut must not be shared with another.  A sequence with a page outside
+ * the cache among its used pages keeps its entries as they are (its kept is -1,
+ * its new_len is len).  budget >= 1, first, last >= 0, first + last <= budget.
+ * workspace: device, 16-byte aligned, >= oes_kv_evict_workspace bytes.  Async. */
+oes_status oes_kv_evict_workspace(const oes_kv *kv, int32_t budget, int64_t *bytes);
+oes_status oes_kv_evict(const oes_kv *kv, float *acc, int64_t acc_stride, int32_t budget, int32_t first,
+                        int32_t last, int32_t *kept, int32_t *new_len, void *workspace, int64_t workspace_bytes,
+                        void *stream);
+
 /* ------------------------------------------------------------------ measurement probes */
 /* Ceilings the benchmark divides by.  All sync and return times in ms.
  * oes_probe_h2d_dma: one hipMemcpyAsync of `bytes` from pinned host to device.

@@ -15,6 +15,14 @@ The names follow the C ABI in ``include/oes.h``:
     Layers(schema, depth, device)              .set_source / .prefetch / .ffn
     CpuMoe(schema, threads)                    .set_source / .run   (hybrid backend, host)
     hybrid_decide(format, cpu, pcie) / combine_cpu(y, y_cpu)
+
+and, for the layer around the expert step:
+
+    linear(format, x, banks, y)                4-bit weights in a bank format
+    KvPages(k, v, table, len)                  a paged key / value cache (caller-owned tensors)
+    rope_freqs(rot_dim, ...) / rope(x, y, ...) / rope_append(q, q_out, k, v, ..., kv, q_start)
+    attn(q, out, kv, q_start, scale, workspace) / attn_weigh(q, lse, kv, q_start, scale, acc)
+    kv_evict(kv, acc, budget, kept, new_len, workspace)
 """
 import ctypes
 import os
@@ -34,6 +42,8 @@ FFN_AUTO, FFN_PER_PAIR, FFN_GROUPED = 0, 1, 2
 COPY_ZERO, COPY_SDMA = 0, 1
 OK, ERR_ARG, ERR_CAPACITY, ERR_HIP, ERR_NOMEM, ERR_STATE, ERR_UNSUPPORTED = 0, -1, -2, -3, -4, -5, -6
 FFN_NOALLOC_SCRATCH_BYTES = 16 << 20   # OES_FFN_NOALLOC_SCRATCH_BYTES of include/oes.h
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 MAX_BANKS = 6
 MAX_SLOTS = 4096
 
@@ -71,6 +81,17 @@ class Stats(ctypes.Structure):
                 ("last_misses", ctypes.c_uint32), ("failed_steps", ctypes.c_int32),
                 ("last_indices", ctypes.c_uint32), ("last_missing_full", ctypes.c_uint32),
                 ("cpu_experts", ctypes.c_uint64)]
+
+
+class Kv(ctypes.Structure):
+    """oes_kv of include/oes.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p), ("len", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)] + \
+               [(f, ctypes.c_int64) for f in ("k_page", "k_row", "k_head", "v_page", "v_row", "v_head",
+                                              "table_stride")] + \
+               [(f, ctypes.c_int32) for f in ("elem", "num_pages", "page_size", "kv_heads", "head_dim", "batch",
+                                              "max_pages")] + \
+               [("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
 _lib = None
@@ -131,6 +152,17 @@ _SIGS = {
     "oes_hybrid_decide": (_I32, [_I32, ctypes.c_double, ctypes.c_double, ctypes.c_double, _PI32,
                                  ctypes.POINTER(ctypes.c_double)]),
     "oes_combine_cpu": (_I32, [_P, _P, _I64, _P]),
+    "oes_linear": (_I32, [_I32, _P, _P, _P, _I32, _I32, _P, _I64, _P, _I64, _I32, _P]),
+    "oes_debug_kv_entry": (_I32, [_P, _P, _I32, _I32, _PI64, _PI64]),
+    "oes_rope_freqs": (_I32, [_I32, _I32, ctypes.c_double, ctypes.c_double, _I32, _P, _PF]),
+    "oes_rope": (_I32, [_P, _I64, _I64, _P, _I64, _I64, _I32, _I32, _I32, _I32, _I32, _P, ctypes.c_float, _P, _P]),
+    "oes_rope_append": (_I32, [_P, _P, _I64, _I64, _P, _I64, _I64, _I32, _P, _I64, _I64, _P, _I64, _I64, _I32, _P, _I32,
+                               _I32, _P, ctypes.c_float, _P, _P]),
+    "oes_attn_workspace": (_I32, [_P, _I32, _I32, _PI64]),
+    "oes_attn": (_I32, [_P, _P, _I64, _I64, _P, _I64, _I64, _P, _I32, _I32, _P, ctypes.c_float, _I32, _P, _I64, _P]),
+    "oes_attn_weigh": (_I32, [_P, _P, _I64, _I64, _P, _I32, _I32, _P, ctypes.c_float, _I32, _P, _I64, _P]),
+    "oes_kv_evict_workspace": (_I32, [_P, _I32, _PI64]),
+    "oes_kv_evict": (_I32, [_P, _P, _I64, _I32, _I32, _I32, _P, _P, _P, _I64, _P]),
     "oes_hybrid_workspace": (_I32, [_P, _I32, _I32, _PI64, _PI64]),
     "oes_hybrid_step": (_I32, [_P, _P, _I32, _P, _P, _P, _I32, _I32, _P, _P, _P, _I64, _P, _I64, _P, _I64, _I32,
                                ctypes.c_double, _P]),
@@ -509,3 +541,232 @@ def probe_mfma_f8f4(blocks, iters, sink, stream=None):
     ms, flops = ctypes.c_float(), ctypes.c_double()
     _check(lib().oes_probe_mfma_f8f4(blocks, iters, _ptr(sink), _stream(stream), ctypes.byref(ms), ctypes.byref(flops)))
     return ms.value, flops.value
+
+
+# ---------------------------------------------------------------- the layer around the step
+# These calls take torch tensors and check them before the library does: element
+# types, shapes that belong together, one device.  They launch on the tensors' device.
+def _bad(message):
+    raise OesError(ERR_ARG, f"OES_ERR_ARG: {message}")
+
+
+def _elem(t):
+    """Cache element of a tensor's type: bf16 (or its bits as 16-bit integers), e4m3 (or its bytes)."""
+    import torch
+    kinds = {torch.bfloat16: ELEM_BF16, torch.int16: ELEM_BF16, torch.float8_e4m3fn: ELEM_E4M3,
+             torch.uint8: ELEM_E4M3}
+    if t.dtype not in kinds:
+        _bad(f"element type {t.dtype}: bfloat16 (or int16 bits) or float8_e4m3fn (or uint8 bytes)")
+    return kinds[t.dtype]
+
+
+def _typed(name, t, kinds, shape=None, device=None, packed=True):
+    """Check one tensor argument: its type (names of torch types), shape, device, and that it is contiguous."""
+    if str(t.dtype)[6:] not in kinds:
+        _bad(f"{name}: element type {t.dtype}, not {' or '.join(kinds)}")
+    if shape is not None and t.shape != shape:
+        _bad(f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}")
+    if device is not None and t.device != device:
+        _bad(f"{name}: on {t.device}, not {device}")
+    if packed and not t.is_contiguous():
+        _bad(f"{name} must be contiguous")
+
+
+_BF16 = ("bfloat16", "int16")
+
+
+def _heads(name, t, device=None):
+    """(address, row stride, head stride) of bf16 [n, heads, head_dim] rows."""
+    if t.dim() != 3:
+        _bad(f"{name}: [n, heads, head_dim], not {tuple(t.shape)}")
+    _typed(name, t, _BF16, None, device, False)
+    row, head, one = t.stride()
+    if one != 1 and t.shape[2] > 1:
+        _bad(f"{name}: the head_dim values of a head must be adjacent")
+    return t.data_ptr(), row, head
+
+
+def _enqueue(device, fn, *args, stream=None):
+    """fn(*args, stream) on `device`: its current stream unless one is given."""
+    import torch
+    if device.type != "cuda":
+        _bad(f"tensors are on {device}, not on a GPU")
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream)))
+
+
+def linear(fmt, x, banks, y, stream=None):
+    """y[n, N] = x[n, K] . W^T: 4-bit weights W [N, K] as the banks of one matrix of `fmt` (oes_linear).
+
+    banks: q4_0 (codes, d), nvfp4 (codes, scale, global), mxfp4_t (blocks, scales, bias or None).
+    """
+    f = FORMAT_IDS.get(fmt, fmt)
+    w = list(banks) + [None] * (3 - len(banks))
+    if x.dim() != 2 or y.dim() != 2 or len(w) != 3:
+        _bad("x [n, K], y [n, N] and two or three banks")
+    (n, K), N, dev = x.shape, y.shape[1], x.device
+    _typed("x", x, _BF16, None, None, False)
+    _typed("y", y, _BF16, (n, N), dev, False)
+    if (x.stride(1) != 1 and K > 1) or (y.stride(1) != 1 and N > 1):
+        _bad("the values of a row of x or y must be adjacent")
+    if w[0] is None or w[1] is None:
+        _bad("the codes or scales are missing")
+    half = ("float16", "int16")
+    sizes = {Q4_0: (N * K // 2, N * (K // 32), None), NVFP4: (N * K // 2, N * (K // 16), N),
+             MXFP4_T: (N * K // 2, N * (K // 32), N)}.get(f)
+    types = {Q4_0: half, NVFP4: ("uint8", "float8_e4m3fn"), MXFP4_T: ("uint8", "float8_e8m0fnu")}.get(f)
+    if sizes:
+        _typed("codes", w[0], ("uint8",), None, dev)
+        _typed("scales", w[1], types, None, dev)
+        if w[2] is not None:
+            _typed("third bank", w[2], half if f == NVFP4 else _BF16, None, dev)
+        for name, t, size in zip(("codes", "scales", "third bank"), w, sizes):
+            if t is not None and size is not None and t.numel() != size:
+                _bad(f"{name}: {t.numel()} elements, {size} belong to N = {N}, K = {K}")
+    _enqueue(dev, lib().oes_linear, f, _ptr(w[0]), _ptr(w[1]), _ptr(w[2]), N, K, x.data_ptr(), x.stride(0), y.data_ptr(),
+             y.stride(0), n, stream=stream)
+
+
+class KvPages:
+    """A paged key / value cache in caller-owned tensors (oes_kv).
+
+    k, v    [pages, page_size, kv_heads, head_dim], any strides over the first three (a head-major
+            cache is passed transposed), bf16 or e4m3 with k_scale, v_scale
+    table   int32 [batch, max_pages], len int32 [batch], both on the GPU and read by every call
+
+    ``status`` is an int32 word on the GPU that a kernel sets when it meets a bad page, length or
+    row range; ``check()`` reads and clears it.
+    """
+
+    def __init__(self, k, v, table, len, k_scale=1.0, v_scale=1.0):
+        import torch
+        if k.dim() != 4 or v.shape != k.shape:
+            _bad(f"k and v: [pages, page_size, kv_heads, head_dim], not {tuple(k.shape)} and {tuple(v.shape)}")
+        if _elem(k) != _elem(v) or k.dtype != v.dtype:
+            _bad("k and v must have one element type")
+        if (k.stride(3) != 1 or v.stride(3) != 1) and k.shape[3] > 1:
+            _bad("the head_dim values of a head must be adjacent")
+        _typed("v", v, (str(k.dtype)[6:],), None, k.device, False)
+        _typed("table", table, ("int32",), None, k.device, False)
+        if table.dim() != 2 or (table.stride(1) != 1 and table.shape[1] > 1):
+            _bad("table: [batch, max_pages] with adjacent columns")
+        _typed("len", len, ("int32",), (table.shape[0],), k.device)
+        self.k, self.v, self.table, self.len = k, v, table, len
+        self.device = k.device
+        self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self.kv_heads, self.head_dim, self.batch = k.shape[2], k.shape[3], table.shape[0]
+        self.capacity = table.shape[1] * k.shape[1]
+        ks, vs = k.stride(), v.stride()
+        self._kv = Kv(k.data_ptr(), v.data_ptr(), table.data_ptr(), len.data_ptr(), self.status.data_ptr(),
+                      *ks[:3], *vs[:3], table.stride(0), _elem(k), k.shape[0], k.shape[1], k.shape[2], k.shape[3],
+                      table.shape[0], table.shape[1], k_scale, v_scale)
+        self._ref = ctypes.byref(self._kv)
+
+    def check(self):
+        """Syncs; raises OesError if a call since the last check met a bad page, length or row range."""
+        bad = int(self.status.item())
+        self.status.zero_()
+        if bad:
+            raise OesError(bad, "a page, length or row range outside the cache")
+
+
+def _q_start(kv, q_start):
+    _typed("q_start", q_start, ("int32",), (kv.batch + 1,), kv.device)
+    return q_start.data_ptr()
+
+
+def rope_freqs(rot_dim, base=10000.0, scaling="none", factor=1.0, trained_len=4096):
+    """(angle per position of every pair, float64 [rot_dim / 2], and the factor on the rotated values)."""
+    freq = np.empty(max(1, int(rot_dim) // 2), dtype=np.float64)
+    m = ctypes.c_float()
+    _check(lib().oes_rope_freqs(ROPE_SCALINGS.get(scaling, scaling), int(rot_dim), float(base), float(factor),
+                                int(trained_len), freq.ctypes.data, ctypes.byref(m)))
+    return freq, m.value
+
+
+def rope(x, y, freq, pos, layout="half", mscale=1.0, stream=None):
+    """y = x [n, heads, head_dim] turned by its positions (oes_rope); y may be x."""
+    xp, yp = _heads("x", x), _heads("y", y, x.device)
+    n, heads, D = x.shape
+    if y.shape != x.shape:
+        _bad(f"y: shape {tuple(y.shape)}, not {tuple(x.shape)}")
+    _typed("freq", freq, ("float64",), None, x.device)
+    _typed("pos", pos, ("int32",), (n,), x.device)
+    _enqueue(x.device, lib().oes_rope, *xp, *yp, n, heads, D, 2 * freq.numel(), ROPE_LAYOUTS.get(layout, layout),
+             freq.data_ptr(), mscale, pos.data_ptr(), stream=stream)
+
+
+def rope_append(q, q_out, k, v, freq, pos, kv, q_start, layout="half", mscale=1.0, stream=None):
+    """rope on a step's q and k; k and v become the last entries of their sequences (oes_rope_append)."""
+    dev = kv.device
+    qp, op, kp, vp = _heads("q", q, dev), _heads("q_out", q_out, dev), _heads("k", k, dev), _heads("v", v, dev)
+    n, heads, D = q.shape
+    # k and v may end with the last sequence's rows, before q's spare ones
+    if q_out.shape != q.shape or D != kv.head_dim or k.shape != v.shape or k.shape[1:] != (kv.kv_heads, D) \
+            or k.shape[0] > n:
+        _bad("q_out has the shape of q; k and v are [rows, kv_heads, head_dim], with no more rows than q")
+    _typed("freq", freq, ("float64",), None, dev)
+    _typed("pos", pos, ("int32",), (k.shape[0],), dev)
+    _enqueue(dev, lib().oes_rope_append, kv._ref, *qp, *op, heads, *kp, *vp, k.shape[0], _q_start(kv, q_start),
+             2 * freq.numel(), ROPE_LAYOUTS.get(layout, layout), freq.data_ptr(), mscale, pos.data_ptr(),
+             stream=stream)
+
+
+def attn_workspace_bytes(kv, q_heads, n):
+    b = _I64()
+    _check(lib().oes_attn_workspace(kv._ref, q_heads, n, ctypes.byref(b)))
+    return b.value
+
+
+def attn(q, out, kv, q_start, scale, workspace, window=0, lse=None, stream=None):
+    """Attention of the new tokens' rows q over the cache into out, log-sum-exps into lse (oes_attn)."""
+    dev = kv.device
+    qp, op = _heads("q", q, dev), _heads("out", out, dev)
+    n, heads, D = q.shape
+    if out.shape != q.shape or D != kv.head_dim:
+        _bad(f"q and out: [n, q_heads, {kv.head_dim}], not {tuple(q.shape)} and {tuple(out.shape)}")
+    if lse is not None:
+        _typed("lse", lse, ("float32",), (n, heads), dev)
+    if workspace.device != dev:
+        _bad("the workspace is on another device")
+    _enqueue(dev, lib().oes_attn, kv._ref, *qp, *op, _ptr(lse), heads, n, _q_start(kv, q_start), scale, window,
+             workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream=stream)
+
+
+def _acc(kv, acc):
+    _typed("acc", acc, ("float32",), None, kv.device)
+    if acc.dim() != 3 or acc.shape[:2] != (kv.batch, kv.kv_heads):
+        _bad(f"acc: [batch, kv_heads, entries], not {tuple(acc.shape)}")
+    return acc.data_ptr(), acc.shape[2]
+
+
+def attn_weigh(q, lse, kv, q_start, scale, acc, window=0, stream=None):
+    """acc[batch, kv_heads, entries] += the attention weight every entry received from q's rows (oes_attn_weigh)."""
+    dev = kv.device
+    qp = _heads("q", q, dev)
+    n, heads, D = q.shape
+    if D != kv.head_dim:
+        _bad(f"q: head_dim {D}, not {kv.head_dim}")
+    _typed("lse", lse, ("float32",), (n, heads), dev)
+    _enqueue(dev, lib().oes_attn_weigh, kv._ref, *qp, lse.data_ptr(), heads, n, _q_start(kv, q_start), scale, window,
+             *_acc(kv, acc), stream=stream)
+
+
+def kv_evict_workspace_bytes(kv, budget):
+    b = _I64()
+    _check(lib().oes_kv_evict_workspace(kv._ref, budget, ctypes.byref(b)))
+    return b.value
+
+
+def kv_evict(kv, acc, budget, kept, new_len, workspace, first=0, last=0, stream=None):
+    """Cut every head's entries to `budget`: the first, the last and the heaviest stay, closed up (oes_kv_evict)."""
+    dev = kv.device
+    _typed("kept", kept, ("int32",), (kv.batch, kv.kv_heads, budget), dev)
+    _typed("new_len", new_len, ("int32",), (kv.batch,), dev)
+    if workspace.device != dev:
+        _bad("the workspace is on another device")
+    _enqueue(dev, lib().oes_kv_evict, kv._ref, *_acc(kv, acc), budget, first, last, kept.data_ptr(), new_len.data_ptr(),
+             workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream=stream)

@@ -12,8 +12,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 PKG = os.path.dirname(HERE)
 ROOT = os.path.dirname(PKG)
-SOURCES = ["api.hip", "k_lru.hip", "k_copy.hip", "k_route.hip", "k_ffn.hip", "k_prefill.hip", "cpu_moe.cpp",
-           "host_common.cpp"]
+SOURCES = ["api.hip", "k_lru.hip", "k_copy.hip", "k_route.hip", "k_ffn.hip", "k_prefill.hip", "api_layer.hip",
+           "k_linear.hip", "k_rope.hip", "k_attn.hip", "k_evict.hip", "cpu_moe.cpp", "host_common.cpp"]
 OUT = os.path.join(PKG, "liboes.so")
 BUILD = os.path.join(HERE, "_build")
 

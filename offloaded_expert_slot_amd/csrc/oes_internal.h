@@ -122,6 +122,63 @@ bool prefill_supported(int H, int I, int E);
 int64_t prefill_workspace_bytes(int H, int I, int n, int k, int E);
 hipError_t launch_prefill_ffn(const PrefillArgs &a, hipStream_t s);
 
+// ---------------------------------------------------------------- 4-bit linear
+struct LinearArgs {
+  int32_t format, N, K, n;
+  const uint8_t *w0, *w1, *w2;
+  const uint16_t *x;
+  int64_t x_stride;
+  uint16_t *y;
+  int64_t y_stride;
+};
+hipError_t launch_linear(const LinearArgs &a, hipStream_t s);
+
+// ---------------------------------------------------------------- rotary positions, paged cache
+// bf16 [n, heads, head_dim] rows: token t, head h at p + t * row + h * head
+struct Rows {
+  uint16_t *p;
+  int64_t row, head;
+};
+struct RopeArgs {
+  Rows x, y;               // q, or the one tensor of oes_rope
+  int32_t heads, n, head_dim, rot_dim, layout;
+  const double *freq;
+  float mscale;
+  const int32_t *pos;
+  int32_t append;          // 1: k and v go into the cache
+  Rows k, v;
+  oes_kv kv;
+  const int32_t *q_start;
+};
+hipError_t launch_rope(const RopeArgs &a, hipStream_t s);
+
+struct AttnArgs {
+  oes_kv kv;
+  Rows q, out;
+  float *lse;              // [n, q_heads]: written by attn (may be NULL), read by weigh
+  int32_t q_heads, n;
+  const int32_t *q_start;
+  float scale;
+  int32_t window;
+  float *ws;               // attn: partial sums of the splits
+  float *acc;              // weigh
+  int64_t acc_stride;
+};
+int64_t attn_workspace_bytes(const oes_kv &kv, int q_heads, int n);
+hipError_t launch_attn(const AttnArgs &a, hipStream_t s);
+hipError_t launch_attn_weigh(const AttnArgs &a, hipStream_t s);
+
+struct EvictArgs {
+  oes_kv kv;
+  float *acc;
+  int64_t acc_stride;
+  int32_t budget, first, last;
+  int32_t *kept, *new_len;
+  int32_t *ws;
+};
+int64_t evict_workspace_bytes(const oes_kv &kv, int budget);
+hipError_t launch_evict(const EvictArgs &a, hipStream_t s);
+
 // ---------------------------------------------------------------- probes
 hipError_t launch_stream_copy(uint8_t *dst, const uint8_t *src, int64_t bytes, int blocks,
                               hipStream_t s);
