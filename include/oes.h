@@ -520,8 +520,8 @@ oes_status oes_rope_append(const oes_kv *kv, const void *q, int64_t q_row, int64
  * rounded to bf16 once.
  *   q, out  bf16 [n, q_heads, head_dim] with row and head strides (elements,
  *           16-byte aligned rows); lse fp32 [n, q_heads] or NULL
- *   q_heads a multiple of kv_heads, q_heads / kv_heads <= 128; scale finite,
- *   positive; window >= 0 (0: none)
+ *   q_heads a multiple of kv_heads, q_heads / kv_heads <= 128; scale * k_scale
+ *   in [1e-30, 1e30]; window >= 0 (0: none)
  *   workspace: device, 16-byte aligned, >= oes_attn_workspace bytes for the
  *   same kv sizes, q_heads and n (the splits of a long cache are summed through
  *   it, in a fixed order).  Async. */

@@ -107,7 +107,8 @@ oes_status check_attn(const oes_kv *kv, int32_t q_heads, int32_t n, float scale,
   oes_status st = check_q_heads(kv, q_heads);
   if (st != OES_OK) return st;
   if (n < 0 || window < 0) return fail(OES_ERR_ARG, "n < 0 or window < 0");
-  if (!(scale > 0) || !isfinite(scale)) return fail(OES_ERR_ARG, "scale must be positive and finite");
+  const float s = scale * kv->k_scale;  // what the scores are multiplied with
+  if (!(scale > 0) || !(s >= 1e-30f) || !(s <= 1e30f)) return fail(OES_ERR_ARG, "scale (and scale * k_scale) must lie in [1e-30, 1e30]");
   return OES_OK;
 }
 

@@ -1,9 +1,40 @@
-// Attention of new tokens over a paged cache, and the weights that its entries receive.
+// Attention of new tokens over a paged cache.
 //
-//   attn   one wave per (row, head): 64 entries at a time, each lane the score of one
-//          entry, then each lane sums four of the output's values over the 64 weights
-//          (running maximum and sum, one pass over the cache);
-//   weigh  one thread per entry, over all rows and heads that see it.
+// One pass over the cache with the running maximum and sum of the softmax.  A workgroup
+// takes a tile of rows - (token, query head) pairs of one sequence and one cache head, so
+// that every key and value read serves all query heads of its group - and goes over the
+// entries that any of them sees.  Both products run on the matrix units, transposed:
+//
+//   S^T = K Q^T   (entries x rows)   A = keys from LDS, B = queries in registers
+//   O^T = V^T P^T (dims x rows)      A = values from LDS, read transposed, B = weights
+//
+// In the accumulator of v_mfma_f32_32x32x16_bf16 a lane holds one column, so one row of
+// the attention: its statistics are lane scalars, and the weights are in the lane that
+// needs them as the next product's B operand, with no trip through LDS.  (Accumulator
+// register i of lane (c, h) is entry 8 (i / 4) + 4 h + i % 4; the sum over entries may
+// run in any order, so the V operand is read in that order.)
+//
+// Two shapes:
+//   TILE    128 rows, 32 to each of 4 waves, which share tiles of 64 entries;
+//   SPLIT   up to 32 rows (decode steps, small chunks), the same for all waves, each of
+//           which goes over entries of its own, 32 at a time, with no barrier; the waves'
+//           sums are joined through LDS.
+// Either is split over the entries where there are too few tiles to fill the GPU; the
+// parts' sums go through the workspace and attn_merge_kernel joins them in order.
+//
+// Rows of LDS tiles are DP values (head_dim padded to 64, 128 or 256) in 16-byte chunks,
+// chunk c of row r at c ^ swizzle(r), so that neither the 16-byte key reads (16 rows, one
+// chunk) nor the transposing value reads (4 rows, 4 chunks) meet in a bank.  A bf16 cache
+// goes to LDS with direct loads (each lane's global address carries page and swizzle);
+// e4m3 goes through registers, where it becomes bf16 (exactly).  Entries that no row
+// sees, bad pages and values behind head_dim are staged from a zero chunk.
+//
+// Weights are rounded to bf16 (the matrix product's type) with the row sum taken before
+// the rounding; half a bf16 step per weight averages out over a row's entries and stays
+// below the rounding of the output.
+
+#include <algorithm>
+#include <type_traits>
 
 #include "layer_device.h"
 #include "oes_internal.h"
@@ -12,29 +43,551 @@ namespace oes {
 
 namespace {
 
-// Sequence that row t belongs to (wave-wide), or -1.
-__device__ inline int find_seq(const AttnArgs &a, int t, int *first, int *rows) {
-  const int lane = threadIdx.x & 63;
-  for (int b0 = 0; b0 < a.kv.batch; b0 += 64) {
-    const int b = b0 + lane;
-    bool bad = false, hit = false;
-    int f = 0, r = 0;
-    if (b < a.kv.batch) {
-      r = kv_rows(a.q_start[b], a.q_start[b + 1], a.n, &f, &bad);
-      hit = t >= f && t < f + r;
-      if (bad) raise_status(a.kv);
-    }
-    const uint64_t m = __ballot(hit);
-    if (m) {
-      const int w = __ffsll((unsigned long long)m) - 1;
-      *first = __shfl(f, w, 64);
-      *rows = __shfl(r, w, 64);
-      return b0 + w;
-    }
-  }
-  return -1;
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kSlack = 8.f;   // a running maximum may be this much (log2) too small
+
+__device__ __attribute__((aligned(16))) const uint32_t zero_chunk[4] = {0, 0, 0, 0};
+
+template <int DP>
+__device__ inline int swizzle(int row) {
+  // DP = 64: two rows share the 256 bytes of all banks
+  return DP == 64 ? ((row >> 1) & 1) << 2 | ((row >> 2) & 3) : (row & 3) << 2 | ((row >> 2) & 3);
 }
 
+// 16 bytes per lane from global memory to LDS base + 16 * lane; counted by vmcnt only
+__device__ inline void load_to_lds(const void *src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");
+}
+template <int N>
+__device__ inline void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ inline uint32_t lds_addr(const void *p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
+}
+// the value of the lane's other half (lane ^ 32) joined with its own
+__device__ inline float max_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ inline float sum_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+template <bool HI>
+__device__ inline uint32_t fp8_bf16_pair(uint32_t w) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
+}
+
+// What a launch is cut into.
+struct Plan {
+  int tile_tokens;   // tokens of a tile
+  int tiles;         // tiles of all sequences, at most
+  int splits;        // parts of the entries, at most
+  int chunk;         // entries of a part
+};
+
+// A tile of rows and the entries that it sees.
+struct Tile {
+  int b, first, t0, tokens;    // sequence, its first row, the tile's first token and tokens
+  int len, rows;               // entries and rows of the sequence
+  int lo, hi;                  // entries that any row sees
+  int lo_last, hi_first;       // entries that every row sees
+  int base, parts;             // first entry of part 0; parts that hold entries (at least 1)
+  bool bad;
+};
+
+__device__ inline void tile_entries(const AttnArgs &a, const Plan &p, Tile &t) {
+  kv_seen(t.len, t.rows, t.t0, a.window, &t.lo, &t.hi_first);
+  kv_seen(t.len, t.rows, t.t0 + t.tokens - 1, a.window, &t.lo_last, &t.hi);
+  t.base = t.lo & ~31;
+  t.parts = t.hi > t.base ? (t.hi - t.base + p.chunk - 1) / p.chunk : 1;
+}
+
+// Tile `idx` in the order of the sequences (wave-wide; the same answer in every lane).
+__device__ inline bool find_tile(const AttnArgs &a, const Plan &p, int idx, Tile &t) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int b0 = 0; b0 < a.kv.batch; b0 += 64) {
+    const int b = b0 + lane;
+    int first = 0, rows = 0;
+    bool bad = false;
+    if (b < a.kv.batch) rows = kv_rows(a.q_start[b], a.q_start[b + 1], a.n, &first, &bad);
+    const int mine = (rows + p.tile_tokens - 1) / p.tile_tokens;
+    int upto = mine;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(upto, d, 64);
+      if (lane >= d) upto += v;
+    }
+    const uint64_t hit = __ballot(mine > 0 && before + upto > idx && before + upto - mine <= idx);
+    const bool any_bad = __any(bad);
+    if (hit) {
+      const int w = __builtin_ctzll(hit);
+      t.b = b0 + w;
+      t.first = __builtin_amdgcn_readfirstlane(__shfl(first, w, 64));
+      t.rows = __builtin_amdgcn_readfirstlane(__shfl(rows, w, 64));
+      const int at = __builtin_amdgcn_readfirstlane(__shfl(upto - mine, w, 64));
+      t.t0 = (idx - before - at) * p.tile_tokens;
+      t.tokens = min(p.tile_tokens, t.rows - t.t0);
+      t.bad = any_bad;
+      t.len = __builtin_amdgcn_readfirstlane(kv_len(a.kv, a.kv.len[t.b], &t.bad));
+      tile_entries(a, p, t);
+      if (t.bad && lane == 0) raise_status(a.kv);
+      return true;
+    }
+    if (any_bad && lane == 0) raise_status(a.kv);
+    before += __shfl(upto, 63, 64);
+  }
+  return false;
+}
+
+// Partial sums of a row: ws holds [splits][n][q_heads] pairs (maximum in log2, sum), then
+// [splits][n][q_heads][head_dim] values, fp32.
+__device__ inline float2 *part_stats(const AttnArgs &a, int split, int64_t row_head) {
+  return reinterpret_cast<float2 *>(a.ws) + (int64_t)split * a.n * a.q_heads + row_head;
+}
+__device__ inline float *part_sums(const AttnArgs &a, int splits, int split, int64_t row_head) {
+  const int64_t rows = (int64_t)a.n * a.q_heads;
+  return a.ws + 2 * splits * rows + ((int64_t)split * rows + row_head) * a.kv.head_dim;
+}
+
+template <int DP, bool FP8, bool TILE>
+struct Shape {
+  static constexpr int waves = TILE ? 4 : (DP == 256 ? 2 : 4);
+  static constexpr int entries = TILE ? 64 : 32;            // of an LDS tile
+  static constexpr int buffers = FP8 && !TILE ? 1 : 2;
+  static constexpr int copies = TILE ? 1 : waves;           // SPLIT: a tile per wave
+  static constexpr int tile_bytes = entries * DP * 2;       // K; V as much again
+  static constexpr int lds = copies * buffers * 2 * tile_bytes;
+  static constexpr int own = TILE ? entries / waves : entries;  // rows that a wave stages
+  // waves of a SIMD that registers and LDS are held to
+  static constexpr int resident = DP == 256 ? 1 : (TILE || FP8 || DP == 64 ? 2 : 1);
+};
+
+template <int DP, bool FP8, bool TILE>
+__global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8, TILE>::resident)) void attn_kernel(AttnArgs a, Plan plan) {
+  using S = Shape<DP, FP8, TILE>;
+  constexpr int KT = S::entries / 32, NB = S::buffers, KS = DP / 16, DT = DP / 32;
+  __shared__ __attribute__((aligned(16))) uint8_t sm[S::lds];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 31, half = lane >> 5;
+  const int D = a.kv.head_dim, G = a.q_heads / a.kv.kv_heads;
+
+  // heads are the fastest index: neighbouring workgroups, on different XCDs, take different heads,
+  // so that an XCD keeps to few of them
+  int id = blockIdx.x;
+  const int g = id % a.kv.kv_heads;
+  id /= a.kv.kv_heads;
+  const int split = id / plan.tiles, idx = plan.tiles - 1 - (id - split * plan.tiles);
+  Tile t;
+  if (!find_tile(a, plan, idx, t) || split >= t.parts) return;
+  const int from = t.base + split * plan.chunk, to = min(t.hi, from + plan.chunk);
+  const int32_t *table = a.kv.table + t.b * a.kv.table_stride;
+  const int shift = kv_shift(a.kv.page_size);
+
+  // this lane's row
+  const int r = (TILE ? wave * 32 : 0) + c;
+  const bool row_live = r < t.tokens * G;
+  const int tok = r / G, row_t = t.first + t.t0 + tok, row_h = g * G + (r - tok * G);
+  int lo = 0, hi = 0;
+  if (row_live) kv_seen(t.len, t.rows, t.t0 + tok, a.window, &lo, &hi);
+  bf16x8 q[KS];
+  {
+    const uint16_t *qp = a.q.p + row_t * a.q.row + row_h * a.q.head + 8 * half;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      u32x4 v = {0, 0, 0, 0};
+      if (row_live && ks * 16 < D) v = *reinterpret_cast<const u32x4 *>(qp + 16 * ks);
+      q[ks] = __builtin_bit_cast(bf16x8, v);
+    }
+  }
+  f32x16 o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+  float m = -INFINITY, l = 0.f;
+  const float cs = a.scale * a.kv.k_scale * kLog2e;
+
+  // ---- staging: lane `e` of a wave looks up the page of entry e of a tile
+  uint8_t *tiles = sm + (TILE ? 0 : wave * NB * 2 * S::tile_bytes);
+  const int step = TILE ? S::entries : S::entries * S::waves;
+  const int j_first = from + (TILE ? 0 : wave * S::entries);
+  const uint8_t *kb = static_cast<const uint8_t *>(a.kv.k) + a.kv.k_head * g * (FP8 ? 1 : 2);
+  const uint8_t *vb = static_cast<const uint8_t *>(a.kv.v) + a.kv.v_head * g * (FP8 ? 1 : 2);
+  auto lookup = [&](int j0, int *in_page) {
+    const int j = j0 + (S::entries == 32 ? c : lane);
+    int page = -1;
+    *in_page = 0;
+    if (j >= t.lo && j < to) {
+      page = kv_page(a.kv, table, shift, j, in_page);
+      if (page < 0) raise_status(a.kv);
+    }
+    return page;
+  };
+  // the k and v chunks of row `row` of the tile, chunk `ch` of 16 bytes; `bytes` of a head row
+  auto source = [&](int page, int in_page, int row, int ch, int bytes, const uint8_t **ks, const uint8_t **vs) {
+    const int pg = __shfl(page, row, 64), ip = __shfl(in_page, row, 64);
+    const bool live = pg >= 0 && ch * 16 < bytes;
+    constexpr int es = FP8 ? 1 : 2;
+    const uint8_t *z = reinterpret_cast<const uint8_t *>(zero_chunk);
+    *ks = live ? kb + kv_k_off(a.kv, pg, ip) * es + ch * 16 : z;
+    *vs = live ? vb + kv_v_off(a.kv, pg, ip) * es + ch * 16 : z;
+  };
+  constexpr int CPR = FP8 ? DP / 16 : DP / 8;   // chunks of a head row
+  constexpr int RPI = 64 / CPR;                 // rows that a wave's load covers
+  constexpr int LD = S::own / RPI;              // loads of a wave for k, and for v
+  u32x4 stage_k[FP8 ? LD : 1], stage_v[FP8 ? LD : 1];
+  auto issue = [&](int page, int in_page, int buf) {
+#pragma unroll
+    for (int i = 0; i < LD; ++i) {
+      const int row = (TILE ? wave * S::own : 0) + i * RPI + lane / CPR, phys = lane % CPR;
+      const uint8_t *ks, *vs;
+      if (FP8) {
+        source(page, in_page, row, phys, D, &ks, &vs);
+        stage_k[i] = *reinterpret_cast<const u32x4 *>(ks);
+        stage_v[i] = *reinterpret_cast<const u32x4 *>(vs);
+      } else {
+        source(page, in_page, row, phys ^ swizzle<DP>(row), 2 * D, &ks, &vs);
+        uint8_t *dst = tiles + buf * 2 * S::tile_bytes + ((TILE ? wave * S::own : 0) + i * RPI) * DP * 2;
+        load_to_lds(ks, __builtin_amdgcn_readfirstlane(lds_addr(dst)));
+        load_to_lds(vs, __builtin_amdgcn_readfirstlane(lds_addr(dst + S::tile_bytes)));
+      }
+    }
+  };
+  auto store = [&](int buf) {  // FP8: the staged registers to LDS as bf16
+    if (!FP8) return;
+#pragma unroll
+    for (int i = 0; i < LD; ++i) {
+      const int row = (TILE ? wave * S::own : 0) + i * RPI + lane / CPR, q2 = 2 * (lane % CPR);
+      uint8_t *dst = tiles + buf * 2 * S::tile_bytes + row * DP * 2;
+      const int c0 = (q2 ^ swizzle<DP>(row)) * 16, c1 = ((q2 + 1) ^ swizzle<DP>(row)) * 16;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const u32x4 w = kv ? stage_v[i] : stage_k[i];
+        const u32x4 w0 = {fp8_bf16_pair<false>(w.x), fp8_bf16_pair<true>(w.x), fp8_bf16_pair<false>(w.y), fp8_bf16_pair<true>(w.y)};
+        const u32x4 w1 = {fp8_bf16_pair<false>(w.z), fp8_bf16_pair<true>(w.z), fp8_bf16_pair<false>(w.w), fp8_bf16_pair<true>(w.w)};
+        *reinterpret_cast<u32x4 *>(dst + kv * S::tile_bytes + c0) = w0;
+        *reinterpret_cast<u32x4 *>(dst + kv * S::tile_bytes + c1) = w1;
+      }
+    }
+  };
+
+  // ---- one tile of entries
+  auto compute = [&](int j0, int buf, uint64_t paged) {
+    const uint8_t *kt_base = tiles + buf * 2 * S::tile_bytes, *vt_base = kt_base + S::tile_bytes;
+    f32x16 s[KT];
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
+      const int row = kt * 32 + c;
+      const uint8_t *kr = kt_base + row * DP * 2;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const bf16x8 kf = *reinterpret_cast<const bf16x8 *>(kr + ((2 * ks + half) ^ swizzle<DP>(row)) * 16);
+        s[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[ks], s[kt], 0, 0, 0);
+      }
+    }
+    // entries that some row of the tile does not see, or that have no page
+    const int j1 = min(j0 + S::entries, to);
+    const bool whole = j0 >= t.lo_last && j0 + S::entries <= min(t.hi_first, to) &&
+                       paged == (S::entries == 64 ? ~0ull : 0xffffffffull);
+    if (!whole) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int e = kt * 32 + 8 * (i / 4) + 4 * half + i % 4, j = j0 + e;
+          if (j < lo || j >= hi || j >= j1 || !((paged >> e) & 1)) s[kt][i] = -INFINITY;
+        }
+    }
+    float mx = s[0][0];
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[kt][i]);
+    mx = max_halves(mx) * cs;
+    if (__any(mx > m + kSlack)) {  // true for the first visible entries (m = -inf)
+      const float mn = fmaxf(m, mx);
+      const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] *= f;
+    }
+    const float mu = m == -INFINITY ? 0.f : m;
+    uint32_t p[KT][8];
+    float sum = 0.f;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const float p0 = __builtin_amdgcn_exp2f(fmaf(s[kt][i], cs, -mu)), p1 = __builtin_amdgcn_exp2f(fmaf(s[kt][i + 1], cs, -mu));
+        sum += p0;
+        sum += p1;
+        p[kt][i / 2] = f2bf16_pair(p0, p1);
+      }
+    l += sum;
+    // transposing reads: lane i of 16 points at row i / 4, 4 dims i % 4, and gets dim i of 4 rows
+    const int gq = lane >> 4, tr_row = 4 * (gq >> 1) + ((lane & 15) >> 2), tr_ch = 2 * (gq & 1) + ((lane & 3) >> 1),
+              tr_off = 8 * (lane & 1);
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    // Where the rows of the tile see different entries, a value that is not finite must not meet the
+    // zero weight of a row that does not see it (0 * inf): it is taken out of the product, and added
+    // entry by entry, to the rows that see it, behind it.
+    const bool mixed = !whole && t.tokens > 1;
+    uint32_t odd = 0;
+    auto values = [&](int row0, int d, auto clean) {
+      const int row = row0 + tr_row;
+      const uint8_t *v = vt_base + row * DP * 2 + ((d * 4 + tr_ch) ^ swizzle<DP>(row)) * 16 + tr_off;
+      u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)v));
+      if (clean) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t e = ((w[x] & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;  // exponents of all ones
+          odd |= e;
+          w[x] &= ~((e >> 15) * 0xffffu);
+        }
+      }
+      return w;
+    };
+    auto weigh_values = [&](auto clean) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2) {
+          const u32x4 pw = {p[kt][4 * k2], p[kt][4 * k2 + 1], p[kt][4 * k2 + 2], p[kt][4 * k2 + 3]};
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            const u32x2 v0 = values(kt * 32 + 16 * k2, d, clean), v1 = values(kt * 32 + 16 * k2 + 8, d, clean);
+            const u32x4 vw = {v0.x, v0.y, v1.x, v1.y};
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vw), __builtin_bit_cast(bf16x8, pw), o[d], 0, 0, 0);
+          }
+        }
+    };
+    if (!mixed) {
+      weigh_values(std::false_type{});
+      return;
+    }
+    weigh_values(std::true_type{});
+    if (__any(odd != 0)) {
+#pragma unroll 1
+      for (int e = 0; e < S::entries; ++e) {
+        const int j = j0 + e, i = (e & 32) / 2 + 4 * ((e & 31) / 8) + e % 4;  // register 16 kt + i of half (e / 4) % 2
+        uint32_t word = 0;
+#pragma unroll
+        for (int x = 0; x < KT * 8; ++x)
+          if (x == i / 2) word = p[x / 8][x % 8];
+        const float w = __shfl((i & 1) ? bf16_hi(word) : bf16_lo(word), c + 32 * ((e >> 2) & 1), 64);
+        const bool sees = j >= lo && j < hi && j < j1 && ((paged >> e) & 1);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int dim = d * 32 + 8 * (k / 4) + 4 * half + k % 4;
+            const uint32_t v = *reinterpret_cast<const uint16_t *>(vt_base + e * DP * 2 + ((dim >> 3) ^ swizzle<DP>(e)) * 16 + (dim & 7) * 2);
+            if (sees && (v & 0x7f80u) == 0x7f80u) o[d][k] = fmaf(w, bf16f(v), o[d][k]);
+          }
+      }
+    }
+  };
+
+  // ---- the loop: loads of the next tile run under the products of this one
+  if (j_first < to) {
+    int ip, ip_next = 0, buf = 0;
+    int page = lookup(j_first, &ip);
+    issue(page, ip, 0);
+    int page_next = lookup(j_first + step, &ip_next);
+    uint64_t paged = __ballot(page >= 0);
+    if (FP8 && !TILE) store(0);
+    for (int j0 = j_first; j0 < to; j0 += step) {
+      const bool more = j0 + step < to;
+      const uint64_t paged_next = __ballot(page_next >= 0);
+      int page_after = -1, ip_after = 0;
+      if (more) page_after = lookup(j0 + 2 * step, &ip_after);
+      if (TILE) {
+        if (FP8)
+          store(buf);
+        else
+          wait_loads<0>();
+        __syncthreads();
+        if (more) issue(page_next, ip_next, buf ^ 1);
+      } else if (FP8) {
+        if (more) issue(page_next, ip_next, 0);
+      } else if (more) {
+        issue(page_next, ip_next, buf ^ 1);
+        wait_loads<2 * LD>();
+      } else {
+        wait_loads<0>();
+      }
+      compute(j0, NB == 2 ? buf : 0, S::entries == 64 ? paged : paged & 0xffffffffull);
+      if (!TILE && FP8 && more) store(0);
+      buf ^= 1;
+      page_next = page_after;
+      ip_next = ip_after;
+      paged = paged_next;
+    }
+  }
+
+  // ---- results
+  l = sum_halves(l);
+  const bool direct = t.parts == 1;
+  if (TILE) {
+    if (!row_live) return;
+    const int64_t rh = (int64_t)row_t * a.q_heads + row_h;
+    if (direct) {
+      const float inv = l == 0.f ? 0.f : a.kv.v_scale / l;
+      uint16_t *op = a.out.p + row_t * a.out.row + row_h * a.out.head + 4 * half;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          if (d * 32 + 2 * i < D) {
+            const u32x2 w = {f2bf16_pair(o[d][i] * inv, o[d][i + 1] * inv), f2bf16_pair(o[d][i + 2] * inv, o[d][i + 3] * inv)};
+            *reinterpret_cast<u32x2 *>(op + d * 32 + 2 * i) = w;
+          }
+      if (a.lse && half == 0) a.lse[rh] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    } else {
+      float *op = part_sums(a, plan.splits, split, rh) + 4 * half;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          if (d * 32 + 2 * i < D) {
+            typedef float f32x4 __attribute__((ext_vector_type(4)));
+            const f32x4 w = {o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
+            *reinterpret_cast<f32x4 *>(op + d * 32 + 2 * i) = w;
+          }
+      if (half == 0) *part_stats(a, split, rh) = make_float2(m, l);
+    }
+    return;
+  }
+  // SPLIT: join the waves
+  __syncthreads();  // every wave is done with its tiles
+  float *jo = reinterpret_cast<float *>(sm);                 // [waves][32][DP]
+  constexpr int JS = 32 * DP;
+  __shared__ float jm[4][32], jl[4][32];
+  {
+    float *mine = jo + wave * JS + c * DP + 4 * half;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        typedef float f32x4 __attribute__((ext_vector_type(4)));
+        const f32x4 w = {o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
+        *reinterpret_cast<f32x4 *>(mine + d * 32 + 2 * i) = w;
+      }
+    if (half == 0) {
+      jm[wave][c] = m;
+      jl[wave][c] = l;
+    }
+  }
+  __syncthreads();
+  for (int it = threadIdx.x; it < t.tokens * G * (D / 4); it += S::waves * 64) {
+    const int jr = it / (D / 4), d4 = (it - jr * (D / 4)) * 4;
+    const int jt = jr / G, rt = t.first + t.t0 + jt, rh_ = g * G + (jr - jt * G);
+    float mm = jm[0][jr];
+#pragma unroll
+    for (int w = 1; w < S::waves; ++w) mm = fmaxf(mm, jm[w][jr]);
+    float ll = 0.f, s4[4] = {0.f, 0.f, 0.f, 0.f};
+    if (mm != -INFINITY) {
+#pragma unroll
+      for (int w = 0; w < S::waves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(jm[w][jr] - mm);
+        ll = fmaf(jl[w][jr], f, ll);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s4[x] = fmaf(jo[w * JS + jr * DP + d4 + x], f, s4[x]);
+      }
+    }
+    const int64_t rh = (int64_t)rt * a.q_heads + rh_;
+    if (direct) {
+      const float inv = ll == 0.f ? 0.f : a.kv.v_scale / ll;
+      const u32x2 w = {f2bf16_pair(s4[0] * inv, s4[1] * inv), f2bf16_pair(s4[2] * inv, s4[3] * inv)};
+      *reinterpret_cast<u32x2 *>(a.out.p + rt * a.out.row + rh_ * a.out.head + d4) = w;
+      if (a.lse && d4 == 0) a.lse[rh] = ll == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * kLn2;
+    } else {
+      typedef float f32x4 __attribute__((ext_vector_type(4)));
+      const f32x4 w = {s4[0], s4[1], s4[2], s4[3]};
+      *reinterpret_cast<f32x4 *>(part_sums(a, plan.splits, split, rh) + d4) = w;
+      if (d4 == 0) *part_stats(a, split, rh) = make_float2(mm, ll);
+    }
+  }
+}
+
+// Joins the parts of a row, in their order.  One workgroup of 4 waves per (row, head): wave w
+// adds parts w, w + 4, ...; lane i holds dims 4 i .. 4 i + 3.
+__global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a, Plan plan) {
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  __shared__ f32x4 so[4][64];
+  __shared__ float sl[4];
+  const int row = blockIdx.x / a.q_heads, h = blockIdx.x - row * a.q_heads, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // the sequence of this row, then its tile
+  Tile t;
+  t.b = -1;
+  for (int b0 = 0; b0 < a.kv.batch; b0 += 64) {
+    const int b = b0 + lane;
+    int first = 0, rows = 0;
+    bool bad = false;
+    if (b < a.kv.batch) rows = kv_rows(a.q_start[b], a.q_start[b + 1], a.n, &first, &bad);
+    const uint64_t hit = __ballot(row >= first && row < first + rows);
+    if (hit) {
+      const int w = __builtin_ctzll(hit);
+      t.b = b0 + w;
+      t.first = __shfl(first, w, 64);
+      t.rows = __shfl(rows, w, 64);
+      break;
+    }
+  }
+  if (t.b < 0) return;
+  t.len = kv_len(a.kv, a.kv.len[t.b], &t.bad);
+  t.t0 = (row - t.first) / plan.tile_tokens * plan.tile_tokens;
+  t.tokens = min(plan.tile_tokens, t.rows - t.t0);
+  tile_entries(a, plan, t);
+  if (t.parts == 1) return;  // written by its workgroup
+  const int64_t rh = (int64_t)row * a.q_heads + h;
+  float mm = -INFINITY;
+  for (int s = lane; s < t.parts; s += 64) mm = fmaxf(mm, part_stats(a, s, rh)->x);
+  for (int d = 32; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor(mm, d, 64));
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  float ll = 0.f;
+  const bool live = 4 * lane < a.kv.head_dim;
+  if (mm != -INFINITY) {
+#pragma unroll 4
+    for (int s = wave; s < t.parts; s += 4) {
+      const float2 st = *part_stats(a, s, rh);
+      const float f = __builtin_amdgcn_exp2f(st.x - mm);
+      ll = fmaf(st.y, f, ll);
+      if (live) {
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(part_sums(a, plan.splits, s, rh) + 4 * lane);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) sum[x] = fmaf(v[x], f, sum[x]);
+      }
+    }
+  }
+  so[wave][lane] = sum;
+  if (lane == 0) sl[wave] = ll;
+  __syncthreads();
+  if (wave) return;
+  ll = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+  const float inv = ll == 0.f ? 0.f : a.kv.v_scale / ll;
+  if (live) {
+    f32x4 v;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v[x] = ((so[0][lane][x] + so[1][lane][x]) + (so[2][lane][x] + so[3][lane][x])) * inv;
+    const u32x2 w = {f2bf16_pair(v[0], v[1]), f2bf16_pair(v[2], v[3])};
+    *reinterpret_cast<u32x2 *>(a.out.p + row * a.out.row + h * a.out.head + 4 * lane) = w;
+  }
+  if (a.lse && lane == 0) a.lse[rh] = ll == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * kLn2;
+}
+
+// ------------------------------------------------------------------ weigh
 template <bool FP8>
 __device__ inline float cache_at(const void *base, int64_t off) {
   if (FP8) return e4m3_pair<false>((uint32_t) static_cast<const uint8_t *>(base)[off]).x;
@@ -47,57 +600,6 @@ __device__ inline float dot_key(const AttnArgs &a, const uint16_t *q, int page, 
   float s = 0.f;
   for (int d = 0; d < a.kv.head_dim; ++d) s = fmaf(bf16f(q[d]), cache_at<FP8>(a.kv.k, off + d), s);
   return s * a.kv.k_scale * a.scale;
-}
-
-template <bool FP8>
-__global__ __launch_bounds__(64) void attn_kernel(AttnArgs a) {
-  const int t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x, D = a.kv.head_dim;
-  int first = 0, rows = 0;
-  const int b = find_seq(a, t, &first, &rows);
-  if (b < 0) return;
-  bool bad = false;
-  const int len = kv_len(a.kv, a.kv.len[b], &bad);
-  if (bad) raise_status(a.kv);
-  const int g = h / (a.q_heads / a.kv.kv_heads), shift = kv_shift(a.kv.page_size);
-  const int32_t *table = a.kv.table + b * a.kv.table_stride;
-  const uint16_t *q = a.q.p + t * a.q.row + h * a.q.head;
-  int lo, hi;
-  kv_seen(len, rows, t - first, a.window, &lo, &hi);
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int j0 = lo; j0 < hi; j0 += 64) {
-    const int j = j0 + lane;
-    int page = -1, in_page = 0;
-    float s = -INFINITY;
-    if (j < hi) {
-      page = kv_page(a.kv, table, shift, j, &in_page);
-      if (page >= 0)
-        s = dot_key<FP8>(a, q, page, in_page, g);
-      else
-        raise_status(a.kv);
-    }
-    float mx = s;
-    for (int d = 32; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d, 64));
-    const float mn = fmaxf(m, mx);
-    if (mn == -INFINITY) continue;
-    const float p = page >= 0 ? expf(s - mn) : 0.f, f = expf(m - mn);
-    m = mn;
-    float ps = p;
-    for (int d = 32; d > 0; d >>= 1) ps += __shfl_xor(ps, d, 64);
-    l = l * f + ps;
-    for (int c = 0; c < 4; ++c) o[c] *= f;
-    for (int w = 0; w < 64 && j0 + w < hi; ++w) {
-      const int pg = __shfl(page, w, 64), ip = __shfl(in_page, w, 64);
-      const float pw = __shfl(p, w, 64);
-      if (pg < 0) continue;
-      const int64_t off = kv_v_off(a.kv, pg, ip) + a.kv.v_head * g;
-      for (int c = 0; c < 4; ++c)
-        if (lane + 64 * c < D) o[c] = fmaf(pw, cache_at<FP8>(a.kv.v, off + lane + 64 * c), o[c]);
-    }
-  }
-  uint16_t *out = a.out.p + t * a.out.row + h * a.out.head;
-  for (int c = 0; c < 4; ++c)
-    if (lane + 64 * c < D) out[lane + 64 * c] = (uint16_t)f2bf16(l > 0.f ? o[c] * a.kv.v_scale / l : l == 0.f ? 0.f : l);
-  if (a.lse && lane == 0) a.lse[(int64_t)t * a.q_heads + h] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
 template <bool FP8>
@@ -131,16 +633,69 @@ __global__ __launch_bounds__(256) void weigh_kernel(AttnArgs a) {
   a.acc[((int64_t)b * a.kv.kv_heads + g) * a.acc_stride + j] += sum;
 }
 
+bool split_shape(const oes_kv &kv, int q_heads, int n) {
+  // SPLIT holds 32 rows; beyond, on average per sequence and cache head, TILE's 128 fill up better
+  const int G = q_heads / kv.kv_heads;
+  return G <= 32 && (int64_t)n * G <= 32ll * kv.batch;
+}
+
+Plan make_plan(const oes_kv &kv, int q_heads, int n) {
+  const int G = q_heads / kv.kv_heads;
+  const bool split = split_shape(kv, q_heads, n);
+  Plan p;
+  p.tile_tokens = (split ? 32 : 128) / G;
+  // every sequence with rows has at most one tile that is not full
+  const int64_t tiles = std::min<int64_t>(n, ((int64_t)n + (int64_t)kv.batch * (p.tile_tokens - 1)) / p.tile_tokens);
+  p.tiles = (int)tiles;
+  const int64_t cap = ((int64_t)kv.max_pages * kv.page_size + 31) / 32 * 32 + 32;
+  const int64_t units = tiles * kv.kv_heads;
+  int64_t chunk;
+  if (split) {
+    chunk = std::max<int64_t>(128, (cap * units / 4096 + 127) / 128 * 128);
+  } else {
+    const int64_t parts = std::max<int64_t>(1, 512 / units);
+    chunk = std::max<int64_t>(256, ((cap + parts - 1) / parts + 63) / 64 * 64);
+  }
+  p.splits = (int)((cap + chunk - 1) / chunk);
+  if (p.splits == 1) chunk = cap;
+  p.chunk = (int)std::min<int64_t>(chunk, 1 << 30);
+  return p;
+}
+
+template <int DP, bool FP8, bool TILE>
+hipError_t launch_shape(const AttnArgs &a, const Plan &p, uint32_t blocks, hipStream_t s) {
+  hipLaunchKernelGGL((attn_kernel<DP, FP8, TILE>), dim3(blocks), dim3(Shape<DP, FP8, TILE>::waves * 64), 0, s, a, p);
+  return hipGetLastError();
+}
+
 }  // namespace
 
-int64_t attn_workspace_bytes(const oes_kv &, int, int) { return 0; }
+int64_t attn_workspace_bytes(const oes_kv &kv, int q_heads, int n) {
+  const Plan p = make_plan(kv, q_heads, n);
+  return p.splits == 1 ? 0 : (int64_t)p.splits * n * q_heads * (kv.head_dim + 2) * 4;
+}
 
 hipError_t launch_attn(const AttnArgs &a, hipStream_t s) {
-  const dim3 g(a.n, a.q_heads), b(64);
-  if (a.kv.elem == OES_ELEM_E4M3)
-    hipLaunchKernelGGL(attn_kernel<true>, g, b, 0, s, a);
+  const Plan p = make_plan(a.kv, a.q_heads, a.n);
+  const bool split = split_shape(a.kv, a.q_heads, a.n), fp8 = a.kv.elem == OES_ELEM_E4M3;
+  const int64_t blocks = (int64_t)p.tiles * a.kv.kv_heads * p.splits;
+  if (blocks > 0x7fffffff || (int64_t)a.n * a.q_heads > 0x7fffffff) return hipErrorInvalidConfiguration;
+  const int dp = a.kv.head_dim <= 64 ? 64 : (a.kv.head_dim <= 128 ? 128 : 256);
+  hipError_t e = hipSuccess;
+#define OES_ATTN(DPV)                                                                                             \
+  e = split ? (fp8 ? launch_shape<DPV, true, false>(a, p, (uint32_t)blocks, s)                                    \
+                   : launch_shape<DPV, false, false>(a, p, (uint32_t)blocks, s))                                  \
+            : (fp8 ? launch_shape<DPV, true, true>(a, p, (uint32_t)blocks, s)                                     \
+                   : launch_shape<DPV, false, true>(a, p, (uint32_t)blocks, s))
+  if (dp == 64)
+    OES_ATTN(64);
+  else if (dp == 128)
+    OES_ATTN(128);
   else
-    hipLaunchKernelGGL(attn_kernel<false>, g, b, 0, s, a);
+    OES_ATTN(256);
+#undef OES_ATTN
+  if (e != hipSuccess || p.splits == 1) return e;
+  hipLaunchKernelGGL(attn_merge_kernel, dim3((uint32_t)(a.n * a.q_heads)), dim3(256), 0, s, a, p);
   return hipGetLastError();
 }
 
