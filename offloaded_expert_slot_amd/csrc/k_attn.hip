@@ -1,4 +1,4 @@
-// Attention of new tokens over a paged cache.
+// Attention of new tokens over a paged cache, and the weights that its entries receive.
 //
 // One pass over the cache with the running maximum and sum of the softmax.  A workgroup
 // takes a tile of rows - (token, query head) pairs of one sequence and one cache head, so
@@ -588,49 +588,156 @@ __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a, Plan plan) 
 }
 
 // ------------------------------------------------------------------ weigh
-template <bool FP8>
-__device__ inline float cache_at(const void *base, int64_t off) {
-  if (FP8) return e4m3_pair<false>((uint32_t) static_cast<const uint8_t *>(base)[off]).x;
-  return bf16f(static_cast<const uint16_t *>(base)[off]);
-}
+// The weights that entries receive: S^T = K Q^T once more, with the row's log-sum-exp known.
+// A wave keeps its 32 KT entries' keys in registers (A operand) and goes over the rows that
+// see any entry of the workgroup, 32 at a time, from LDS; a lane adds up the weights of its
+// row (column) for 16 KT entries, and the 32 rows' sums are joined through LDS at the end.
+// No two workgroups share an entry, so nothing is added atomically.  Bound by the
+// exponentials (one for each entry, row pair; 16 cycles per 64) rather than by the product.
+template <int DP>
+struct WeighShape {
+  static constexpr int kt = DP == 256 ? 1 : 2;
+  static constexpr int entries = 4 * 32 * kt;
+  static constexpr int tile_bytes = 32 * DP * 2;
+};
 
-template <bool FP8>
-__device__ inline float dot_key(const AttnArgs &a, const uint16_t *q, int page, int in_page, int g) {
-  const int64_t off = kv_k_off(a.kv, page, in_page) + a.kv.k_head * g;
-  float s = 0.f;
-  for (int d = 0; d < a.kv.head_dim; ++d) s = fmaf(bf16f(q[d]), cache_at<FP8>(a.kv.k, off + d), s);
-  return s * a.kv.k_scale * a.scale;
-}
-
-template <bool FP8>
-__global__ __launch_bounds__(256) void weigh_kernel(AttnArgs a) {
-  const int b = blockIdx.z, g = blockIdx.y, j = blockIdx.x * 256 + threadIdx.x;
-  const int G = a.q_heads / a.kv.kv_heads;
+template <int DP, bool FP8>
+__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void weigh_kernel(AttnArgs a, int blocks_per_seq) {
+  using S = WeighShape<DP>;
+  constexpr int KT = S::kt, KS = DP / 16, CPR = DP / 8, RPI = 64 / CPR, LD = 8 / RPI;
+  __shared__ __attribute__((aligned(16))) uint8_t sm[2 * S::tile_bytes > 4 * 32 * 33 * 4 ? 2 * S::tile_bytes : 4 * 32 * 33 * 4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 31, half = lane >> 5;
+  const int D = a.kv.head_dim, G = a.q_heads / a.kv.kv_heads;
+  int id = blockIdx.x;
+  const int g = id % a.kv.kv_heads;
+  id /= a.kv.kv_heads;
+  const int b = id / blocks_per_seq, e0 = (id - b * blocks_per_seq) * S::entries;
   bool bad = false;
   const int len = kv_len(a.kv, a.kv.len[b], &bad);
   int first;
   const int rows = kv_rows(a.q_start[b], a.q_start[b + 1], a.n, &first, &bad);
   if (bad) raise_status(a.kv);
-  if (j >= len || rows == 0) return;
-  int in_page;
-  const int page = kv_page(a.kv, a.kv.table + b * a.kv.table_stride, kv_shift(a.kv.page_size), j, &in_page);
-  if (page < 0) {
-    raise_status(a.kv);
-    return;
-  }
-  float sum = 0.f;
-  for (int i = 0; i < rows; ++i) {
-    int lo, hi;
-    kv_seen(len, rows, i, a.window, &lo, &hi);
-    if (j < lo || j >= hi) continue;
-    for (int c = 0; c < G; ++c) {
-      const int h = g * G + c;
-      const float lse = a.lse[(int64_t)(first + i) * a.q_heads + h];
-      if (lse == -INFINITY) continue;
-      sum += expf(dot_key<FP8>(a, a.q.p + (first + i) * a.q.row + h * a.q.head, page, in_page, g) - lse);
+  if (e0 >= len || rows == 0) return;
+  // tokens that see an entry of the workgroup: at >= e0, and at < last entry + window
+  const int before = len - rows, e1 = min(e0 + S::entries, len);
+  const int i0 = max(0, e0 - before);
+  const int i1 = a.window > 0 ? (int)min((int64_t)rows, (int64_t)e1 - 1 + a.window - before) : rows;
+  if (i0 >= i1) return;
+  const int r0 = i0 * G, r1 = i1 * G;
+
+  // keys of this wave
+  const int shift = kv_shift(a.kv.page_size);
+  const int32_t *table = a.kv.table + b * a.kv.table_stride;
+  const int ew = e0 + wave * 32 * KT;
+  bf16x8 key[KT][KS];
+  uint64_t paged = 0;
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) {
+    const int j = ew + 32 * kt + c;
+    int ip = 0, page = -1;
+    if (j < len) {
+      page = kv_page(a.kv, table, shift, j, &ip);
+      if (page < 0) raise_status(a.kv);
+    }
+    paged |= (__ballot(page >= 0) & 0xffffffffull) << (32 * kt);
+    const int64_t off = kv_k_off(a.kv, max(page, 0), ip) + a.kv.k_head * g + 8 * half;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      u32x4 w = {0, 0, 0, 0};
+      if (page >= 0 && ks * 16 < D) {
+        if (FP8) {
+          const u32x2 v = *reinterpret_cast<const u32x2 *>(static_cast<const uint8_t *>(a.kv.k) + off + 16 * ks);
+          w = u32x4{fp8_bf16_pair<false>(v.x), fp8_bf16_pair<true>(v.x), fp8_bf16_pair<false>(v.y), fp8_bf16_pair<true>(v.y)};
+        } else {
+          w = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.kv.k) + off + 16 * ks);
+        }
+      }
+      key[kt][ks] = __builtin_bit_cast(bf16x8, w);
     }
   }
-  a.acc[((int64_t)b * a.kv.kv_heads + g) * a.acc_stride + j] += sum;
+  float acc[KT][16];
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[kt][i] = 0.f;
+  const float cs = a.scale * a.kv.k_scale * kLog2e;
+
+  // 32 rows to LDS: wave w stages rows 8 w .. 8 w + 7
+  auto issue = [&](int r, int buf) {
+#pragma unroll
+    for (int i = 0; i < LD; ++i) {
+      const int row = 8 * wave + i * RPI + lane / CPR, ch = (lane % CPR) ^ swizzle<DP>(row), rr = r + row;
+      const int tok = rr / G;
+      const uint16_t *src = reinterpret_cast<const uint16_t *>(zero_chunk);
+      if (rr < r1 && ch * 8 < D) src = a.q.p + (int64_t)(first + tok) * a.q.row + (g * G + rr - tok * G) * a.q.head + ch * 8;
+      load_to_lds(src, __builtin_amdgcn_readfirstlane(lds_addr(sm + buf * S::tile_bytes + (8 * wave + i * RPI) * DP * 2)));
+    }
+  };
+  auto row_lse = [&](int r) {
+    const int rr = r + c, tok = rr / G;
+    return rr < r1 ? a.lse[(int64_t)(first + tok) * a.q_heads + g * G + rr - tok * G] : -INFINITY;
+  };
+  issue(r0, 0);
+  float lse = row_lse(r0);
+  int buf = 0;
+  for (int r = r0; r < r1; r += 32) {
+    wait_loads<0>();
+    __syncthreads();
+    const bool more = r + 32 < r1;
+    const float lse2 = lse * kLog2e;
+    if (more) {
+      lse = row_lse(r + 32);
+      issue(r + 32, buf ^ 1);
+    }
+    f32x16 s[KT];
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
+    const uint8_t *qr = sm + buf * S::tile_bytes + c * DP * 2;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const bf16x8 qf = *reinterpret_cast<const bf16x8 *>(qr + ((2 * ks + half) ^ swizzle<DP>(c)) * 16);
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) s[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key[kt][ks], qf, s[kt], 0, 0, 0);
+    }
+    // every row of this tile sees every entry of the wave, and all entries have pages: no masks
+    const int at0 = before + r / G, at1 = before + min(r + 31, r1 - 1) / G;
+    const bool whole = r + 32 <= r1 && at0 >= ew + 32 * KT - 1 && (a.window == 0 || (int64_t)at1 - a.window < ew) &&
+                       paged == (KT == 2 ? ~0ull : 0xffffffffull) && !__any(lse2 == -INFINITY);
+    if (whole) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[kt][i] += __builtin_amdgcn_exp2f(fmaf(s[kt][i], cs, -lse2));
+    } else {
+      int lo = 0, hi = 0;
+      if (r + c < r1 && lse2 != -INFINITY) kv_seen(len, rows, (r + c) / G, a.window, &lo, &hi);
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int e = kt * 32 + 8 * (i / 4) + 4 * half + i % 4, j = ew + e;
+          if (j >= lo && j < hi && ((paged >> e) & 1)) acc[kt][i] += __builtin_amdgcn_exp2f(fmaf(s[kt][i], cs, -lse2));
+        }
+    }
+    buf ^= 1;
+  }
+  // join the rows: 32 entries x 32 rows (padded) of every wave at a time
+  float *join = reinterpret_cast<float *>(sm) + wave * 32 * 33;
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) join[(8 * (i / 4) + 4 * half + i % 4) * 33 + c] = acc[kt][i];
+    __syncthreads();
+    float sum = 0.f;   // lane (c, half): entry c, rows 16 half .. + 15
+#pragma unroll
+    for (int x = 0; x < 16; ++x) sum += join[c * 33 + 16 * half + x];
+    sum = sum_halves(sum);
+    const int j = ew + 32 * kt + c;
+    if (half == 0 && j < len && ((paged >> (32 * kt + c)) & 1)) a.acc[((int64_t)b * a.kv.kv_heads + g) * a.acc_stride + j] += sum;
+  }
 }
 
 bool split_shape(const oes_kv &kv, int q_heads, int n) {
@@ -699,15 +806,24 @@ hipError_t launch_attn(const AttnArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_attn_weigh(const AttnArgs &a, hipStream_t s) {
-  const int64_t cap = (int64_t)a.kv.max_pages * a.kv.page_size;
-  if (a.kv.batch > 65535) return hipErrorInvalidConfiguration;
-  const dim3 g((uint32_t)((cap + 255) / 256), a.kv.kv_heads, a.kv.batch), b(256);
+namespace {
+template <int DP>
+hipError_t launch_weigh(const AttnArgs &a, hipStream_t s) {
+  const int64_t cap = (int64_t)a.kv.max_pages * a.kv.page_size, per = (cap + WeighShape<DP>::entries - 1) / WeighShape<DP>::entries;
+  const int64_t blocks = per * a.kv.kv_heads * a.kv.batch;
+  if (blocks > 0x7fffffff || (int64_t)a.n * a.q_heads > 0x7fffffff) return hipErrorInvalidConfiguration;
   if (a.kv.elem == OES_ELEM_E4M3)
-    hipLaunchKernelGGL(weigh_kernel<true>, g, b, 0, s, a);
+    hipLaunchKernelGGL((weigh_kernel<DP, true>), dim3((uint32_t)blocks), dim3(256), 0, s, a, (int)per);
   else
-    hipLaunchKernelGGL(weigh_kernel<false>, g, b, 0, s, a);
+    hipLaunchKernelGGL((weigh_kernel<DP, false>), dim3((uint32_t)blocks), dim3(256), 0, s, a, (int)per);
   return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_attn_weigh(const AttnArgs &a, hipStream_t s) {
+  if (a.kv.head_dim <= 64) return launch_weigh<64>(a, s);
+  if (a.kv.head_dim <= 128) return launch_weigh<128>(a, s);
+  return launch_weigh<256>(a, s);
 }
 
 }  // namespace oes
