@@ -550,36 +550,52 @@ def _bad(message):
     raise OesError(ERR_ARG, f"OES_ERR_ARG: {message}")
 
 
-def _elem(t):
-    """Cache element of a tensor's type: bf16 (or its bits as 16-bit integers), e4m3 (or its bytes)."""
-    import torch
-    kinds = {torch.bfloat16: ELEM_BF16, torch.int16: ELEM_BF16, torch.float8_e4m3fn: ELEM_E4M3,
-             torch.uint8: ELEM_E4M3}
+class _Torch:
+    """torch and the groups of its types that the checks compare with, looked up once."""
+
+    def __init__(self):
+        import torch
+        self.torch = torch
+        self.bf16 = (torch.bfloat16, torch.int16)          # values, or their bits
+        self.fp16 = (torch.float16, torch.int16)
+        self.e4m3 = (torch.float8_e4m3fn, torch.uint8)
+        self.e8m0 = (torch.float8_e8m0fnu, torch.uint8)
+        self.u8, self.i32, self.f32, self.f64 = (torch.uint8,), (torch.int32,), (torch.float32,), (torch.float64,)
+        self.device = torch.cuda.current_device
+        self.stream = torch._C._cuda_getCurrentRawStream
+
+
+_torch = None
+
+
+def _th():
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
+
+
+def _typed(name, t, kinds, shape, device):
+    """Address of a contiguous tensor of one of `kinds`, of `shape` (None: any), on `device`."""
+    if t.dtype in kinds and (shape is None or t.shape == shape) and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype not in kinds:
-        _bad(f"element type {t.dtype}: bfloat16 (or int16 bits) or float8_e4m3fn (or uint8 bytes)")
-    return kinds[t.dtype]
-
-
-def _typed(name, t, kinds, shape=None, device=None, packed=True):
-    """Check one tensor argument: its type (names of torch types), shape, device, and that it is contiguous."""
-    if str(t.dtype)[6:] not in kinds:
-        _bad(f"{name}: element type {t.dtype}, not {' or '.join(kinds)}")
+        _bad(f"{name}: element type {t.dtype}, not {' or '.join(str(k) for k in kinds)}")
     if shape is not None and t.shape != shape:
         _bad(f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}")
-    if device is not None and t.device != device:
+    if t.device != device:
         _bad(f"{name}: on {t.device}, not {device}")
-    if packed and not t.is_contiguous():
-        _bad(f"{name} must be contiguous")
+    _bad(f"{name} must be contiguous")
 
 
-_BF16 = ("bfloat16", "int16")
-
-
-def _heads(name, t, device=None):
+def _heads(name, t, device):
     """(address, row stride, head stride) of bf16 [n, heads, head_dim] rows."""
     if t.dim() != 3:
         _bad(f"{name}: [n, heads, head_dim], not {tuple(t.shape)}")
-    _typed(name, t, _BF16, None, device, False)
+    if t.dtype not in _th().bf16:
+        _bad(f"{name}: element type {t.dtype}, not bfloat16 (or its bits as int16)")
+    if t.device != device:
+        _bad(f"{name}: on {t.device}, not {device}")
     row, head, one = t.stride()
     if one != 1 and t.shape[2] > 1:
         _bad(f"{name}: the head_dim values of a head must be adjacent")
@@ -588,14 +604,17 @@ def _heads(name, t, device=None):
 
 def _enqueue(device, fn, *args, stream=None):
     """fn(*args, stream) on `device`: its current stream unless one is given."""
-    import torch
     if device.type != "cuda":
         _bad(f"tensors are on {device}, not on a GPU")
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
+    th, index = _th(), device.index
+    stream = th.stream(index) if stream is None else _stream(stream)
+    if index == th.device():
+        status = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream(stream)))
+        with th.torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status:
+        _check(status)
 
 
 def linear(fmt, x, banks, y, stream=None):
@@ -603,31 +622,36 @@ def linear(fmt, x, banks, y, stream=None):
 
     banks: q4_0 (codes, d), nvfp4 (codes, scale, global), mxfp4_t (blocks, scales, bias or None).
     """
-    f = FORMAT_IDS.get(fmt, fmt)
-    w = list(banks) + [None] * (3 - len(banks))
-    if x.dim() != 2 or y.dim() != 2 or len(w) != 3:
+    th, f = _th(), FORMAT_IDS.get(fmt, fmt)
+    if x.dim() != 2 or y.dim() != 2 or not 2 <= len(banks) <= 3:
         _bad("x [n, K], y [n, N] and two or three banks")
-    (n, K), N, dev = x.shape, y.shape[1], x.device
-    _typed("x", x, _BF16, None, None, False)
-    _typed("y", y, _BF16, (n, N), dev, False)
-    if (x.stride(1) != 1 and K > 1) or (y.stride(1) != 1 and N > 1):
+    n, K = x.shape
+    N, dev = y.shape[1], x.device
+    if x.dtype not in th.bf16 or y.dtype not in th.bf16:
+        _bad(f"x and y: element types {x.dtype} and {y.dtype}, not bfloat16 (or its bits as int16)")
+    if y.shape[0] != n or y.device != dev:
+        _bad(f"y: {tuple(y.shape)} on {y.device}, not {n} rows on {dev}")
+    xs, ys = x.stride(), y.stride()
+    if (xs[1] != 1 and K > 1) or (ys[1] != 1 and N > 1):
         _bad("the values of a row of x or y must be adjacent")
-    if w[0] is None or w[1] is None:
+    codes, scales, third = banks[0], banks[1], banks[2] if len(banks) == 3 else None
+    if codes is None or scales is None:
         _bad("the codes or scales are missing")
-    half = ("float16", "int16")
-    sizes = {Q4_0: (N * K // 2, N * (K // 32), None), NVFP4: (N * K // 2, N * (K // 16), N),
-             MXFP4_T: (N * K // 2, N * (K // 32), N)}.get(f)
-    types = {Q4_0: half, NVFP4: ("uint8", "float8_e4m3fn"), MXFP4_T: ("uint8", "float8_e8m0fnu")}.get(f)
-    if sizes:
-        _typed("codes", w[0], ("uint8",), None, dev)
-        _typed("scales", w[1], types, None, dev)
-        if w[2] is not None:
-            _typed("third bank", w[2], half if f == NVFP4 else _BF16, None, dev)
-        for name, t, size in zip(("codes", "scales", "third bank"), w, sizes):
-            if t is not None and size is not None and t.numel() != size:
-                _bad(f"{name}: {t.numel()} elements, {size} belong to N = {N}, K = {K}")
-    _enqueue(dev, lib().oes_linear, f, _ptr(w[0]), _ptr(w[1]), _ptr(w[2]), N, K, x.data_ptr(), x.stride(0), y.data_ptr(),
-             y.stride(0), n, stream=stream)
+    w0 = _typed("codes", codes, th.u8, None, dev)
+    if f == Q4_0:
+        w1, per = _typed("d", scales, th.fp16, None, dev), 32
+    elif f == NVFP4:
+        w1, per = _typed("scale", scales, th.e4m3, None, dev), 16
+    else:
+        w1, per = _typed("scales", scales, th.e8m0, None, dev), 32
+    if 2 * codes.numel() != N * K or scales.numel() * per != N * K:
+        _bad(f"{codes.numel()} code bytes and {scales.numel()} scales do not belong to N = {N}, K = {K}")
+    w2 = None
+    if third is not None:
+        w2 = _typed("third bank", third, th.fp16 if f == NVFP4 else th.bf16, None, dev)
+        if third.numel() != N:
+            _bad(f"third bank: {third.numel()} values, not N = {N}")
+    _enqueue(dev, lib().oes_linear, f, w0, w1, w2, N, K, x.data_ptr(), xs[0], y.data_ptr(), ys[0], n, stream=stream)
 
 
 class KvPages:
@@ -642,26 +666,28 @@ class KvPages:
     """
 
     def __init__(self, k, v, table, len, k_scale=1.0, v_scale=1.0):
-        import torch
+        th = _th()
         if k.dim() != 4 or v.shape != k.shape:
             _bad(f"k and v: [pages, page_size, kv_heads, head_dim], not {tuple(k.shape)} and {tuple(v.shape)}")
-        if _elem(k) != _elem(v) or k.dtype != v.dtype:
-            _bad("k and v must have one element type")
+        if k.dtype != v.dtype or k.dtype not in th.bf16 + th.e4m3:
+            _bad(f"k and v: element types {k.dtype} and {v.dtype}, not one of bfloat16 (or int16 bits) and "
+                 "float8_e4m3fn (or uint8 bytes)")
         if (k.stride(3) != 1 or v.stride(3) != 1) and k.shape[3] > 1:
             _bad("the head_dim values of a head must be adjacent")
-        _typed("v", v, (str(k.dtype)[6:],), None, k.device, False)
-        _typed("table", table, ("int32",), None, k.device, False)
-        if table.dim() != 2 or (table.stride(1) != 1 and table.shape[1] > 1):
-            _bad("table: [batch, max_pages] with adjacent columns")
-        _typed("len", len, ("int32",), (table.shape[0],), k.device)
+        if v.device != k.device or table.device != k.device:
+            _bad("k, v and table must be on one device")
+        if table.dim() != 2 or table.dtype != th.torch.int32 or (table.stride(1) != 1 and table.shape[1] > 1):
+            _bad("table: int32 [batch, max_pages] with adjacent columns")
+        _typed("len", len, th.i32, (table.shape[0],), k.device)
         self.k, self.v, self.table, self.len = k, v, table, len
         self.device = k.device
-        self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self.status = th.torch.zeros(1, dtype=th.torch.int32, device=k.device)
         self.kv_heads, self.head_dim, self.batch = k.shape[2], k.shape[3], table.shape[0]
         self.capacity = table.shape[1] * k.shape[1]
         ks, vs = k.stride(), v.stride()
         self._kv = Kv(k.data_ptr(), v.data_ptr(), table.data_ptr(), len.data_ptr(), self.status.data_ptr(),
-                      *ks[:3], *vs[:3], table.stride(0), _elem(k), k.shape[0], k.shape[1], k.shape[2], k.shape[3],
+                      *ks[:3], *vs[:3], table.stride(0),
+                      ELEM_BF16 if k.dtype in th.bf16 else ELEM_E4M3, k.shape[0], k.shape[1], k.shape[2], k.shape[3],
                       table.shape[0], table.shape[1], k_scale, v_scale)
         self._ref = ctypes.byref(self._kv)
 
@@ -674,8 +700,7 @@ class KvPages:
 
 
 def _q_start(kv, q_start):
-    _typed("q_start", q_start, ("int32",), (kv.batch + 1,), kv.device)
-    return q_start.data_ptr()
+    return _typed("q_start", q_start, _th().i32, (kv.batch + 1,), kv.device)
 
 
 def rope_freqs(rot_dim, base=10000.0, scaling="none", factor=1.0, trained_len=4096):
@@ -689,30 +714,29 @@ def rope_freqs(rot_dim, base=10000.0, scaling="none", factor=1.0, trained_len=40
 
 def rope(x, y, freq, pos, layout="half", mscale=1.0, stream=None):
     """y = x [n, heads, head_dim] turned by its positions (oes_rope); y may be x."""
-    xp, yp = _heads("x", x), _heads("y", y, x.device)
+    th, dev = _th(), x.device
+    xp, yp = _heads("x", x, dev), _heads("y", y, dev)
     n, heads, D = x.shape
     if y.shape != x.shape:
         _bad(f"y: shape {tuple(y.shape)}, not {tuple(x.shape)}")
-    _typed("freq", freq, ("float64",), None, x.device)
-    _typed("pos", pos, ("int32",), (n,), x.device)
-    _enqueue(x.device, lib().oes_rope, *xp, *yp, n, heads, D, 2 * freq.numel(), ROPE_LAYOUTS.get(layout, layout),
-             freq.data_ptr(), mscale, pos.data_ptr(), stream=stream)
+    _enqueue(dev, lib().oes_rope, *xp, *yp, n, heads, D, 2 * freq.numel(), ROPE_LAYOUTS.get(layout, layout),
+             _typed("freq", freq, th.f64, None, dev), mscale, _typed("pos", pos, th.i32, (n,), dev), stream=stream)
 
 
 def rope_append(q, q_out, k, v, freq, pos, kv, q_start, layout="half", mscale=1.0, stream=None):
-    """rope on a step's q and k; k and v become the last entries of their sequences (oes_rope_append)."""
-    dev = kv.device
+    """rope on a step's q and k; k and v become the last entries of their sequences (oes_rope_append).
+
+    q and q_out may have spare rows behind the last sequence's; k, v and pos have n rows, up to q's.
+    """
+    th, dev = _th(), kv.device
     qp, op, kp, vp = _heads("q", q, dev), _heads("q_out", q_out, dev), _heads("k", k, dev), _heads("v", v, dev)
-    n, heads, D = q.shape
-    # k and v may end with the last sequence's rows, before q's spare ones
-    if q_out.shape != q.shape or D != kv.head_dim or k.shape != v.shape or k.shape[1:] != (kv.kv_heads, D) \
-            or k.shape[0] > n:
-        _bad("q_out has the shape of q; k and v are [rows, kv_heads, head_dim], with no more rows than q")
-    _typed("freq", freq, ("float64",), None, dev)
-    _typed("pos", pos, ("int32",), (k.shape[0],), dev)
-    _enqueue(dev, lib().oes_rope_append, kv._ref, *qp, *op, heads, *kp, *vp, k.shape[0], _q_start(kv, q_start),
-             2 * freq.numel(), ROPE_LAYOUTS.get(layout, layout), freq.data_ptr(), mscale, pos.data_ptr(),
-             stream=stream)
+    n, heads, D = k.shape[0], q.shape[1], kv.head_dim
+    shape = (n, kv.kv_heads, D)
+    if q_out.shape != q.shape or q.shape[2] != D or k.shape != shape or v.shape != shape or n > q.shape[0]:
+        _bad("q_out has the shape of q; k and v are [n, kv_heads, head_dim], with no more rows than q")
+    _enqueue(dev, lib().oes_rope_append, kv._ref, *qp, *op, heads, *kp, *vp, n, _q_start(kv, q_start),
+             2 * freq.numel(), ROPE_LAYOUTS.get(layout, layout), _typed("freq", freq, th.f64, None, dev), mscale,
+             _typed("pos", pos, th.i32, (n,), dev), stream=stream)
 
 
 def attn_workspace_bytes(kv, q_heads, n):
@@ -728,19 +752,21 @@ def attn(q, out, kv, q_start, scale, workspace, window=0, lse=None, stream=None)
     n, heads, D = q.shape
     if out.shape != q.shape or D != kv.head_dim:
         _bad(f"q and out: [n, q_heads, {kv.head_dim}], not {tuple(q.shape)} and {tuple(out.shape)}")
-    if lse is not None:
-        _typed("lse", lse, ("float32",), (n, heads), dev)
-    if workspace.device != dev:
-        _bad("the workspace is on another device")
-    _enqueue(dev, lib().oes_attn, kv._ref, *qp, *op, _ptr(lse), heads, n, _q_start(kv, q_start), scale, window,
-             workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream=stream)
+    lsep = None if lse is None else _typed("lse", lse, _th().f32, (n, heads), dev)
+    _enqueue(dev, lib().oes_attn, kv._ref, *qp, *op, lsep, heads, n, _q_start(kv, q_start), scale, window,
+             *_workspace(workspace, dev), stream=stream)
+
+
+def _workspace(ws, dev):
+    if ws.device != dev or not ws.is_contiguous():
+        _bad("the workspace is on another device, or not contiguous")
+    return ws.data_ptr(), ws.nbytes
 
 
 def _acc(kv, acc):
-    _typed("acc", acc, ("float32",), None, kv.device)
     if acc.dim() != 3 or acc.shape[:2] != (kv.batch, kv.kv_heads):
         _bad(f"acc: [batch, kv_heads, entries], not {tuple(acc.shape)}")
-    return acc.data_ptr(), acc.shape[2]
+    return _typed("acc", acc, _th().f32, None, kv.device), acc.shape[2]
 
 
 def attn_weigh(q, lse, kv, q_start, scale, acc, window=0, stream=None):
@@ -750,9 +776,8 @@ def attn_weigh(q, lse, kv, q_start, scale, acc, window=0, stream=None):
     n, heads, D = q.shape
     if D != kv.head_dim:
         _bad(f"q: head_dim {D}, not {kv.head_dim}")
-    _typed("lse", lse, ("float32",), (n, heads), dev)
-    _enqueue(dev, lib().oes_attn_weigh, kv._ref, *qp, lse.data_ptr(), heads, n, _q_start(kv, q_start), scale, window,
-             *_acc(kv, acc), stream=stream)
+    _enqueue(dev, lib().oes_attn_weigh, kv._ref, *qp, _typed("lse", lse, _th().f32, (n, heads), dev), heads, n,
+             _q_start(kv, q_start), scale, window, *_acc(kv, acc), stream=stream)
 
 
 def kv_evict_workspace_bytes(kv, budget):
@@ -763,10 +788,7 @@ def kv_evict_workspace_bytes(kv, budget):
 
 def kv_evict(kv, acc, budget, kept, new_len, workspace, first=0, last=0, stream=None):
     """Cut every head's entries to `budget`: the first, the last and the heaviest stay, closed up (oes_kv_evict)."""
-    dev = kv.device
-    _typed("kept", kept, ("int32",), (kv.batch, kv.kv_heads, budget), dev)
-    _typed("new_len", new_len, ("int32",), (kv.batch,), dev)
-    if workspace.device != dev:
-        _bad("the workspace is on another device")
-    _enqueue(dev, lib().oes_kv_evict, kv._ref, *_acc(kv, acc), budget, first, last, kept.data_ptr(), new_len.data_ptr(),
-             workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream=stream)
+    th, dev = _th(), kv.device
+    _enqueue(dev, lib().oes_kv_evict, kv._ref, *_acc(kv, acc), budget, first, last,
+             _typed("kept", kept, th.i32, (kv.batch, kv.kv_heads, budget), dev),
+             _typed("new_len", new_len, th.i32, (kv.batch,), dev), *_workspace(workspace, dev), stream=stream)
