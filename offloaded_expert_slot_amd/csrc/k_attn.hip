@@ -15,12 +15,16 @@
 // run in any order, so the V operand is read in that order.)
 //
 // Two shapes:
-//   TILE    128 rows, 32 to each of 4 waves, which share tiles of 64 entries;
+//   TILE    128 rows, 32 to each of 4 waves, which share tiles of 64 entries.  With few tiles
+//           of rows the entries are split over several workgroups.
 //   SPLIT   up to 32 rows (decode steps, small chunks), the same for all waves, each of
 //           which goes over entries of its own, 32 at a time, with no barrier; the waves'
-//           sums are joined through LDS.
-// Either is split over the entries where there are too few tiles to fill the GPU; the
-// parts' sums go through the workspace and attn_merge_kernel joins them in order.
+//           sums are joined through LDS.  The entries of all (tile, head) pairs, in units of
+//           32 per wave, are cut into equal shares for as many workgroups as the GPU holds at
+//           once, whatever the sequences' lengths (a grid over (tile, head, split) took 62 us
+//           for 32 sequences of 1 .. 16384 entries, most of it short and empty workgroups).
+// The sums of a pair that several workgroups share go through the workspace, and
+// attn_merge_kernel joins them in order.
 //
 // Rows of LDS tiles are DP values (head_dim padded to 64, 128 or 256) in 16-byte chunks,
 // chunk c of row r at c ^ swizzle(r), so that neither the 16-byte key reads (16 rows, one
@@ -62,6 +66,12 @@ __device__ inline int swizzle(int row) {
 __device__ inline void load_to_lds(const void *src, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");
 }
+// the same with a wave-uniform base and a 32-bit offset per lane
+__device__ inline void load_to_lds(const void *base, uint32_t off, uint32_t lds) {
+  const uint64_t b = (uint64_t)base;
+  const uint64_t u = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(b >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)b);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(u) : "memory");
+}
 template <int N>
 __device__ inline void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
@@ -87,8 +97,9 @@ __device__ inline uint32_t fp8_bf16_pair(uint32_t w) {
 struct Plan {
   int tile_tokens;   // tokens of a tile
   int tiles;         // tiles of all sequences, at most
-  int splits;        // parts of the entries, at most
-  int chunk;         // entries of a part
+  int splits;        // TILE: parts of the entries, at most
+  int chunk;         // TILE: entries of a part; SPLIT: entries of a unit
+  int blocks;        // SPLIT: workgroups
 };
 
 // A tile of rows and the entries that it sees.
@@ -97,62 +108,121 @@ struct Tile {
   int len, rows;               // entries and rows of the sequence
   int lo, hi;                  // entries that any row sees
   int lo_last, hi_first;       // entries that every row sees
-  int base, parts;             // first entry of part 0; parts that hold entries (at least 1)
-  bool bad;
+  int base, parts;             // first entry of part (unit) 0; parts (units) that hold entries, at least 1
 };
 
 __device__ inline void tile_entries(const AttnArgs &a, const Plan &p, Tile &t) {
+  t.tokens = min(p.tile_tokens, t.rows - t.t0);
   kv_seen(t.len, t.rows, t.t0, a.window, &t.lo, &t.hi_first);
   kv_seen(t.len, t.rows, t.t0 + t.tokens - 1, a.window, &t.lo_last, &t.hi);
   t.base = t.lo & ~31;
   t.parts = t.hi > t.base ? (t.hi - t.base + p.chunk - 1) / p.chunk : 1;
 }
 
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ inline int scan64(int v) {  // inclusive, over the wave
+  const int lane = threadIdx.x & 63;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int u = __shfl_up(v, d, 64);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
+
+// The lane's sequence b0 + lane: rows, entries; 0 where there is none.
+__device__ inline void lane_sequence(const AttnArgs &a, int b0, int *first, int *rows, int *len) {
+  const int b = b0 + (threadIdx.x & 63);
+  *first = *rows = *len = 0;
+  bool bad = false;
+  if (b < a.kv.batch) {
+    *rows = kv_rows(a.q_start[b], a.q_start[b + 1], a.n, first, &bad);
+    *len = kv_len(a.kv, a.kv.len[b], &bad);
+    if (bad) raise_status(a.kv);
+  }
+}
+__device__ inline void take_sequence(Tile &t, int b0, int w, int first, int rows, int len) {
+  t.b = uniform(b0 + w);
+  t.first = uniform(__shfl(first, w, 64));
+  t.rows = uniform(__shfl(rows, w, 64));
+  t.len = uniform(__shfl(len, w, 64));
+}
+
 // Tile `idx` in the order of the sequences (wave-wide; the same answer in every lane).
 __device__ inline bool find_tile(const AttnArgs &a, const Plan &p, int idx, Tile &t) {
-  const int lane = threadIdx.x & 63;
   int before = 0;
   for (int b0 = 0; b0 < a.kv.batch; b0 += 64) {
-    const int b = b0 + lane;
-    int first = 0, rows = 0;
-    bool bad = false;
-    if (b < a.kv.batch) rows = kv_rows(a.q_start[b], a.q_start[b + 1], a.n, &first, &bad);
-    const int mine = (rows + p.tile_tokens - 1) / p.tile_tokens;
-    int upto = mine;
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(upto, d, 64);
-      if (lane >= d) upto += v;
-    }
-    const uint64_t hit = __ballot(mine > 0 && before + upto > idx && before + upto - mine <= idx);
-    const bool any_bad = __any(bad);
+    int first, rows, len;
+    lane_sequence(a, b0, &first, &rows, &len);
+    const int mine = (rows + p.tile_tokens - 1) / p.tile_tokens, upto = before + scan64(mine);
+    const uint64_t hit = __ballot(upto > idx && upto - mine <= idx);
     if (hit) {
       const int w = __builtin_ctzll(hit);
-      t.b = b0 + w;
-      t.first = __builtin_amdgcn_readfirstlane(__shfl(first, w, 64));
-      t.rows = __builtin_amdgcn_readfirstlane(__shfl(rows, w, 64));
-      const int at = __builtin_amdgcn_readfirstlane(__shfl(upto - mine, w, 64));
-      t.t0 = (idx - before - at) * p.tile_tokens;
-      t.tokens = min(p.tile_tokens, t.rows - t.t0);
-      t.bad = any_bad;
-      t.len = __builtin_amdgcn_readfirstlane(kv_len(a.kv, a.kv.len[t.b], &t.bad));
+      take_sequence(t, b0, w, first, rows, len);
+      t.t0 = uniform((idx - __shfl(upto - mine, w, 64)) * p.tile_tokens);
       tile_entries(a, p, t);
-      if (t.bad && lane == 0) raise_status(a.kv);
       return true;
     }
-    if (any_bad && lane == 0) raise_status(a.kv);
-    before += __shfl(upto, 63, 64);
+    before = uniform(__shfl(upto, 63, 64));
   }
   return false;
 }
 
-// Partial sums of a row: ws holds [splits][n][q_heads] pairs (maximum in log2, sum), then
-// [splits][n][q_heads][head_dim] values, fp32.
-__device__ inline float2 *part_stats(const AttnArgs &a, int split, int64_t row_head) {
-  return reinterpret_cast<float2 *>(a.ws) + (int64_t)split * a.n * a.q_heads + row_head;
+// Units of a sequence, over its tiles and all cache heads.
+__device__ inline int sequence_units(const AttnArgs &a, const Plan &p, int rows, int len) {
+  int sum = 0;
+  Tile t;
+  t.rows = rows;
+  t.len = len;
+  for (t.t0 = 0; t.t0 < rows; t.t0 += p.tile_tokens) {
+    tile_entries(a, p, t);
+    sum += t.parts;
+  }
+  return sum * a.kv.kv_heads;
 }
-__device__ inline float *part_sums(const AttnArgs &a, int splits, int split, int64_t row_head) {
-  const int64_t rows = (int64_t)a.n * a.q_heads;
-  return a.ws + 2 * splits * rows + ((int64_t)split * rows + row_head) * a.kv.head_dim;
+
+// SPLIT's order of units: sequence, tile, head, entries.  Where unit `u` stands: its tile, head and place `x`
+// among the tile's units; *total: all units.  (u < 0: only the total.)  Wave-wide.
+__device__ inline bool find_unit(const AttnArgs &a, const Plan &p, int u, Tile &t, int *g, int *x, int *total) {
+  int before = 0;
+  bool found = false;
+  for (int b0 = 0; b0 < a.kv.batch; b0 += 64) {
+    int first, rows, len;
+    lane_sequence(a, b0, &first, &rows, &len);
+    const int mine = sequence_units(a, p, rows, len), upto = before + scan64(mine);
+    const uint64_t hit = __ballot(upto > u && upto - mine <= u);
+    if (hit) {
+      const int w = __builtin_ctzll(hit);
+      take_sequence(t, b0, w, first, rows, len);
+      int left = uniform(u - __shfl(upto - mine, w, 64));
+      for (t.t0 = 0;; t.t0 += p.tile_tokens) {
+        tile_entries(a, p, t);
+        if (left < t.parts * a.kv.kv_heads) break;
+        left -= t.parts * a.kv.kv_heads;
+      }
+      *g = left / t.parts;
+      *x = left - *g * t.parts;
+      found = true;
+      if (!total) return true;
+    }
+    before = uniform(__shfl(upto, 63, 64));
+  }
+  if (total) *total = before;
+  return found;
+}
+// units of a workgroup
+__device__ inline int unit_share(const Plan &p, int total) { return (total + p.blocks - 1) / p.blocks; }
+
+// Partial sums.  TILE: ws holds [splits][n][q_heads] pairs (maximum in log2, sum), then as many rows of head_dim
+// values.  SPLIT: the same of [blocks][2][32]: rows of the pair that a workgroup's share begins within (0), and of
+// the one that its share ends within (1).
+template <bool TILE>
+__device__ inline float2 *part_stats(const AttnArgs &a, int64_t at) {
+  return reinterpret_cast<float2 *>(a.ws) + at;
+}
+template <bool TILE>
+__device__ inline float *part_sums(const AttnArgs &a, const Plan &p, int64_t at) {
+  const int64_t rows = TILE ? (int64_t)p.splits * a.n * a.q_heads : (int64_t)p.blocks * 64;
+  return a.ws + 2 * rows + at * a.kv.head_dim;
 }
 
 template <int DP, bool FP8, bool TILE>
@@ -171,194 +241,273 @@ struct Shape {
 template <int DP, bool FP8, bool TILE>
 __global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8, TILE>::resident)) void attn_kernel(AttnArgs a, Plan plan) {
   using S = Shape<DP, FP8, TILE>;
-  constexpr int KT = S::entries / 32, NB = S::buffers, KS = DP / 16, DT = DP / 32;
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  constexpr int KT = S::entries / 32, NB = S::buffers, KS = DP / 16, DT = DP / 32, E = S::entries, es = FP8 ? 1 : 2;
+  constexpr uint64_t kAll = E == 64 ? ~0ull : 0xffffffffull;
   __shared__ __attribute__((aligned(16))) uint8_t sm[S::lds];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c = lane & 31, half = lane >> 5;
-  const int D = a.kv.head_dim, G = a.q_heads / a.kv.kv_heads;
-
-  // heads are the fastest index: neighbouring workgroups, on different XCDs, take different heads,
-  // so that an XCD keeps to few of them
-  int id = blockIdx.x;
-  const int g = id % a.kv.kv_heads;
-  id /= a.kv.kv_heads;
-  const int split = id / plan.tiles, idx = plan.tiles - 1 - (id - split * plan.tiles);
-  Tile t;
-  if (!find_tile(a, plan, idx, t) || split >= t.parts) return;
-  const int from = t.base + split * plan.chunk, to = min(t.hi, from + plan.chunk);
-  const int32_t *table = a.kv.table + t.b * a.kv.table_stride;
-  const int shift = kv_shift(a.kv.page_size);
-
-  // this lane's row
-  const int r = (TILE ? wave * 32 : 0) + c;
-  const bool row_live = r < t.tokens * G;
-  const int tok = r / G, row_t = t.first + t.t0 + tok, row_h = g * G + (r - tok * G);
-  int lo = 0, hi = 0;
-  if (row_live) kv_seen(t.len, t.rows, t.t0 + tok, a.window, &lo, &hi);
-  bf16x8 q[KS];
-  {
-    const uint16_t *qp = a.q.p + row_t * a.q.row + row_h * a.q.head + 8 * half;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      u32x4 v = {0, 0, 0, 0};
-      if (row_live && ks * 16 < D) v = *reinterpret_cast<const u32x4 *>(qp + 16 * ks);
-      q[ks] = __builtin_bit_cast(bf16x8, v);
-    }
-  }
-  f32x16 o[DT];
-#pragma unroll
-  for (int d = 0; d < DT; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
-  float m = -INFINITY, l = 0.f;
+  __shared__ float jm[4][32], jl[4][32];
+  __shared__ int odd_sm;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c = lane & 31, half = lane >> 5;
+  const int D = a.kv.head_dim, G = a.q_heads / a.kv.kv_heads, shift = kv_shift(a.kv.page_size);
   const float cs = a.scale * a.kv.k_scale * kLog2e;
 
-  // ---- staging: lane `e` of a wave looks up the page of entry e of a tile
-  uint8_t *tiles = sm + (TILE ? 0 : wave * NB * 2 * S::tile_bytes);
-  const int step = TILE ? S::entries : S::entries * S::waves;
-  const int j_first = from + (TILE ? 0 : wave * S::entries);
-  const uint8_t *kb = static_cast<const uint8_t *>(a.kv.k) + a.kv.k_head * g * (FP8 ? 1 : 2);
-  const uint8_t *vb = static_cast<const uint8_t *>(a.kv.v) + a.kv.v_head * g * (FP8 ? 1 : 2);
-  auto lookup = [&](int j0, int *in_page) {
-    const int j = j0 + (S::entries == 32 ? c : lane);
-    int page = -1;
-    *in_page = 0;
-    if (j >= t.lo && j < to) {
-      page = kv_page(a.kv, table, shift, j, in_page);
-      if (page < 0) raise_status(a.kv);
-    }
-    return page;
-  };
-  // the k and v chunks of row `row` of the tile, chunk `ch` of 16 bytes; `bytes` of a head row
-  auto source = [&](int page, int in_page, int row, int ch, int bytes, const uint8_t **ks, const uint8_t **vs) {
-    const int pg = __shfl(page, row, 64), ip = __shfl(in_page, row, 64);
-    const bool live = pg >= 0 && ch * 16 < bytes;
-    constexpr int es = FP8 ? 1 : 2;
-    const uint8_t *z = reinterpret_cast<const uint8_t *>(zero_chunk);
-    *ks = live ? kb + kv_k_off(a.kv, pg, ip) * es + ch * 16 : z;
-    *vs = live ? vb + kv_v_off(a.kv, pg, ip) * es + ch * 16 : z;
-  };
+  // ---- lane constants of the staging
   constexpr int CPR = FP8 ? DP / 16 : DP / 8;   // chunks of a head row
   constexpr int RPI = 64 / CPR;                 // rows that a wave's load covers
   constexpr int LD = S::own / RPI;              // loads of a wave for k, and for v
-  u32x4 stage_k[FP8 ? LD : 1], stage_v[FP8 ? LD : 1];
-  auto issue = [&](int page, int in_page, int buf) {
+  constexpr int own0 = TILE ? S::own : 0;       // rows of a tile before those that wave 1 stages
+  constexpr int GR = S::own / 16, LG = 16 / RPI, NG = E / 16;   // groups of 16 rows; loads of a group
+  uint8_t *tiles = sm + (TILE ? 0 : wave * NB * 2 * S::tile_bytes);
+  // Whole tiles of pages of 16 entries and more: 16 rows stand in one page, so their addresses are a scalar base
+  // and an offset that the lane keeps (with an address of its own per lane and load, the long chunk of 2048 tokens
+  // at 24111 entries took 1.29 ms; see below).  Page numbers are read a tile ahead, through the scalar cache.
+  const bool paged16 = shift >= 4 && D == DP && (a.kv.k_row | a.kv.v_row) < (1 << 22);
+  uint32_t k_lane[LG], v_lane[LG];
 #pragma unroll
-    for (int i = 0; i < LD; ++i) {
-      const int row = (TILE ? wave * S::own : 0) + i * RPI + lane / CPR, phys = lane % CPR;
-      const uint8_t *ks, *vs;
-      if (FP8) {
-        source(page, in_page, row, phys, D, &ks, &vs);
-        stage_k[i] = *reinterpret_cast<const u32x4 *>(ks);
-        stage_v[i] = *reinterpret_cast<const u32x4 *>(vs);
-      } else {
-        source(page, in_page, row, phys ^ swizzle<DP>(row), 2 * D, &ks, &vs);
-        uint8_t *dst = tiles + buf * 2 * S::tile_bytes + ((TILE ? wave * S::own : 0) + i * RPI) * DP * 2;
-        load_to_lds(ks, __builtin_amdgcn_readfirstlane(lds_addr(dst)));
-        load_to_lds(vs, __builtin_amdgcn_readfirstlane(lds_addr(dst + S::tile_bytes)));
-      }
-    }
-  };
-  auto store = [&](int buf) {  // FP8: the staged registers to LDS as bf16
-    if (!FP8) return;
-#pragma unroll
-    for (int i = 0; i < LD; ++i) {
-      const int row = (TILE ? wave * S::own : 0) + i * RPI + lane / CPR, q2 = 2 * (lane % CPR);
-      uint8_t *dst = tiles + buf * 2 * S::tile_bytes + row * DP * 2;
-      const int c0 = (q2 ^ swizzle<DP>(row)) * 16, c1 = ((q2 + 1) ^ swizzle<DP>(row)) * 16;
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const u32x4 w = kv ? stage_v[i] : stage_k[i];
-        const u32x4 w0 = {fp8_bf16_pair<false>(w.x), fp8_bf16_pair<true>(w.x), fp8_bf16_pair<false>(w.y), fp8_bf16_pair<true>(w.y)};
-        const u32x4 w1 = {fp8_bf16_pair<false>(w.z), fp8_bf16_pair<true>(w.z), fp8_bf16_pair<false>(w.w), fp8_bf16_pair<true>(w.w)};
-        *reinterpret_cast<u32x4 *>(dst + kv * S::tile_bytes + c0) = w0;
-        *reinterpret_cast<u32x4 *>(dst + kv * S::tile_bytes + c1) = w1;
-      }
-    }
-  };
+  for (int i = 0; i < LG; ++i) {
+    const int row = i * RPI + lane / CPR, ch = FP8 ? lane % CPR : (lane % CPR) ^ swizzle<DP>(row);
+    k_lane[i] = (uint32_t)(row * a.kv.k_row) * es + ch * 16;
+    v_lane[i] = (uint32_t)(row * a.kv.v_row) * es + ch * 16;
+  }
 
-  // ---- one tile of entries
-  auto compute = [&](int j0, int buf, uint64_t paged) {
-    const uint8_t *kt_base = tiles + buf * 2 * S::tile_bytes, *vt_base = kt_base + S::tile_bytes;
-    f32x16 s[KT];
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
-      const int row = kt * 32 + c;
-      const uint8_t *kr = kt_base + row * DP * 2;
+  // ---- what this workgroup goes over: one part of a pair (TILE), or its share of the units (SPLIT)
+  Tile t;
+  int g = 0, split = 0, unit = 0, unit_end = 0;
+  if (TILE) {
+    // heads are the fastest index: neighbouring workgroups, on different XCDs, take different heads, so that an
+    // XCD keeps to few of them; later tiles, which see more, come first
+    int id = blockIdx.x;
+    g = id % a.kv.kv_heads;
+    id /= a.kv.kv_heads;
+    split = id / plan.tiles;
+    if (!find_tile(a, plan, plan.tiles - 1 - (id - split * plan.tiles), t) || split >= t.parts) return;
+    if (threadIdx.x == 0) odd_sm = 0;
+  } else {
+    int total, x;
+    find_unit(a, plan, -1, t, &g, &x, &total);
+    const int share = unit_share(plan, total);
+    unit = min((int64_t)blockIdx.x * share, (int64_t)total);
+    unit_end = min((int64_t)unit + share, (int64_t)total);
+    if (unit >= unit_end) return;
+  }
+  do {
+    int from, to, x = 0;
+    bool direct;
+    if (TILE) {
+      from = t.base + split * plan.chunk;
+      to = min(t.hi, from + plan.chunk);
+      direct = t.parts == 1;
+    } else {
+      find_unit(a, plan, unit, t, &g, &x, nullptr);
+      const int n = min(t.parts - x, unit_end - unit);
+      from = t.base + x * plan.chunk;
+      to = min(t.hi, from + n * plan.chunk);
+      direct = n == t.parts;
+      unit += n;
+    }
+    const int32_t *table = a.kv.table + t.b * a.kv.table_stride;
+    typedef __attribute__((address_space(4))) const int32_t const_i32;
+    const const_i32 *ctable = (const const_i32 *)(uintptr_t)table;
+    const uint8_t *kb = static_cast<const uint8_t *>(a.kv.k) + a.kv.k_head * g * es;
+    const uint8_t *vb = static_cast<const uint8_t *>(a.kv.v) + a.kv.v_head * g * es;
+    const int step = TILE ? E : E * S::waves, j_first = from + (TILE ? 0 : wave * E);
+
+    // ---- this lane's row
+    const int r = (TILE ? wave * 32 : 0) + c;
+    const bool row_live = r < t.tokens * G;
+    const int tok = r / G, row_t = t.first + t.t0 + tok, row_h = g * G + (r - tok * G);
+    int lo = 0, hi = 0;
+    if (row_live) kv_seen(t.len, t.rows, t.t0 + tok, a.window, &lo, &hi);
+    bf16x8 q[KS];
+    {
+      const uint16_t *qp = a.q.p + row_t * a.q.row + row_h * a.q.head + 8 * half;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        const bf16x8 kf = *reinterpret_cast<const bf16x8 *>(kr + ((2 * ks + half) ^ swizzle<DP>(row)) * 16);
-        s[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[ks], s[kt], 0, 0, 0);
+        u32x4 v = {0, 0, 0, 0};
+        if (row_live && ks * 16 < D) v = *reinterpret_cast<const u32x4 *>(qp + 16 * ks);
+        q[ks] = __builtin_bit_cast(bf16x8, v);
       }
     }
-    // entries that some row of the tile does not see, or that have no page
-    const int j1 = min(j0 + S::entries, to);
-    const bool whole = j0 >= t.lo_last && j0 + S::entries <= min(t.hi_first, to) &&
-                       paged == (S::entries == 64 ? ~0ull : 0xffffffffull);
-    if (!whole) {
+    f32x16 o[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+    float m = -INFINITY, l = 0.f;
+
+    // ---- staging
+    u32x4 stage_k[FP8 ? LD : 1], stage_v[FP8 ? LD : 1];
+    int pages[NG];
+    auto peek = [&](int j0) {  // pages of the tile at j0, where the tile is whole
+      if (paged16 && j0 >= t.lo && j0 + E <= to) {
+#pragma unroll
+        for (int y = 0; y < NG; ++y) pages[y] = ctable[(j0 + 16 * y) >> shift];
+      }
+    };
+    // Loads of the tile at j0 into buffer `buf`; returns which of its entries there are.
+    auto issue = [&](int j0, int buf) -> uint64_t {
+      uint8_t *dst = tiles + buf * 2 * S::tile_bytes + wave * own0 * DP * 2;
+      if (paged16 && j0 >= t.lo && j0 + E <= to) {
+        bool ok = true;
+#pragma unroll
+        for (int y = 0; y < NG; ++y) ok &= (uint32_t)pages[y] < (uint32_t)a.kv.num_pages;
+        if (ok) {
+#pragma unroll
+          for (int z = 0; z < GR; ++z) {
+            int page = pages[z];
+            if (TILE) {
+#pragma unroll
+              for (int y = 1; y < NG; ++y)
+                if (wave == y) page = pages[y];
+            }
+            const int in_page = (j0 + wave * own0 + 16 * z) & (a.kv.page_size - 1);
+            const uint8_t *kp = kb + kv_k_off(a.kv, page, in_page) * es, *vp = vb + kv_v_off(a.kv, page, in_page) * es;
+#pragma unroll
+            for (int i = 0; i < LG; ++i) {
+              if (FP8) {
+                stage_k[z * LG + i] = *reinterpret_cast<const u32x4 *>(kp + k_lane[i]);
+                stage_v[z * LG + i] = *reinterpret_cast<const u32x4 *>(vp + v_lane[i]);
+              } else {
+                const uint32_t at = uniform(lds_addr(dst + (16 * z + i * RPI) * DP * 2));
+                load_to_lds(kp, k_lane[i], at);
+                load_to_lds(vp, v_lane[i], at + S::tile_bytes);
+              }
+            }
+          }
+          return ~0ull;
+        }
+      }
+      // one entry per lane, zeros where there is none.  (The lane is made opaque: what this rare path computes
+      // from it is not to live in registers through the loop.)
+      int ln = lane;
+      asm volatile("" : "+v"(ln));
+      const int j = j0 + (E == 32 ? ln & 31 : ln);
+      int page = -1, in_page = 0;
+      if (j >= t.lo && j < to) {
+        page = kv_page(a.kv, table, shift, j, &in_page);
+        if (page < 0) raise_status(a.kv);
+      }
+#pragma unroll
+      for (int i = 0; i < LD; ++i) {
+        const int row = wave * own0 + i * RPI + ln / CPR, ch = FP8 ? ln % CPR : (ln % CPR) ^ swizzle<DP>(row);
+        const int pg = __shfl(page, row, 64), ip = __shfl(in_page, row, 64);
+        const uint8_t *ks = reinterpret_cast<const uint8_t *>(zero_chunk), *vs = ks;
+        if (pg >= 0 && ch * 16 < D * es) {
+          ks = kb + kv_k_off(a.kv, pg, ip) * es + ch * 16;
+          vs = vb + kv_v_off(a.kv, pg, ip) * es + ch * 16;
+        }
+        if (FP8) {
+          stage_k[i] = *reinterpret_cast<const u32x4 *>(ks);
+          stage_v[i] = *reinterpret_cast<const u32x4 *>(vs);
+        } else {
+          const uint32_t at = uniform(lds_addr(dst + i * RPI * DP * 2));
+          load_to_lds(ks, at);
+          load_to_lds(vs, at + S::tile_bytes);
+        }
+      }
+      return (uint64_t)__ballot(page >= 0);
+    };
+    auto store = [&](int buf) {  // FP8: the staged registers to LDS as bf16
+#pragma unroll
+      for (int i = 0; i < (FP8 ? LD : 0); ++i) {
+        const int row = wave * own0 + i * RPI + lane / CPR, q2 = 2 * (lane % CPR);
+        uint8_t *dst = tiles + buf * 2 * S::tile_bytes + row * DP * 2;
+        const int c0 = (q2 ^ swizzle<DP>(row)) * 16, c1 = ((q2 + 1) ^ swizzle<DP>(row)) * 16;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const u32x4 w = kv ? stage_v[i] : stage_k[i];
+          const u32x4 w0 = {fp8_bf16_pair<false>(w.x), fp8_bf16_pair<true>(w.x), fp8_bf16_pair<false>(w.y), fp8_bf16_pair<true>(w.y)};
+          const u32x4 w1 = {fp8_bf16_pair<false>(w.z), fp8_bf16_pair<true>(w.z), fp8_bf16_pair<false>(w.w), fp8_bf16_pair<true>(w.w)};
+          *reinterpret_cast<u32x4 *>(dst + kv * S::tile_bytes + c0) = w0;
+          *reinterpret_cast<u32x4 *>(dst + kv * S::tile_bytes + c1) = w1;
+        }
+      }
+    };
+
+    // Whether every row of the tile of rows sees all entries of the tile at j0.
+    auto seen_by_all = [&](int j0) { return j0 >= t.lo_last && j0 + E <= min(t.hi_first, to); };
+    // Where they do not, a value that is not finite must not meet the zero weight of a row that does not see it
+    // (0 * inf): it is cleared in LDS, and added behind the loop to the rows that see it.  Whether there was one in
+    // the rows that this wave stages.
+    auto clear_odd = [&](int buf) {
+      uint32_t *v = reinterpret_cast<uint32_t *>(tiles + buf * 2 * S::tile_bytes + S::tile_bytes + wave * own0 * DP * 2);
+      bool any = false;
+#pragma unroll 1
+      for (int i = lane; i < S::own * DP / 2; i += 64) {
+        const uint32_t w = v[i], e = ((w & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;  // exponents of all ones
+        if (e) v[i] = w & ~((e >> 15) * 0xffffu);
+        any |= e != 0;
+      }
+      return __any(any) != 0;
+    };
+
+    // ---- one tile of entries
+    auto compute = [&](int j0, int buf, uint64_t paged) {
+      const uint8_t *kt_base = tiles + buf * 2 * S::tile_bytes, *vt_base = kt_base + S::tile_bytes;
+      f32x16 s[KT];
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
+        const int row = kt * 32 + c;
+        const uint8_t *kr = kt_base + row * DP * 2;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const bf16x8 kf = *reinterpret_cast<const bf16x8 *>(kr + ((2 * ks + half) ^ swizzle<DP>(row)) * 16);
+          s[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[ks], s[kt], 0, 0, 0);
+        }
+      }
+      if (!seen_by_all(j0) || paged != kAll) {
+        asm volatile("");   // (or the compiler makes selects of this, in every tile)
+        // entries of registers i are 8 (i / 4) + i % 4 from the half's first
+        const int at = j0 + 4 * half, lo_at = lo - at, hi_at = min(hi, to) - at;
+        const uint64_t bits = paged >> (4 * half);
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int e = kt * 32 + 8 * (i / 4) + i % 4;
+            if (e < lo_at || e >= hi_at || !((bits >> e) & 1)) s[kt][i] = -INFINITY;
+          }
+      }
+      float mx = s[0][0];
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int e = kt * 32 + 8 * (i / 4) + 4 * half + i % 4, j = j0 + e;
-          if (j < lo || j >= hi || j >= j1 || !((paged >> e) & 1)) s[kt][i] = -INFINITY;
-        }
-    }
-    float mx = s[0][0];
+        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[kt][i]);
+      mx = max_halves(mx) * cs;
+      if (__any(mx > m + kSlack)) {  // true for the first visible entries (m = -inf)
+        const float mn = fmaxf(m, mx);
+        const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        l *= f;
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
+        for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[kt][i]);
-    mx = max_halves(mx) * cs;
-    if (__any(mx > m + kSlack)) {  // true for the first visible entries (m = -inf)
-      const float mn = fmaxf(m, mx);
-      const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
-      m = mn;
-      l *= f;
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[d][i] *= f;
-    }
-    const float mu = m == -INFINITY ? 0.f : m;
-    uint32_t p[KT][8];
-    float sum = 0.f;
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const float p0 = __builtin_amdgcn_exp2f(fmaf(s[kt][i], cs, -mu)), p1 = __builtin_amdgcn_exp2f(fmaf(s[kt][i + 1], cs, -mu));
-        sum += p0;
-        sum += p1;
-        p[kt][i / 2] = f2bf16_pair(p0, p1);
+          for (int i = 0; i < 16; ++i) o[d][i] *= f;
       }
-    l += sum;
-    // transposing reads: lane i of 16 points at row i / 4, 4 dims i % 4, and gets dim i of 4 rows
-    const int gq = lane >> 4, tr_row = 4 * (gq >> 1) + ((lane & 15) >> 2), tr_ch = 2 * (gq & 1) + ((lane & 3) >> 1),
-              tr_off = 8 * (lane & 1);
-    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-    // Where the rows of the tile see different entries, a value that is not finite must not meet the
-    // zero weight of a row that does not see it (0 * inf): it is taken out of the product, and added
-    // entry by entry, to the rows that see it, behind it.
-    const bool mixed = !whole && t.tokens > 1;
-    uint32_t odd = 0;
-    auto values = [&](int row0, int d, auto clean) {
-      const int row = row0 + tr_row;
-      const uint8_t *v = vt_base + row * DP * 2 + ((d * 4 + tr_ch) ^ swizzle<DP>(row)) * 16 + tr_off;
-      u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)v));
-      if (clean) {
+      const float mu = m == -INFINITY ? 0.f : m;
+      uint32_t p[KT][8];
+      float sum = 0.f;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t e = ((w[x] & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;  // exponents of all ones
-          odd |= e;
-          w[x] &= ~((e >> 15) * 0xffffu);
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const float p0 = __builtin_amdgcn_exp2f(fmaf(s[kt][i], cs, -mu)), p1 = __builtin_amdgcn_exp2f(fmaf(s[kt][i + 1], cs, -mu));
+          sum += p0;
+          sum += p1;
+          p[kt][i / 2] = f2bf16_pair(p0, p1);
         }
-      }
-      return w;
-    };
-    auto weigh_values = [&](auto clean) {
+      l += sum;
+      // transposing reads: lane i of 16 points at row i / 4, 4 dims i % 4, and gets dim i of 4 rows
+      const int gq = lane >> 4, tr_row = 4 * (gq >> 1) + ((lane & 15) >> 2), tr_ch = 2 * (gq & 1) + ((lane & 3) >> 1),
+                tr_off = 8 * (lane & 1);
+      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+      auto values = [&](int row0, int d) {
+        const int row = row0 + tr_row;
+        const uint8_t *v = vt_base + row * DP * 2 + ((d * 4 + tr_ch) ^ swizzle<DP>(row)) * 16 + tr_off;
+        return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)v));
+      };
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -366,208 +515,241 @@ __global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8,
           const u32x4 pw = {p[kt][4 * k2], p[kt][4 * k2 + 1], p[kt][4 * k2 + 2], p[kt][4 * k2 + 3]};
 #pragma unroll
           for (int d = 0; d < DT; ++d) {
-            const u32x2 v0 = values(kt * 32 + 16 * k2, d, clean), v1 = values(kt * 32 + 16 * k2 + 8, d, clean);
+            const u32x2 v0 = values(kt * 32 + 16 * k2, d), v1 = values(kt * 32 + 16 * k2 + 8, d);
             const u32x4 vw = {v0.x, v0.y, v1.x, v1.y};
             o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vw), __builtin_bit_cast(bf16x8, pw), o[d], 0, 0, 0);
           }
         }
     };
-    if (!mixed) {
-      weigh_values(std::false_type{});
-      return;
+
+    // ---- the loop: loads of the next tile run under the products of this one
+    bool odd = false;
+    if (j_first < to) {
+      int buf = 0;
+      peek(j_first);
+      uint64_t paged = issue(j_first, 0);
+      peek(j_first + step);
+      if (FP8 && !TILE) store(0);
+      for (int j0 = j_first; j0 < to; j0 += step) {
+        const bool more = j0 + step < to;
+        uint64_t paged_next = 0;
+        if (TILE) {
+          if (FP8)
+            store(buf);
+          else
+            wait_loads<0>();
+          __syncthreads();
+          if (more) paged_next = issue(j0 + step, buf ^ 1);
+        } else if (more) {
+          paged_next = issue(j0 + step, NB == 2 ? buf ^ 1 : 0);
+          if (!FP8) wait_loads<2 * LD>();
+        } else if (!FP8) {
+          wait_loads<0>();
+        }
+        peek(j0 + 2 * step);
+        const int at = NB == 2 ? buf : 0;
+        if (t.tokens > 1 && !seen_by_all(j0)) {
+          if (clear_odd(at)) {
+            odd = true;
+            if (TILE && lane == 0) odd_sm = 1;
+          }
+          if (TILE) __syncthreads();
+        }
+        compute(j0, at, paged & kAll);
+        if (!TILE && FP8 && more) store(0);
+        buf ^= 1;
+        paged = paged_next;
+      }
     }
-    weigh_values(std::true_type{});
-    if (__any(odd != 0)) {
+    if (TILE) {
+      __syncthreads();
+      odd = odd_sm != 0;
+    }
+    if (odd) {
+      // the cleared values, entry by entry, with the weights formed anew: m is the final maximum
 #pragma unroll 1
-      for (int e = 0; e < S::entries; ++e) {
-        const int j = j0 + e, i = (e & 32) / 2 + 4 * ((e & 31) / 8) + e % 4;  // register 16 kt + i of half (e / 4) % 2
-        uint32_t word = 0;
+      for (int j0 = j_first; j0 < to; j0 += step) {
+        if (seen_by_all(j0)) continue;
+#pragma unroll 1
+        for (int j = max(j0, t.lo); j < min(j0 + E, to); ++j) {
+          int in_page;
+          const int page = kv_page(a.kv, table, shift, j, &in_page);
+          if (page < 0) continue;
+          const uint8_t *vp = vb + kv_v_off(a.kv, page, in_page) * es, *kp = kb + kv_k_off(a.kv, page, in_page) * es;
+          bool any = false;
+          for (int d = lane; d < D; d += 64) {
+            const uint32_t v = FP8 ? vp[d] : reinterpret_cast<const uint16_t *>(vp)[d];
+            any |= FP8 ? (v & 0x7f) == 0x7f : (v & 0x7f80) == 0x7f80;
+          }
+          if (!__any(any)) continue;
+          float dot = 0.f;
 #pragma unroll
-        for (int x = 0; x < KT * 8; ++x)
-          if (x == i / 2) word = p[x / 8][x % 8];
-        const float w = __shfl((i & 1) ? bf16_hi(word) : bf16_lo(word), c + 32 * ((e >> 2) & 1), 64);
-        const bool sees = j >= lo && j < hi && j < j1 && ((paged >> e) & 1);
+          for (int ks = 0; ks < KS; ++ks)
+            if (ks * 16 < D) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int d = 16 * ks + 8 * half + e;
+                dot = fmaf((float)q[ks][e], FP8 ? e4m3_pair<false>(kp[d]).x : bf16f(reinterpret_cast<const uint16_t *>(kp)[d]), dot);
+              }
+            }
+          const float w = __builtin_amdgcn_exp2f(fmaf(sum_halves(dot), cs, -m));
+          if (j < lo || j >= hi) continue;
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int dim = d * 32 + 8 * (i / 4) + 4 * half + i % 4;
+              if (dim < D) {
+                const float v = FP8 ? e4m3_pair<false>(vp[dim]).x : bf16f(reinterpret_cast<const uint16_t *>(vp)[dim]);
+                if (!(fabsf(v) < INFINITY)) o[d][i] = fmaf(w, v, o[d][i]);
+              }
+            }
+        }
+      }
+    }
+
+    // ---- results
+    l = sum_halves(l);
+    if (TILE) {
+      if (!row_live) return;
+      const int64_t rh = (int64_t)row_t * a.q_heads + row_h;
+      if (direct) {
+        const float inv = l == 0.f ? 0.f : a.kv.v_scale / l;
+        uint16_t *op = a.out.p + row_t * a.out.row + row_h * a.out.head + 4 * half;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int dim = d * 32 + 8 * (k / 4) + 4 * half + k % 4;
-            const uint32_t v = *reinterpret_cast<const uint16_t *>(vt_base + e * DP * 2 + ((dim >> 3) ^ swizzle<DP>(e)) * 16 + (dim & 7) * 2);
-            if (sees && (v & 0x7f80u) == 0x7f80u) o[d][k] = fmaf(w, bf16f(v), o[d][k]);
-          }
-      }
-    }
-  };
-
-  // ---- the loop: loads of the next tile run under the products of this one
-  if (j_first < to) {
-    int ip, ip_next = 0, buf = 0;
-    int page = lookup(j_first, &ip);
-    issue(page, ip, 0);
-    int page_next = lookup(j_first + step, &ip_next);
-    uint64_t paged = __ballot(page >= 0);
-    if (FP8 && !TILE) store(0);
-    for (int j0 = j_first; j0 < to; j0 += step) {
-      const bool more = j0 + step < to;
-      const uint64_t paged_next = __ballot(page_next >= 0);
-      int page_after = -1, ip_after = 0;
-      if (more) page_after = lookup(j0 + 2 * step, &ip_after);
-      if (TILE) {
-        if (FP8)
-          store(buf);
-        else
-          wait_loads<0>();
-        __syncthreads();
-        if (more) issue(page_next, ip_next, buf ^ 1);
-      } else if (FP8) {
-        if (more) issue(page_next, ip_next, 0);
-      } else if (more) {
-        issue(page_next, ip_next, buf ^ 1);
-        wait_loads<2 * LD>();
+          for (int i = 0; i < 16; i += 4)
+            if (d * 32 + 2 * i < D) {
+              const u32x2 w = {f2bf16_pair(o[d][i] * inv, o[d][i + 1] * inv), f2bf16_pair(o[d][i + 2] * inv, o[d][i + 3] * inv)};
+              *reinterpret_cast<u32x2 *>(op + d * 32 + 2 * i) = w;
+            }
+        if (a.lse && half == 0) a.lse[rh] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
       } else {
-        wait_loads<0>();
+        const int64_t at = (int64_t)split * a.n * a.q_heads + rh;
+        float *op = part_sums<TILE>(a, plan, at) + 4 * half;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            if (d * 32 + 2 * i < D) *reinterpret_cast<f32x4 *>(op + d * 32 + 2 * i) = f32x4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
+        if (half == 0) *part_stats<TILE>(a, at) = make_float2(m, l);
       }
-      compute(j0, NB == 2 ? buf : 0, S::entries == 64 ? paged : paged & 0xffffffffull);
-      if (!TILE && FP8 && more) store(0);
-      buf ^= 1;
-      page_next = page_after;
-      ip_next = ip_after;
-      paged = paged_next;
+      return;
     }
-  }
-
-  // ---- results
-  l = sum_halves(l);
-  const bool direct = t.parts == 1;
-  if (TILE) {
-    if (!row_live) return;
-    const int64_t rh = (int64_t)row_t * a.q_heads + row_h;
-    if (direct) {
-      const float inv = l == 0.f ? 0.f : a.kv.v_scale / l;
-      uint16_t *op = a.out.p + row_t * a.out.row + row_h * a.out.head + 4 * half;
+    // SPLIT: join the waves
+    __syncthreads();  // every wave is done with its tiles
+    float *jo = reinterpret_cast<float *>(sm);                 // [waves][32][DP]
+    constexpr int JS = 32 * DP;
+    {
+      float *mine = jo + wave * JS + c * DP + 4 * half;
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          if (d * 32 + 2 * i < D) {
-            const u32x2 w = {f2bf16_pair(o[d][i] * inv, o[d][i + 1] * inv), f2bf16_pair(o[d][i + 2] * inv, o[d][i + 3] * inv)};
-            *reinterpret_cast<u32x2 *>(op + d * 32 + 2 * i) = w;
-          }
-      if (a.lse && half == 0) a.lse[rh] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
-    } else {
-      float *op = part_sums(a, plan.splits, split, rh) + 4 * half;
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          if (d * 32 + 2 * i < D) {
-            typedef float f32x4 __attribute__((ext_vector_type(4)));
-            const f32x4 w = {o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
-            *reinterpret_cast<f32x4 *>(op + d * 32 + 2 * i) = w;
-          }
-      if (half == 0) *part_stats(a, split, rh) = make_float2(m, l);
-    }
-    return;
-  }
-  // SPLIT: join the waves
-  __syncthreads();  // every wave is done with its tiles
-  float *jo = reinterpret_cast<float *>(sm);                 // [waves][32][DP]
-  constexpr int JS = 32 * DP;
-  __shared__ float jm[4][32], jl[4][32];
-  {
-    float *mine = jo + wave * JS + c * DP + 4 * half;
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        typedef float f32x4 __attribute__((ext_vector_type(4)));
-        const f32x4 w = {o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
-        *reinterpret_cast<f32x4 *>(mine + d * 32 + 2 * i) = w;
-      }
-    if (half == 0) {
-      jm[wave][c] = m;
-      jl[wave][c] = l;
-    }
-  }
-  __syncthreads();
-  for (int it = threadIdx.x; it < t.tokens * G * (D / 4); it += S::waves * 64) {
-    const int jr = it / (D / 4), d4 = (it - jr * (D / 4)) * 4;
-    const int jt = jr / G, rt = t.first + t.t0 + jt, rh_ = g * G + (jr - jt * G);
-    float mm = jm[0][jr];
-#pragma unroll
-    for (int w = 1; w < S::waves; ++w) mm = fmaxf(mm, jm[w][jr]);
-    float ll = 0.f, s4[4] = {0.f, 0.f, 0.f, 0.f};
-    if (mm != -INFINITY) {
-#pragma unroll
-      for (int w = 0; w < S::waves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(jm[w][jr] - mm);
-        ll = fmaf(jl[w][jr], f, ll);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) s4[x] = fmaf(jo[w * JS + jr * DP + d4 + x], f, s4[x]);
+        for (int i = 0; i < 16; i += 4) *reinterpret_cast<f32x4 *>(mine + d * 32 + 2 * i) = f32x4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
+      if (half == 0) {
+        jm[wave][c] = m;
+        jl[wave][c] = l;
       }
     }
-    const int64_t rh = (int64_t)rt * a.q_heads + rh_;
-    if (direct) {
-      const float inv = ll == 0.f ? 0.f : a.kv.v_scale / ll;
-      const u32x2 w = {f2bf16_pair(s4[0] * inv, s4[1] * inv), f2bf16_pair(s4[2] * inv, s4[3] * inv)};
-      *reinterpret_cast<u32x2 *>(a.out.p + rt * a.out.row + rh_ * a.out.head + d4) = w;
-      if (a.lse && d4 == 0) a.lse[rh] = ll == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * kLn2;
-    } else {
-      typedef float f32x4 __attribute__((ext_vector_type(4)));
-      const f32x4 w = {s4[0], s4[1], s4[2], s4[3]};
-      *reinterpret_cast<f32x4 *>(part_sums(a, plan.splits, split, rh) + d4) = w;
-      if (d4 == 0) *part_stats(a, split, rh) = make_float2(mm, ll);
+    __syncthreads();
+    for (int it = threadIdx.x; it < t.tokens * G * (D / 4); it += S::waves * 64) {
+      const int jr = it / (D / 4), d4 = (it - jr * (D / 4)) * 4;
+      const int jt = jr / G, rt = t.first + t.t0 + jt, rh_ = g * G + (jr - jt * G);
+      float mm = jm[0][jr];
+#pragma unroll
+      for (int w = 1; w < S::waves; ++w) mm = fmaxf(mm, jm[w][jr]);
+      float ll = 0.f;
+      f32x4 s4 = {0.f, 0.f, 0.f, 0.f};
+      if (mm != -INFINITY) {
+#pragma unroll
+        for (int w = 0; w < S::waves; ++w) {
+          const float f = __builtin_amdgcn_exp2f(jm[w][jr] - mm);
+          ll = fmaf(jl[w][jr], f, ll);
+          const f32x4 v = *reinterpret_cast<const f32x4 *>(jo + w * JS + jr * DP + d4);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) s4[y] = fmaf(v[y], f, s4[y]);
+        }
+      }
+      if (direct) {
+        const float inv = ll == 0.f ? 0.f : a.kv.v_scale / ll;
+        const u32x2 w = {f2bf16_pair(s4[0] * inv, s4[1] * inv), f2bf16_pair(s4[2] * inv, s4[3] * inv)};
+        *reinterpret_cast<u32x2 *>(a.out.p + rt * a.out.row + rh_ * a.out.head + d4) = w;
+        if (a.lse && d4 == 0) a.lse[(int64_t)rt * a.q_heads + rh_] = ll == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * kLn2;
+      } else {
+        const int64_t at = (blockIdx.x * 2ll + (x == 0)) * 32 + jr;
+        *reinterpret_cast<f32x4 *>(part_sums<TILE>(a, plan, at) + d4) = s4;
+        if (d4 == 0) *part_stats<TILE>(a, at) = make_float2(mm, ll);
+      }
     }
-  }
+    if (unit < unit_end) __syncthreads();  // before the next pair's tiles
+  } while (!TILE && unit < unit_end);
 }
 
 // Joins the parts of a row, in their order.  One workgroup of 4 waves per (row, head): wave w
 // adds parts w, w + 4, ...; lane i holds dims 4 i .. 4 i + 3.
+template <bool TILE>
 __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a, Plan plan) {
   typedef float f32x4 __attribute__((ext_vector_type(4)));
   __shared__ f32x4 so[4][64];
   __shared__ float sl[4];
   const int row = blockIdx.x / a.q_heads, h = blockIdx.x - row * a.q_heads, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  // the sequence of this row, then its tile
+  const int G = a.q_heads / a.kv.kv_heads, g = h / G;
+  // the sequence of this row, then its tile and where its parts are
   Tile t;
   t.b = -1;
+  int before = 0, total = 0, start = 0;
   for (int b0 = 0; b0 < a.kv.batch; b0 += 64) {
-    const int b = b0 + lane;
-    int first = 0, rows = 0;
-    bool bad = false;
-    if (b < a.kv.batch) rows = kv_rows(a.q_start[b], a.q_start[b + 1], a.n, &first, &bad);
+    int first, rows, len;
+    lane_sequence(a, b0, &first, &rows, &len);
+    const int mine = TILE ? 0 : sequence_units(a, plan, rows, len), upto = before + scan64(mine);
     const uint64_t hit = __ballot(row >= first && row < first + rows);
-    if (hit) {
+    if (hit && t.b < 0) {
       const int w = __builtin_ctzll(hit);
-      t.b = b0 + w;
-      t.first = __shfl(first, w, 64);
-      t.rows = __shfl(rows, w, 64);
-      break;
+      take_sequence(t, b0, w, first, rows, len);
+      start = __shfl(upto - mine, w, 64);
+      if (TILE) break;
     }
+    before = __shfl(upto, 63, 64);
   }
+  total = before;
   if (t.b < 0) return;
-  t.len = kv_len(a.kv, a.kv.len[t.b], &t.bad);
-  t.t0 = (row - t.first) / plan.tile_tokens * plan.tile_tokens;
-  t.tokens = min(plan.tile_tokens, t.rows - t.t0);
+  const int own_t0 = (row - t.first) / plan.tile_tokens * plan.tile_tokens;
+  if (!TILE)
+    for (t.t0 = 0; t.t0 < own_t0; t.t0 += plan.tile_tokens) {
+      tile_entries(a, plan, t);
+      start += t.parts * a.kv.kv_heads;
+    }
+  t.t0 = own_t0;
   tile_entries(a, plan, t);
-  if (t.parts == 1) return;  // written by its workgroup
-  const int64_t rh = (int64_t)row * a.q_heads + h;
+  int parts = t.parts, b_first = 0;
+  int64_t at0 = (int64_t)row * a.q_heads + h, stride = (int64_t)a.n * a.q_heads;   // TILE: part s at at0 + s * stride
+  if (!TILE) {
+    const int share = unit_share(plan, total);
+    start += g * t.parts;
+    b_first = start / share;
+    parts = (start + t.parts - 1) / share - b_first + 1;
+    at0 = b_first * 64ll + (row - t.first - t.t0) * G + h - g * G;   // part 0 begins a pair: place 1; the others 0
+    stride = 64;
+  }
+  if (parts == 1) return;  // written by its workgroup
+  auto place = [&](int s) { return at0 + s * stride + (!TILE && s == 0 ? 32 : 0); };
   float mm = -INFINITY;
-  for (int s = lane; s < t.parts; s += 64) mm = fmaxf(mm, part_stats(a, s, rh)->x);
+  for (int s = lane; s < parts; s += 64) mm = fmaxf(mm, part_stats<TILE>(a, place(s))->x);
   for (int d = 32; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor(mm, d, 64));
   f32x4 sum = {0.f, 0.f, 0.f, 0.f};
   float ll = 0.f;
   const bool live = 4 * lane < a.kv.head_dim;
   if (mm != -INFINITY) {
 #pragma unroll 4
-    for (int s = wave; s < t.parts; s += 4) {
-      const float2 st = *part_stats(a, s, rh);
+    for (int s = wave; s < parts; s += 4) {
+      const float2 st = *part_stats<TILE>(a, place(s));
       const float f = __builtin_amdgcn_exp2f(st.x - mm);
       ll = fmaf(st.y, f, ll);
       if (live) {
-        const f32x4 v = *reinterpret_cast<const f32x4 *>(part_sums(a, plan.splits, s, rh) + 4 * lane);
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(part_sums<TILE>(a, plan, place(s)) + 4 * lane);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) sum[x] = fmaf(v[x], f, sum[x]);
+        for (int y = 0; y < 4; ++y) sum[y] = fmaf(v[y], f, sum[y]);
       }
     }
   }
@@ -580,11 +762,11 @@ __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a, Plan plan) 
   if (live) {
     f32x4 v;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) v[x] = ((so[0][lane][x] + so[1][lane][x]) + (so[2][lane][x] + so[3][lane][x])) * inv;
+    for (int y = 0; y < 4; ++y) v[y] = ((so[0][lane][y] + so[1][lane][y]) + (so[2][lane][y] + so[3][lane][y])) * inv;
     const u32x2 w = {f2bf16_pair(v[0], v[1]), f2bf16_pair(v[2], v[3])};
     *reinterpret_cast<u32x2 *>(a.out.p + row * a.out.row + h * a.out.head + 4 * lane) = w;
   }
-  if (a.lse && lane == 0) a.lse[rh] = ll == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * kLn2;
+  if (a.lse && lane == 0) a.lse[(int64_t)row * a.q_heads + h] = ll == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * kLn2;
 }
 
 // ------------------------------------------------------------------ weigh
@@ -746,26 +928,29 @@ bool split_shape(const oes_kv &kv, int q_heads, int n) {
   return G <= 32 && (int64_t)n * G <= 32ll * kv.batch;
 }
 
+int head_pad(const oes_kv &kv) { return kv.head_dim <= 64 ? 64 : (kv.head_dim <= 128 ? 128 : 256); }
+
 Plan make_plan(const oes_kv &kv, int q_heads, int n) {
-  const int G = q_heads / kv.kv_heads;
-  const bool split = split_shape(kv, q_heads, n);
-  Plan p;
+  const int G = q_heads / kv.kv_heads, dp = head_pad(kv);
+  const bool split = split_shape(kv, q_heads, n), fp8 = kv.elem == OES_ELEM_E4M3;
+  Plan p = {};
   p.tile_tokens = (split ? 32 : 128) / G;
   // every sequence with rows has at most one tile that is not full
   const int64_t tiles = std::min<int64_t>(n, ((int64_t)n + (int64_t)kv.batch * (p.tile_tokens - 1)) / p.tile_tokens);
   p.tiles = (int)tiles;
-  const int64_t cap = ((int64_t)kv.max_pages * kv.page_size + 31) / 32 * 32 + 32;
-  const int64_t units = tiles * kv.kv_heads;
-  int64_t chunk;
+  const int64_t cap = ((int64_t)kv.max_pages * kv.page_size + 31) / 32 * 32 + 32;   // entries of a tile, from its base
   if (split) {
-    chunk = std::max<int64_t>(128, (cap * units / 4096 + 127) / 128 * 128);
+    p.chunk = 32 * (dp == 256 ? 2 : 4);
+    // as many workgroups as are resident at once: LDS holds two to a CU, or one of the bf16 cache's 128 KiB
+    p.blocks = (int)std::min<int64_t>(dp == 64 || (fp8 && dp == 128) ? 512 : 256, tiles * kv.kv_heads * ((cap + p.chunk - 1) / p.chunk));
+    p.splits = cap <= p.chunk ? 1 : 2;
   } else {
-    const int64_t parts = std::max<int64_t>(1, 512 / units);
-    chunk = std::max<int64_t>(256, ((cap + parts - 1) / parts + 63) / 64 * 64);
+    const int64_t parts = std::max<int64_t>(1, 512 / (tiles * kv.kv_heads));
+    int64_t chunk = std::max<int64_t>(256, ((cap + parts - 1) / parts + 63) / 64 * 64);
+    p.splits = (int)((cap + chunk - 1) / chunk);
+    if (p.splits == 1) chunk = cap;
+    p.chunk = (int)std::min<int64_t>(chunk, 1 << 30);
   }
-  p.splits = (int)((cap + chunk - 1) / chunk);
-  if (p.splits == 1) chunk = cap;
-  p.chunk = (int)std::min<int64_t>(chunk, 1 << 30);
   return p;
 }
 
@@ -775,34 +960,37 @@ hipError_t launch_shape(const AttnArgs &a, const Plan &p, uint32_t blocks, hipSt
   return hipGetLastError();
 }
 
+template <int DP>
+hipError_t launch_dim(const AttnArgs &a, const Plan &p, bool split, uint32_t blocks, hipStream_t s) {
+  if (a.kv.elem == OES_ELEM_E4M3) return split ? launch_shape<DP, true, false>(a, p, blocks, s) : launch_shape<DP, true, true>(a, p, blocks, s);
+  return split ? launch_shape<DP, false, false>(a, p, blocks, s) : launch_shape<DP, false, true>(a, p, blocks, s);
+}
+
 }  // namespace
 
 int64_t attn_workspace_bytes(const oes_kv &kv, int q_heads, int n) {
   const Plan p = make_plan(kv, q_heads, n);
-  return p.splits == 1 ? 0 : (int64_t)p.splits * n * q_heads * (kv.head_dim + 2) * 4;
+  if (p.splits == 1) return 0;
+  const int64_t rows = split_shape(kv, q_heads, n) ? (int64_t)p.blocks * 64 : (int64_t)p.splits * n * q_heads;
+  return rows * (kv.head_dim + 2) * 4;
 }
 
 hipError_t launch_attn(const AttnArgs &a, hipStream_t s) {
   const Plan p = make_plan(a.kv, a.q_heads, a.n);
-  const bool split = split_shape(a.kv, a.q_heads, a.n), fp8 = a.kv.elem == OES_ELEM_E4M3;
-  const int64_t blocks = (int64_t)p.tiles * a.kv.kv_heads * p.splits;
-  if (blocks > 0x7fffffff || (int64_t)a.n * a.q_heads > 0x7fffffff) return hipErrorInvalidConfiguration;
-  const int dp = a.kv.head_dim <= 64 ? 64 : (a.kv.head_dim <= 128 ? 128 : 256);
-  hipError_t e = hipSuccess;
-#define OES_ATTN(DPV)                                                                                             \
-  e = split ? (fp8 ? launch_shape<DPV, true, false>(a, p, (uint32_t)blocks, s)                                    \
-                   : launch_shape<DPV, false, false>(a, p, (uint32_t)blocks, s))                                  \
-            : (fp8 ? launch_shape<DPV, true, true>(a, p, (uint32_t)blocks, s)                                     \
-                   : launch_shape<DPV, false, true>(a, p, (uint32_t)blocks, s))
-  if (dp == 64)
-    OES_ATTN(64);
-  else if (dp == 128)
-    OES_ATTN(128);
-  else
-    OES_ATTN(256);
-#undef OES_ATTN
+  const bool split = split_shape(a.kv, a.q_heads, a.n);
+  const int64_t cap = (int64_t)a.kv.max_pages * a.kv.page_size;
+  const int64_t blocks = split ? p.blocks : (int64_t)p.tiles * a.kv.kv_heads * p.splits;
+  if (blocks > 0x7fffffff || (int64_t)a.n * a.q_heads > 0x7fffffff || (int64_t)p.tiles * a.kv.kv_heads * (cap / 64 + 2) > 0x7fffffff)
+    return hipErrorInvalidConfiguration;
+  const int dp = head_pad(a.kv);
+  const hipError_t e = dp == 64 ? launch_dim<64>(a, p, split, (uint32_t)blocks, s)
+                                : (dp == 128 ? launch_dim<128>(a, p, split, (uint32_t)blocks, s) : launch_dim<256>(a, p, split, (uint32_t)blocks, s));
   if (e != hipSuccess || p.splits == 1) return e;
-  hipLaunchKernelGGL(attn_merge_kernel, dim3((uint32_t)(a.n * a.q_heads)), dim3(256), 0, s, a, p);
+  const dim3 g((uint32_t)(a.n * a.q_heads)), b(256);
+  if (split)
+    hipLaunchKernelGGL(attn_merge_kernel<false>, g, b, 0, s, a, p);
+  else
+    hipLaunchKernelGGL(attn_merge_kernel<true>, g, b, 0, s, a, p);
   return hipGetLastError();
 }
 
