@@ -98,7 +98,8 @@ struct Plan {
   int tile_tokens;   // tokens of a tile
   int tiles;         // tiles of all sequences, at most
   int splits;        // TILE: parts of the entries, at most
-  int chunk;         // TILE: entries of a part; SPLIT: entries of a unit
+  int chunk;         // TILE: entries of a part; SPLIT: entries of a unit, 1 << chunk_log
+  int chunk_log;     // TILE: -1
   int blocks;        // SPLIT: workgroups
 };
 
@@ -116,18 +117,22 @@ __device__ inline void tile_entries(const AttnArgs &a, const Plan &p, Tile &t) {
   kv_seen(t.len, t.rows, t.t0, a.window, &t.lo, &t.hi_first);
   kv_seen(t.len, t.rows, t.t0 + t.tokens - 1, a.window, &t.lo_last, &t.hi);
   t.base = t.lo & ~31;
-  t.parts = t.hi > t.base ? (t.hi - t.base + p.chunk - 1) / p.chunk : 1;
+  const int span = t.hi - t.base + p.chunk - 1;
+  t.parts = t.hi > t.base ? (p.chunk_log >= 0 ? span >> p.chunk_log : span / p.chunk) : 1;
 }
 
 __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ inline int scan64(int v) {  // inclusive, over the wave
-  const int lane = threadIdx.x & 63;
-  for (int d = 1; d < 64; d <<= 1) {
-    const int u = __shfl_up(v, d, 64);
-    if (lane >= d) v += u;
-  }
+// Inclusive sum over the lanes up to this one: within rows of 16, then across them.
+__device__ inline int scan64(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // lane 15 to row 1, lane 47 to row 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // lane 31 to rows 2 and 3
   return v;
 }
+__device__ inline int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
 // The lane's sequence b0 + lane: rows, entries; 0 where there is none.
 __device__ inline void lane_sequence(const AttnArgs &a, int b0, int *first, int *rows, int *len) {
@@ -141,10 +146,10 @@ __device__ inline void lane_sequence(const AttnArgs &a, int b0, int *first, int 
   }
 }
 __device__ inline void take_sequence(Tile &t, int b0, int w, int first, int rows, int len) {
-  t.b = uniform(b0 + w);
-  t.first = uniform(__shfl(first, w, 64));
-  t.rows = uniform(__shfl(rows, w, 64));
-  t.len = uniform(__shfl(len, w, 64));
+  t.b = b0 + w;
+  t.first = lane_value(first, w);
+  t.rows = lane_value(rows, w);
+  t.len = lane_value(len, w);
 }
 
 // Tile `idx` in the order of the sequences (wave-wide; the same answer in every lane).
@@ -156,16 +161,21 @@ __device__ inline bool find_tile(const AttnArgs &a, const Plan &p, int idx, Tile
     const int mine = (rows + p.tile_tokens - 1) / p.tile_tokens, upto = before + scan64(mine);
     const uint64_t hit = __ballot(upto > idx && upto - mine <= idx);
     if (hit) {
-      const int w = __builtin_ctzll(hit);
+      const int w = uniform(__builtin_ctzll(hit));
       take_sequence(t, b0, w, first, rows, len);
-      t.t0 = uniform((idx - __shfl(upto - mine, w, 64)) * p.tile_tokens);
+      t.t0 = (idx - lane_value(upto - mine, w)) * p.tile_tokens;
       tile_entries(a, p, t);
       return true;
     }
-    before = uniform(__shfl(upto, 63, 64));
+    before = lane_value(upto, 63);
   }
   return false;
 }
+
+// A (tile, head) pair costs a workgroup about as much as kBegin units before its first one (rows, pages, a
+// latency each, and the joining of the waves), so it counts as kBegin + parts units, the first kBegin without
+// entries.
+constexpr int kBegin = 4;
 
 // Units of a sequence, over its tiles and all cache heads.
 __device__ inline int sequence_units(const AttnArgs &a, const Plan &p, int rows, int len) {
@@ -175,39 +185,47 @@ __device__ inline int sequence_units(const AttnArgs &a, const Plan &p, int rows,
   t.len = len;
   for (t.t0 = 0; t.t0 < rows; t.t0 += p.tile_tokens) {
     tile_entries(a, p, t);
-    sum += t.parts;
+    sum += kBegin + t.parts;
   }
   return sum * a.kv.kv_heads;
 }
 
-// SPLIT's order of units: sequence, tile, head, entries.  Where unit `u` stands: its tile, head and place `x`
-// among the tile's units; *total: all units.  (u < 0: only the total.)  Wave-wide.
-__device__ inline bool find_unit(const AttnArgs &a, const Plan &p, int u, Tile &t, int *g, int *x, int *total) {
-  int before = 0;
-  bool found = false;
+// SPLIT's order of units: sequence, tile, head, entries.  The lane's sequence of the first 64, kept over the calls.
+struct Scan {
+  int first, rows, len, mine, upto;
+};
+__device__ inline Scan scan_sequences(const AttnArgs &a, const Plan &p, int b0, int before) {
+  Scan s;
+  lane_sequence(a, b0, &s.first, &s.rows, &s.len);
+  s.mine = sequence_units(a, p, s.rows, s.len);
+  s.upto = before + scan64(s.mine);
+  return s;
+}
+__device__ inline int all_units(const AttnArgs &a, const Plan &p, const Scan &s0) {
+  int total = lane_value(s0.upto, 63);
+  for (int b0 = 64; b0 < a.kv.batch; b0 += 64) total = lane_value(scan_sequences(a, p, b0, total).upto, 63);
+  return total;
+}
+// Where unit `u` (there is one) stands: its tile, head and place `x` among the pair's units.  Wave-wide.
+__device__ inline void find_unit(const AttnArgs &a, const Plan &p, const Scan &s0, int u, Tile &t, int *g, int *x) {
+  Scan s = s0;
   for (int b0 = 0; b0 < a.kv.batch; b0 += 64) {
-    int first, rows, len;
-    lane_sequence(a, b0, &first, &rows, &len);
-    const int mine = sequence_units(a, p, rows, len), upto = before + scan64(mine);
-    const uint64_t hit = __ballot(upto > u && upto - mine <= u);
-    if (hit) {
-      const int w = __builtin_ctzll(hit);
-      take_sequence(t, b0, w, first, rows, len);
-      int left = uniform(u - __shfl(upto - mine, w, 64));
-      for (t.t0 = 0;; t.t0 += p.tile_tokens) {
-        tile_entries(a, p, t);
-        if (left < t.parts * a.kv.kv_heads) break;
-        left -= t.parts * a.kv.kv_heads;
-      }
-      *g = left / t.parts;
-      *x = left - *g * t.parts;
-      found = true;
-      if (!total) return true;
+    if (b0) s = scan_sequences(a, p, b0, lane_value(s.upto, 63));
+    const uint64_t hit = __ballot(s.upto > u && s.upto - s.mine <= u);
+    if (!hit) continue;
+    const int w = uniform(__builtin_ctzll(hit));
+    take_sequence(t, b0, w, s.first, s.rows, s.len);
+    int left = u - lane_value(s.upto - s.mine, w);
+    for (t.t0 = 0;; t.t0 += p.tile_tokens) {
+      tile_entries(a, p, t);
+      const int all = (kBegin + t.parts) * a.kv.kv_heads;
+      if (left < all) break;
+      left -= all;
     }
-    before = uniform(__shfl(upto, 63, 64));
+    *g = left / (kBegin + t.parts);
+    *x = left - *g * (kBegin + t.parts);
+    return;
   }
-  if (total) *total = before;
-  return found;
 }
 // units of a workgroup
 __device__ inline int unit_share(const Plan &p, int total) { return (total + p.blocks - 1) / p.blocks; }
@@ -248,7 +266,7 @@ __global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8,
   __shared__ float jm[4][32], jl[4][32];
   __shared__ int odd_sm;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c = lane & 31, half = lane >> 5;
-  const int D = a.kv.head_dim, G = a.q_heads / a.kv.kv_heads, shift = kv_shift(a.kv.page_size);
+  const int D = a.kv.head_dim, G = a.q_heads / a.kv.kv_heads, shift = a.shift;
   const float cs = a.scale * a.kv.k_scale * kLog2e;
 
   // ---- lane constants of the staging
@@ -262,16 +280,19 @@ __global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8,
   // and an offset that the lane keeps (with an address of its own per lane and load, the long chunk of 2048 tokens
   // at 24111 entries took 1.29 ms; see below).  Page numbers are read a tile ahead, through the scalar cache.
   const bool paged16 = shift >= 4 && D == DP && (a.kv.k_row | a.kv.v_row) < (1 << 22);
+  // (FP8: neighbouring lanes take different rows, whose bf16 chunks go to different banks)
+  auto lane_row = [](int ln) { return FP8 ? ln % RPI : ln / CPR; };
   uint32_t k_lane[LG], v_lane[LG];
 #pragma unroll
   for (int i = 0; i < LG; ++i) {
-    const int row = i * RPI + lane / CPR, ch = FP8 ? lane % CPR : (lane % CPR) ^ swizzle<DP>(row);
+    const int row = i * RPI + lane_row(lane), ch = FP8 ? lane / RPI : (lane % CPR) ^ swizzle<DP>(row);
     k_lane[i] = (uint32_t)(row * a.kv.k_row) * es + ch * 16;
     v_lane[i] = (uint32_t)(row * a.kv.v_row) * es + ch * 16;
   }
 
   // ---- what this workgroup goes over: one part of a pair (TILE), or its share of the units (SPLIT)
   Tile t;
+  Scan scan = {};
   int g = 0, split = 0, unit = 0, unit_end = 0;
   if (TILE) {
     // heads are the fastest index: neighbouring workgroups, on different XCDs, take different heads, so that an
@@ -283,12 +304,12 @@ __global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8,
     if (!find_tile(a, plan, plan.tiles - 1 - (id - split * plan.tiles), t) || split >= t.parts) return;
     if (threadIdx.x == 0) odd_sm = 0;
   } else {
-    int total, x;
-    find_unit(a, plan, -1, t, &g, &x, &total);
-    const int share = unit_share(plan, total);
+    scan = scan_sequences(a, plan, 0, 0);
+    const int total = all_units(a, plan, scan), share = unit_share(plan, total);
     unit = min((int64_t)blockIdx.x * share, (int64_t)total);
     unit_end = min((int64_t)unit + share, (int64_t)total);
     if (unit >= unit_end) return;
+    g = a.kv.kv_heads;
   }
   do {
     int from, to, x = 0;
@@ -298,12 +319,17 @@ __global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8,
       to = min(t.hi, from + plan.chunk);
       direct = t.parts == 1;
     } else {
-      find_unit(a, plan, unit, t, &g, &x, nullptr);
-      const int n = min(t.parts - x, unit_end - unit);
-      from = t.base + x * plan.chunk;
-      to = min(t.hi, from + n * plan.chunk);
-      direct = n == t.parts;
+      if (++g < a.kv.kv_heads)
+        x = 0;   // the same tile's next head
+      else
+        find_unit(a, plan, scan, unit, t, &g, &x);
+      const int n = min(kBegin + t.parts - x, unit_end - unit), x1 = x + n - kBegin;
       unit += n;
+      if (x1 <= 0) break;   // the share ends before the pair's first entries
+      x = max(0, x - kBegin);
+      from = t.base + x * plan.chunk;
+      to = min(t.hi, t.base + x1 * plan.chunk);
+      direct = x == 0 && x1 == t.parts;
     }
     const int32_t *table = a.kv.table + t.b * a.kv.table_stride;
     typedef __attribute__((address_space(4))) const int32_t const_i32;
@@ -389,7 +415,7 @@ __global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8,
       }
 #pragma unroll
       for (int i = 0; i < LD; ++i) {
-        const int row = wave * own0 + i * RPI + ln / CPR, ch = FP8 ? ln % CPR : (ln % CPR) ^ swizzle<DP>(row);
+        const int row = wave * own0 + i * RPI + lane_row(ln), ch = FP8 ? ln / RPI : (ln % CPR) ^ swizzle<DP>(row);
         const int pg = __shfl(page, row, 64), ip = __shfl(in_page, row, 64);
         const uint8_t *ks = reinterpret_cast<const uint8_t *>(zero_chunk), *vs = ks;
         if (pg >= 0 && ch * 16 < D * es) {
@@ -410,7 +436,7 @@ __global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8,
     auto store = [&](int buf) {  // FP8: the staged registers to LDS as bf16
 #pragma unroll
       for (int i = 0; i < (FP8 ? LD : 0); ++i) {
-        const int row = wave * own0 + i * RPI + lane / CPR, q2 = 2 * (lane % CPR);
+        const int row = wave * own0 + i * RPI + lane_row(lane), q2 = 2 * (lane / RPI);
         uint8_t *dst = tiles + buf * 2 * S::tile_bytes + row * DP * 2;
         const int c0 = (q2 ^ swizzle<DP>(row)) * 16, c1 = ((q2 + 1) ^ swizzle<DP>(row)) * 16;
 #pragma unroll
@@ -705,12 +731,12 @@ __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a, Plan plan) 
     const int mine = TILE ? 0 : sequence_units(a, plan, rows, len), upto = before + scan64(mine);
     const uint64_t hit = __ballot(row >= first && row < first + rows);
     if (hit && t.b < 0) {
-      const int w = __builtin_ctzll(hit);
+      const int w = uniform(__builtin_ctzll(hit));
       take_sequence(t, b0, w, first, rows, len);
-      start = __shfl(upto - mine, w, 64);
+      start = lane_value(upto - mine, w);
       if (TILE) break;
     }
-    before = __shfl(upto, 63, 64);
+    before = lane_value(upto, 63);
   }
   total = before;
   if (t.b < 0) return;
@@ -718,7 +744,7 @@ __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a, Plan plan) 
   if (!TILE)
     for (t.t0 = 0; t.t0 < own_t0; t.t0 += plan.tile_tokens) {
       tile_entries(a, plan, t);
-      start += t.parts * a.kv.kv_heads;
+      start += (kBegin + t.parts) * a.kv.kv_heads;
     }
   t.t0 = own_t0;
   tile_entries(a, plan, t);
@@ -726,7 +752,7 @@ __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a, Plan plan) 
   int64_t at0 = (int64_t)row * a.q_heads + h, stride = (int64_t)a.n * a.q_heads;   // TILE: part s at at0 + s * stride
   if (!TILE) {
     const int share = unit_share(plan, total);
-    start += g * t.parts;
+    start += g * (kBegin + t.parts) + kBegin;
     b_first = start / share;
     parts = (start + t.parts - 1) / share - b_first + 1;
     at0 = b_first * 64ll + (row - t.first - t.t0) * G + h - g * G;   // part 0 begins a pair: place 1; the others 0
@@ -808,7 +834,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void weigh_kernel(AttnArgs 
   const int r0 = i0 * G, r1 = i1 * G;
 
   // keys of this wave
-  const int shift = kv_shift(a.kv.page_size);
+  const int shift = a.shift;
   const int32_t *table = a.kv.table + b * a.kv.table_stride;
   const int ew = e0 + wave * 32 * KT;
   bf16x8 key[KT][KS];
@@ -934,15 +960,17 @@ Plan make_plan(const oes_kv &kv, int q_heads, int n) {
   const int G = q_heads / kv.kv_heads, dp = head_pad(kv);
   const bool split = split_shape(kv, q_heads, n), fp8 = kv.elem == OES_ELEM_E4M3;
   Plan p = {};
+  p.chunk_log = -1;
   p.tile_tokens = (split ? 32 : 128) / G;
   // every sequence with rows has at most one tile that is not full
   const int64_t tiles = std::min<int64_t>(n, ((int64_t)n + (int64_t)kv.batch * (p.tile_tokens - 1)) / p.tile_tokens);
   p.tiles = (int)tiles;
   const int64_t cap = ((int64_t)kv.max_pages * kv.page_size + 31) / 32 * 32 + 32;   // entries of a tile, from its base
   if (split) {
-    p.chunk = 32 * (dp == 256 ? 2 : 4);
+    p.chunk_log = dp == 256 ? 6 : 7;   // 32 entries a wave
+    p.chunk = 1 << p.chunk_log;
     // as many workgroups as are resident at once: LDS holds two to a CU, or one of the bf16 cache's 128 KiB
-    p.blocks = (int)std::min<int64_t>(dp == 64 || (fp8 && dp == 128) ? 512 : 256, tiles * kv.kv_heads * ((cap + p.chunk - 1) / p.chunk));
+    p.blocks = (int)std::min<int64_t>(dp == 64 || (fp8 && dp == 128) ? 512 : 256, tiles * kv.kv_heads * (kBegin + (cap + p.chunk - 1) / p.chunk));
     p.splits = cap <= p.chunk ? 1 : 2;
   } else {
     const int64_t parts = std::max<int64_t>(1, 512 / (tiles * kv.kv_heads));
@@ -975,12 +1003,14 @@ int64_t attn_workspace_bytes(const oes_kv &kv, int q_heads, int n) {
   return rows * (kv.head_dim + 2) * 4;
 }
 
-hipError_t launch_attn(const AttnArgs &a, hipStream_t s) {
+hipError_t launch_attn(const AttnArgs &args, hipStream_t s) {
+  AttnArgs a = args;
+  a.shift = kv_shift(a.kv.page_size);
   const Plan p = make_plan(a.kv, a.q_heads, a.n);
   const bool split = split_shape(a.kv, a.q_heads, a.n);
   const int64_t cap = (int64_t)a.kv.max_pages * a.kv.page_size;
   const int64_t blocks = split ? p.blocks : (int64_t)p.tiles * a.kv.kv_heads * p.splits;
-  if (blocks > 0x7fffffff || (int64_t)a.n * a.q_heads > 0x7fffffff || (int64_t)p.tiles * a.kv.kv_heads * (cap / 64 + 2) > 0x7fffffff)
+  if (blocks > 0x7fffffff || (int64_t)a.n * a.q_heads > 0x7fffffff || (int64_t)p.tiles * a.kv.kv_heads * (cap / 64 + 2 + kBegin) > 0x7fffffff)
     return hipErrorInvalidConfiguration;
   const int dp = head_pad(a.kv);
   const hipError_t e = dp == 64 ? launch_dim<64>(a, p, split, (uint32_t)blocks, s)
@@ -1008,7 +1038,9 @@ hipError_t launch_weigh(const AttnArgs &a, hipStream_t s) {
 }
 }  // namespace
 
-hipError_t launch_attn_weigh(const AttnArgs &a, hipStream_t s) {
+hipError_t launch_attn_weigh(const AttnArgs &args, hipStream_t s) {
+  AttnArgs a = args;
+  a.shift = kv_shift(a.kv.page_size);
   if (a.kv.head_dim <= 64) return launch_weigh<64>(a, s);
   if (a.kv.head_dim <= 128) return launch_weigh<128>(a, s);
   return launch_weigh<256>(a, s);

@@ -163,6 +163,7 @@ struct AttnArgs {
   float *ws;               // attn: partial sums of the splits
   float *acc;              // weigh
   int64_t acc_stride;
+  int32_t shift;           // log2 of the page size, or -1 (set by the launches)
 };
 int64_t attn_workspace_bytes(const oes_kv &kv, int q_heads, int n);
 hipError_t launch_attn(const AttnArgs &a, hipStream_t s);
