@@ -797,29 +797,31 @@ __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a, Plan plan) 
 
 // ------------------------------------------------------------------ weigh
 // The weights that entries receive: S^T = K Q^T once more, with the row's log-sum-exp known.
-// A wave keeps its 32 KT entries' keys in registers (A operand) and goes over the rows that
-// see any entry of the workgroup, 32 at a time, from LDS; a lane adds up the weights of its
-// row (column) for 16 KT entries, and the 32 rows' sums are joined through LDS at the end.
-// No two workgroups share an entry, so nothing is added atomically.  Bound by the
-// exponentials (one for each entry, row pair; 16 cycles per 64) rather than by the product.
-template <int DP>
+// A workgroup goes over the rows that see any of its 128 entries, 64 RG at a time, from LDS.  Wave
+// (e, x) keeps the keys of 32 entries in registers (A operand) and takes 64 of the rows:
+// a lane adds up the weights of its rows (columns) for 16 entries, and the sums of the lanes and
+// of the RG waves are joined through LDS at the end.  No two workgroups share an entry, so
+// nothing is added atomically.  Bound by the exponentials (one
+// for each entry, row pair, with a multiply-add and an add) rather than by the product.
+// RG = 2 where there are more rows; with RG = 1 the whole of 1000 new tokens took 196 us where 2 takes 128.
+template <int DP, int RG>
 struct WeighShape {
-  static constexpr int kt = DP == 256 ? 1 : 2;
-  static constexpr int entries = 4 * 32 * kt;
-  static constexpr int tile_bytes = 32 * DP * 2;
+  static constexpr int entries = 4 * 32, rows = 64 * RG, threads = 256 * RG;
+  static constexpr int tile_bytes = rows * DP * 2;
 };
 
-template <int DP, bool FP8>
-__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void weigh_kernel(AttnArgs a, int blocks_per_seq) {
-  using S = WeighShape<DP>;
-  constexpr int KT = S::kt, KS = DP / 16, CPR = DP / 8, RPI = 64 / CPR, LD = 8 / RPI;
-  __shared__ __attribute__((aligned(16))) uint8_t sm[2 * S::tile_bytes > 4 * 32 * 33 * 4 ? 2 * S::tile_bytes : 4 * 32 * 33 * 4];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 31, half = lane >> 5;
+template <int DP, bool FP8, int RG>
+__global__ __launch_bounds__(256 * RG, DP == 64 ? 4 : 2) void weigh_kernel(AttnArgs a) {
+  using S = WeighShape<DP, RG>;
+  constexpr int KS = DP / 16, CPR = DP / 8, RPI = 64 / CPR, LD = 16 / RPI;
+  __shared__ __attribute__((aligned(16))) uint8_t sm[2 * S::tile_bytes > RG * 128 * 33 * 4 ? 2 * S::tile_bytes : RG * 128 * 33 * 4];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c = lane & 31, half = lane >> 5;
   const int D = a.kv.head_dim, G = a.q_heads / a.kv.kv_heads;
   int id = blockIdx.x;
   const int g = id % a.kv.kv_heads;
   id /= a.kv.kv_heads;
-  const int b = id / blocks_per_seq, e0 = (id - b * blocks_per_seq) * S::entries;
+  // then the sequences, then the entries: a sequence's first entries, which most rows see, start first
+  const int e0 = id / a.kv.batch * S::entries, b = id - e0 / S::entries * a.kv.batch;
   bool bad = false;
   const int len = kv_len(a.kv, a.kv.len[b], &bad);
   int first;
@@ -831,23 +833,18 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void weigh_kernel(AttnArgs 
   const int i0 = max(0, e0 - before);
   const int i1 = a.window > 0 ? (int)min((int64_t)rows, (int64_t)e1 - 1 + a.window - before) : rows;
   if (i0 >= i1) return;
-  const int r0 = i0 * G, r1 = i1 * G;
-
   // keys of this wave
-  const int shift = a.shift;
-  const int32_t *table = a.kv.table + b * a.kv.table_stride;
-  const int ew = e0 + wave * 32 * KT;
-  bf16x8 key[KT][KS];
-  uint64_t paged = 0;
-#pragma unroll
-  for (int kt = 0; kt < KT; ++kt) {
-    const int j = ew + 32 * kt + c;
+  const int ew = e0 + (wave & 3) * 32, rw = (wave >> 2) * 64;
+  bf16x8 key[KS];
+  uint32_t paged;
+  {
+    const int j = ew + c;
     int ip = 0, page = -1;
     if (j < len) {
-      page = kv_page(a.kv, table, shift, j, &ip);
+      page = kv_page(a.kv, a.kv.table + b * a.kv.table_stride, a.shift, j, &ip);
       if (page < 0) raise_status(a.kv);
     }
-    paged |= (__ballot(page >= 0) & 0xffffffffull) << (32 * kt);
+    paged = (uint32_t)__ballot(page >= 0);
     const int64_t off = kv_k_off(a.kv, max(page, 0), ip) + a.kv.k_head * g + 8 * half;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -860,92 +857,127 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void weigh_kernel(AttnArgs 
           w = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.kv.k) + off + 16 * ks);
         }
       }
-      key[kt][ks] = __builtin_bit_cast(bf16x8, w);
+      key[ks] = __builtin_bit_cast(bf16x8, w);
     }
   }
-  float acc[KT][16];
+  float acc[16];
 #pragma unroll
-  for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[kt][i] = 0.f;
+  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
   const float cs = a.scale * a.kv.k_scale * kLog2e;
 
-  // 32 rows to LDS: wave w stages rows 8 w .. 8 w + 7
-  auto issue = [&](int r, int buf) {
+  // A tile holds the G heads of T = 64 RG / G tokens, so a lane's (token, head) within it is the same in every tile:
+  // its addresses are a scalar base and a constant offset.  Rows of LDS past T G stay zero.
+  const int T = S::rows / G;
+  // rows to LDS: wave w stages rows 16 w .. 16 w + 15
+  uint32_t st_off[LD];
+  int st_tok[LD];
 #pragma unroll
-    for (int i = 0; i < LD; ++i) {
-      const int row = 8 * wave + i * RPI + lane / CPR, ch = (lane % CPR) ^ swizzle<DP>(row), rr = r + row;
-      const int tok = rr / G;
-      const uint16_t *src = reinterpret_cast<const uint16_t *>(zero_chunk);
-      if (rr < r1 && ch * 8 < D) src = a.q.p + (int64_t)(first + tok) * a.q.row + (g * G + rr - tok * G) * a.q.head + ch * 8;
-      load_to_lds(src, __builtin_amdgcn_readfirstlane(lds_addr(sm + buf * S::tile_bytes + (8 * wave + i * RPI) * DP * 2)));
+  for (int i = 0; i < LD; ++i) {
+    const int row = 16 * wave + i * RPI + lane / CPR, ch = (lane % CPR) ^ swizzle<DP>(row), tok = row / G;
+    st_off[i] = (uint32_t)((tok * a.q.row + (g * G + row - tok * G) * a.q.head + ch * 8) * 2);
+    st_tok[i] = ch * 8 < D ? tok : 1 << 30;   // chunks behind head_dim: never a token
+  }
+  const bool near = 129 * a.q.row + (int64_t)a.q_heads * a.q.head < (1ll << 31);   // offsets of 32 bits do
+  int ls_tok[2];
+  uint32_t ls_off[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int row = rw + 32 * x + c;
+    ls_tok[x] = row / G;
+    ls_off[x] = ls_tok[x] * a.q_heads + g * G + row - ls_tok[x] * G;
+    if (row >= T * G) ls_tok[x] = 1 << 30;
+  }
+#pragma unroll
+  for (int i = 0; i < 2 * S::tile_bytes / 16 / S::threads; ++i) *reinterpret_cast<u32x4 *>(sm + (i * S::threads + threadIdx.x) * 16) = u32x4{0, 0, 0, 0};
+  __syncthreads();
+  auto issue = [&](int i, int buf) {  // the tile from token i on
+    const uint16_t *base = a.q.p + (int64_t)(first + i) * a.q.row;
+#pragma unroll
+    for (int x = 0; x < LD; ++x) {
+      const uint32_t lds = uniform(lds_addr(sm + buf * S::tile_bytes + (16 * wave + x * RPI) * DP * 2));
+      if (near && i + T <= i1) {
+        if (st_tok[x] < T) load_to_lds(base, st_off[x], lds);
+      } else {  // a last tile with fewer tokens: zeros behind them
+        const int row = 16 * wave + x * RPI + lane / CPR, ch = (lane % CPR) ^ swizzle<DP>(row), tok = row / G;
+        const uint16_t *src = base + tok * a.q.row + (g * G + row - tok * G) * a.q.head + ch * 8;
+        if (st_tok[x] >= T || i + st_tok[x] >= i1) src = reinterpret_cast<const uint16_t *>(zero_chunk);
+        load_to_lds(src, lds);
+      }
     }
   };
-  auto row_lse = [&](int r) {
-    const int rr = r + c, tok = rr / G;
-    return rr < r1 ? a.lse[(int64_t)(first + tok) * a.q_heads + g * G + rr - tok * G] : -INFINITY;
+  float lse[2];
+  auto next_lse = [&](int i) {  // +inf in rows that add nothing: exp(-inf) = 0
+    const float *base = a.lse + (int64_t)(first + i) * a.q_heads;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const bool in = i + ls_tok[x] < i1;
+      const float v = base[in ? ls_off[x] : 0];
+      lse[x] = in && v != -INFINITY ? v : INFINITY;
+    }
   };
-  issue(r0, 0);
-  float lse = row_lse(r0);
+  next_lse(i0);
+  issue(i0, 0);
   int buf = 0;
-  for (int r = r0; r < r1; r += 32) {
+  for (int i = i0; i < i1; i += T) {
     wait_loads<0>();
     __syncthreads();
-    const bool more = r + 32 < r1;
-    const float lse2 = lse * kLog2e;
-    if (more) {
-      lse = row_lse(r + 32);
-      issue(r + 32, buf ^ 1);
+    float l2[2] = {lse[0] * kLog2e, lse[1] * kLog2e};
+    asm volatile("" : "+v"(l2[0]), "+v"(l2[1]));   // here, before the next loads, or it waits for them
+    if (i + T < i1) {
+      next_lse(i + T);
+      issue(i + T, buf ^ 1);
     }
-    f32x16 s[KT];
+    f32x16 s[2];
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
-    const uint8_t *qr = sm + buf * S::tile_bytes + c * DP * 2;
+      for (int e = 0; e < 16; ++e) s[x][e] = 0.f;
+    const uint8_t *qr = sm + buf * S::tile_bytes + (rw + c) * DP * 2;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      const bf16x8 qf = *reinterpret_cast<const bf16x8 *>(qr + ((2 * ks + half) ^ swizzle<DP>(c)) * 16);
+      const int at = ((2 * ks + half) ^ swizzle<DP>(c)) * 16;   // rows c and c + 32 have one swizzle
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) s[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key[kt][ks], qf, s[kt], 0, 0, 0);
+      for (int x = 0; x < 2; ++x)
+        s[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key[ks], *reinterpret_cast<const bf16x8 *>(qr + x * 32 * DP * 2 + at), s[x], 0, 0, 0);
     }
     // every row of this tile sees every entry of the wave, and all entries have pages: no masks
-    const int at0 = before + r / G, at1 = before + min(r + 31, r1 - 1) / G;
-    const bool whole = r + 32 <= r1 && at0 >= ew + 32 * KT - 1 && (a.window == 0 || (int64_t)at1 - a.window < ew) &&
-                       paged == (KT == 2 ? ~0ull : 0xffffffffull) && !__any(lse2 == -INFINITY);
-    if (whole) {
+    const int last_tok = min(i + T, i1) - 1;
+    if (before + i >= ew + 31 && (a.window == 0 || before + last_tok - a.window < ew) && paged == ~0u) {
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[kt][i] += __builtin_amdgcn_exp2f(fmaf(s[kt][i], cs, -lse2));
+      for (int e = 0; e < 16; ++e)
+        acc[e] += __builtin_amdgcn_exp2f(fmaf(s[0][e], cs, -l2[0])) + __builtin_amdgcn_exp2f(fmaf(s[1][e], cs, -l2[1]));
     } else {
-      int lo = 0, hi = 0;
-      if (r + c < r1 && lse2 != -INFINITY) kv_seen(len, rows, (r + c) / G, a.window, &lo, &hi);
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
+      for (int x = 0; x < 2; ++x) {
+        asm volatile("");   // (or the compiler makes selects of this, in every tile)
+        int lo = 0, hi = 0;
+        if (l2[x] != INFINITY) kv_seen(len, rows, i + ls_tok[x], a.window, &lo, &hi);
+        const int lo_at = lo - ew - 4 * half, hi_at = hi - ew - 4 * half;
+        const uint32_t bits = paged >> (4 * half);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int e = kt * 32 + 8 * (i / 4) + 4 * half + i % 4, j = ew + e;
-          if (j >= lo && j < hi && ((paged >> e) & 1)) acc[kt][i] += __builtin_amdgcn_exp2f(fmaf(s[kt][i], cs, -lse2));
+        for (int y = 0; y < 16; ++y) {
+          const int e = 8 * (y / 4) + y % 4;
+          if (e >= lo_at && e < hi_at && ((bits >> e) & 1)) acc[y] += __builtin_amdgcn_exp2f(fmaf(s[x][y], cs, -l2[x]));
         }
+      }
     }
     buf ^= 1;
   }
-  // join the rows: 32 entries x 32 rows (padded) of every wave at a time
-  float *join = reinterpret_cast<float *>(sm) + wave * 32 * 33;
+  // join the rows: 32 entries x 32 columns (padded) of every wave
+  float *join = reinterpret_cast<float *>(sm);
+  __syncthreads();
 #pragma unroll
-  for (int kt = 0; kt < KT; ++kt) {
-    __syncthreads();
+  for (int i = 0; i < 16; ++i) join[(wave * 32 + 8 * (i / 4) + 4 * half + i % 4) * 33 + c] = acc[i];
+  __syncthreads();
+  if (wave >= 4) return;
+  float sum = 0.f;   // lane (c, half): entry c, columns 16 half .. + 15 of its RG waves
 #pragma unroll
-    for (int i = 0; i < 16; ++i) join[(8 * (i / 4) + 4 * half + i % 4) * 33 + c] = acc[kt][i];
-    __syncthreads();
-    float sum = 0.f;   // lane (c, half): entry c, rows 16 half .. + 15
+  for (int x = 0; x < 16; ++x)
 #pragma unroll
-    for (int x = 0; x < 16; ++x) sum += join[c * 33 + 16 * half + x];
-    sum = sum_halves(sum);
-    const int j = ew + 32 * kt + c;
-    if (half == 0 && j < len && ((paged >> (32 * kt + c)) & 1)) a.acc[((int64_t)b * a.kv.kv_heads + g) * a.acc_stride + j] += sum;
-  }
+    for (int y = 0; y < RG; ++y) sum += join[((wave + 4 * y) * 32 + c) * 33 + 16 * half + x];
+  sum = sum_halves(sum);
+  const int j = ew + c;
+  if (half == 0 && j < len && ((paged >> c) & 1)) a.acc[((int64_t)b * a.kv.kv_heads + g) * a.acc_stride + j] += sum;
 }
 
 bool split_shape(const oes_kv &kv, int q_heads, int n) {
@@ -1025,15 +1057,15 @@ hipError_t launch_attn(const AttnArgs &args, hipStream_t s) {
 }
 
 namespace {
-template <int DP>
+template <int DP, bool FP8>
 hipError_t launch_weigh(const AttnArgs &a, hipStream_t s) {
-  const int64_t cap = (int64_t)a.kv.max_pages * a.kv.page_size, per = (cap + WeighShape<DP>::entries - 1) / WeighShape<DP>::entries;
-  const int64_t blocks = per * a.kv.kv_heads * a.kv.batch;
+  const int64_t cap = (int64_t)a.kv.max_pages * a.kv.page_size, blocks = (cap + 127) / 128 * a.kv.kv_heads * a.kv.batch;
   if (blocks > 0x7fffffff || (int64_t)a.n * a.q_heads > 0x7fffffff) return hipErrorInvalidConfiguration;
-  if (a.kv.elem == OES_ELEM_E4M3)
-    hipLaunchKernelGGL((weigh_kernel<DP, true>), dim3((uint32_t)blocks), dim3(256), 0, s, a, (int)per);
+  const int G = a.q_heads / a.kv.kv_heads;
+  if (G <= 64 && (int64_t)a.n * G <= 64ll * a.kv.batch)
+    hipLaunchKernelGGL((weigh_kernel<DP, FP8, 1>), dim3((uint32_t)blocks), dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((weigh_kernel<DP, false>), dim3((uint32_t)blocks), dim3(256), 0, s, a, (int)per);
+    hipLaunchKernelGGL((weigh_kernel<DP, FP8, 2>), dim3((uint32_t)blocks), dim3(512), 0, s, a);
   return hipGetLastError();
 }
 }  // namespace
@@ -1041,9 +1073,10 @@ hipError_t launch_weigh(const AttnArgs &a, hipStream_t s) {
 hipError_t launch_attn_weigh(const AttnArgs &args, hipStream_t s) {
   AttnArgs a = args;
   a.shift = kv_shift(a.kv.page_size);
-  if (a.kv.head_dim <= 64) return launch_weigh<64>(a, s);
-  if (a.kv.head_dim <= 128) return launch_weigh<128>(a, s);
-  return launch_weigh<256>(a, s);
+  const bool fp8 = a.kv.elem == OES_ELEM_E4M3;
+  if (a.kv.head_dim <= 64) return fp8 ? launch_weigh<64, true>(a, s) : launch_weigh<64, false>(a, s);
+  if (a.kv.head_dim <= 128) return fp8 ? launch_weigh<128, true>(a, s) : launch_weigh<128, false>(a, s);
+  return fp8 ? launch_weigh<256, true>(a, s) : launch_weigh<256, false>(a, s);
 }
 
 }  // namespace oes
