@@ -803,16 +803,17 @@ __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a, Plan plan) 
 // of the RG waves are joined through LDS at the end.  No two workgroups share an entry, so
 // nothing is added atomically.  Bound by the exponentials (one
 // for each entry, row pair, with a multiply-add and an add) rather than by the product.
-// RG = 2 where there are more rows; with RG = 1 the whole of 1000 new tokens took 196 us where 2 takes 128.
-template <int DP, int RG>
+// (With one wave for 32 entries the 8111 entries of 8 heads and 1000 new tokens took 196 us, with two 125.)
+constexpr int RG = 2;
+template <int DP>
 struct WeighShape {
   static constexpr int entries = 4 * 32, rows = 64 * RG, threads = 256 * RG;
   static constexpr int tile_bytes = rows * DP * 2;
 };
 
-template <int DP, bool FP8, int RG>
+template <int DP, bool FP8>
 __global__ __launch_bounds__(256 * RG, DP == 64 ? 4 : 2) void weigh_kernel(AttnArgs a) {
-  using S = WeighShape<DP, RG>;
+  using S = WeighShape<DP>;
   constexpr int KS = DP / 16, CPR = DP / 8, RPI = 64 / CPR, LD = 16 / RPI;
   __shared__ __attribute__((aligned(16))) uint8_t sm[2 * S::tile_bytes > RG * 128 * 33 * 4 ? 2 * S::tile_bytes : RG * 128 * 33 * 4];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c = lane & 31, half = lane >> 5;
@@ -980,6 +981,140 @@ __global__ __launch_bounds__(256 * RG, DP == 64 ? 4 : 2) void weigh_kernel(AttnA
   if (half == 0 && j < len && ((paged >> c) & 1)) a.acc[((int64_t)b * a.kv.kv_heads + g) * a.acc_stride + j] += sum;
 }
 
+// The same for few rows a pair (decode steps): a wave takes 32 entries by itself, with its rows, 32 at a time,
+// straight from global memory (every wave of the pair reads the same few); no barrier.  Units of 128 entries are
+// shared out over a fixed number of workgroups, since the start of a workgroup costs some 4 ns of the launch: a grid
+// over (sequence, head, 128 entries of the table's width) took 20 us for 16 sequences of up to 8192 entries, most of
+// it workgroups without entries.
+constexpr int kFewBlocks = 512;
+
+template <int DP, bool FP8>
+__global__ __launch_bounds__(256, DP == 256 ? 2 : 4) void weigh_few_kernel(AttnArgs a) {
+  constexpr int KS = DP / 16;
+  __shared__ float join_sm[4][32 * 33];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c = lane & 31, half = lane >> 5;
+  const int D = a.kv.head_dim, G = a.q_heads / a.kv.kv_heads;
+  const float cs = a.scale * a.kv.k_scale * kLog2e;
+  const int T = 32 / G, tok = c / G;
+  // units of the lane's sequence of the first 64, and their running sum
+  auto units = [&](int rows, int len) { return rows > 0 ? (len + 127) / 128 * a.kv.kv_heads : 0; };
+  Tile t;
+  int first, rows, len;
+  lane_sequence(a, 0, &first, &rows, &len);
+  const int mine0 = units(rows, len), upto0 = scan64(mine0), first0 = first, rows0 = rows, len0 = len;
+  int total = lane_value(upto0, 63);
+  for (int b0 = 64; b0 < a.kv.batch; b0 += 64) {
+    lane_sequence(a, b0, &first, &rows, &len);
+    total += lane_value(scan64(units(rows, len)), 63);
+  }
+  const int share = (total + gridDim.x - 1) / gridDim.x;
+  const int u1 = (int)min((int64_t)total, ((int64_t)blockIdx.x + 1) * share);
+  int g = a.kv.kv_heads, e = 0;
+  t.len = 0;
+  for (int u = min((int64_t)total, (int64_t)blockIdx.x * share); u < u1; ++u) {
+    e += 128;
+    if (e >= t.len) {   // the next head, or the next sequence
+      e = 0;
+      if (++g >= a.kv.kv_heads) {
+        int before = 0;
+        for (int b0 = 0; b0 < a.kv.batch; b0 += 64) {
+          int mine = mine0, upto = upto0;
+          first = first0, rows = rows0, len = len0;
+          if (b0) {
+            lane_sequence(a, b0, &first, &rows, &len);
+            mine = units(rows, len);
+            upto = before + scan64(mine);
+          }
+          const uint64_t hit = __ballot(upto > u && upto - mine <= u);
+          if (hit) {
+            const int w = uniform(__builtin_ctzll(hit));
+            take_sequence(t, b0, w, first, rows, len);
+            const int left = u - lane_value(upto - mine, w), per = (t.len + 127) / 128;
+            g = left / per;
+            e = (left - g * per) * 128;
+            break;
+          }
+          before = lane_value(upto, 63);
+        }
+      }
+    }
+    const int ew = e + wave * 32, before = t.len - t.rows;
+    if (ew >= t.len) continue;
+    const int i0 = max(0, ew - before);
+    const int i1 = a.window > 0 ? (int)min((int64_t)t.rows, (int64_t)min(ew + 32, t.len) - 1 + a.window - before) : t.rows;
+    if (i0 >= i1) continue;
+    const int head = g * G + c - tok * G;
+    u32x4 key[KS];   // FP8: 8 bytes of each
+    uint32_t paged;
+    {
+      const int j = ew + c;
+      int ip = 0, page = -1;
+      if (j < t.len) {
+        page = kv_page(a.kv, a.kv.table + t.b * a.kv.table_stride, a.shift, j, &ip);
+        if (page < 0) raise_status(a.kv);
+      }
+      paged = (uint32_t)__ballot(page >= 0);
+      const int64_t off = kv_k_off(a.kv, max(page, 0), ip) + a.kv.k_head * g + 8 * half;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        key[ks] = u32x4{0, 0, 0, 0};
+        if (page >= 0 && ks * 16 < D) {
+          if (FP8) {
+            const u32x2 v = *reinterpret_cast<const u32x2 *>(static_cast<const uint8_t *>(a.kv.k) + off + 16 * ks);
+            key[ks].x = v.x;
+            key[ks].y = v.y;
+          } else {
+            key[ks] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.kv.k) + off + 16 * ks);
+          }
+        }
+      }
+    }
+    float acc[16];
+#pragma unroll
+    for (int y = 0; y < 16; ++y) acc[y] = 0.f;
+    for (int i = i0; i < i1; i += T) {
+      const bool in = tok < T && i + tok < i1;
+      const int row = t.first + i + (in ? tok : 0), h = in ? head : g * G;   // others: another row's, and masked
+      const float lse = a.lse[(int64_t)row * a.q_heads + h];
+      const uint16_t *qp = a.q.p + row * a.q.row + h * a.q.head + 8 * half;
+      u32x4 q[KS];
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) q[ks] = *reinterpret_cast<const u32x4 *>(qp + (ks * 16 < D ? 16 * ks : 0));
+      f32x16 s;
+#pragma unroll
+      for (int y = 0; y < 16; ++y) s[y] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        u32x4 w = key[ks];
+        if (FP8) w = u32x4{fp8_bf16_pair<false>(w.x), fp8_bf16_pair<true>(w.x), fp8_bf16_pair<false>(w.y), fp8_bf16_pair<true>(w.y)};
+        if (ks * 16 < D)
+          s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, q[ks]), s, 0, 0, 0);
+      }
+      int lo = 0, hi = 0;
+      if (in && lse != -INFINITY) kv_seen(t.len, t.rows, i + tok, a.window, &lo, &hi);
+      const int lo_at = lo - ew - 4 * half, hi_at = hi - ew - 4 * half;
+      const uint32_t bits = paged >> (4 * half);
+      const float l2 = lse * kLog2e;
+#pragma unroll
+      for (int y = 0; y < 16; ++y) {
+        const int x = 8 * (y / 4) + y % 4;
+        if (x >= lo_at && x < hi_at && ((bits >> x) & 1)) acc[y] += __builtin_amdgcn_exp2f(fmaf(s[y], cs, -l2));
+      }
+    }
+    float *join = join_sm[wave];   // the wave's own: its LDS operations run in order
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int y = 0; y < 16; ++y) join[(8 * (y / 4) + 4 * half + y % 4) * 33 + c] = acc[y];
+    __builtin_amdgcn_wave_barrier();
+    float sum = 0.f;
+#pragma unroll
+    for (int y = 0; y < 16; ++y) sum += join[c * 33 + 16 * half + y];
+    sum = sum_halves(sum);
+    const int j = ew + c;
+    if (half == 0 && j < t.len && ((paged >> c) & 1)) a.acc[((int64_t)t.b * a.kv.kv_heads + g) * a.acc_stride + j] += sum;
+  }
+}
+
 bool split_shape(const oes_kv &kv, int q_heads, int n) {
   // SPLIT holds 32 rows; beyond, on average per sequence and cache head, TILE's 128 fill up better
   const int G = q_heads / kv.kv_heads;
@@ -1059,13 +1194,13 @@ hipError_t launch_attn(const AttnArgs &args, hipStream_t s) {
 namespace {
 template <int DP, bool FP8>
 hipError_t launch_weigh(const AttnArgs &a, hipStream_t s) {
+  const bool few = split_shape(a.kv, a.q_heads, a.n);
   const int64_t cap = (int64_t)a.kv.max_pages * a.kv.page_size, blocks = (cap + 127) / 128 * a.kv.kv_heads * a.kv.batch;
   if (blocks > 0x7fffffff || (int64_t)a.n * a.q_heads > 0x7fffffff) return hipErrorInvalidConfiguration;
-  const int G = a.q_heads / a.kv.kv_heads;
-  if (G <= 64 && (int64_t)a.n * G <= 64ll * a.kv.batch)
-    hipLaunchKernelGGL((weigh_kernel<DP, FP8, 1>), dim3((uint32_t)blocks), dim3(256), 0, s, a);
+  if (few)
+    hipLaunchKernelGGL((weigh_few_kernel<DP, FP8>), dim3((uint32_t)std::min<int64_t>(blocks, kFewBlocks)), dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((weigh_kernel<DP, FP8, 2>), dim3((uint32_t)blocks), dim3(512), 0, s, a);
+    hipLaunchKernelGGL((weigh_kernel<DP, FP8>), dim3((uint32_t)blocks), dim3(512), 0, s, a);
   return hipGetLastError();
 }
 }  // namespace
