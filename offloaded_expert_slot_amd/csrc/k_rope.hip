@@ -1,11 +1,19 @@
 // Rotary positions on q and k, with k and v written into the paged cache.
 //
-// One workgroup per token.  Its rot_dim / 2 sines and cosines are formed once, in LDS:
-// the angle pos * freq in fp64, reduced to a fraction of a turn in fp64 (a position of
-// a million keeps 2^-30 of a turn, where an fp32 product would lose 0.06 radians), the
-// sine and cosine of that fraction in fp32.  All heads of the token share them.  Each
-// thread then owns whole pairs, so an in-place call never reads what another thread
-// wrote.
+// Bound by reading and writing the rows once.  A wave takes one token and a part of its
+// heads; the token's rot_dim / 2 sines and cosines are formed once per wave, in LDS: the
+// angle pos * freq in fp64, reduced to a fraction of a turn in fp64 (a position of a million
+// keeps 2^-30 of a turn, where an fp32 product would lose 0.06 radians), the sine and cosine
+// of that fraction in fp32.  An item is 16 values of a head: two 16-byte pieces that hold 8
+// pairs (values i .. i + 7 and their partners, half a rotation away or next to them), or that
+// are copied.  A lane reads both pieces before it writes them, and no other lane touches
+// them, so a call in place is safe.  Where the pairs of the half layout do not fall into whole
+// pieces (rot_dim no multiple of 16), a lane takes single pairs.
+//
+// The number of workgroups is bounded, since starting one costs some 4 ns of the launch: with
+// one for each of 8740 tokens of 80 heads, pair by pair, the launch took 182 us.
+
+#include <algorithm>
 
 #include "layer_device.h"
 #include "oes_internal.h"
@@ -14,97 +22,180 @@ namespace oes {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWaves = 4, kUnroll = 4;
 
-// Where a token's k and v go: sequence and entry, or entry -1 (none) / seq -1 (a row of
-// no sequence).  All threads of a workgroup call it and get the same answer.
+// Where a token's k and v go: sequence (-1: a row of none), and page (-1: no entry).  Wave-wide.
 struct Place {
-  int seq, entry, page, in_page;
+  int seq, page, in_page;
 };
 
-__device__ inline Place find_place(const RopeArgs &a, int t) {
-  __shared__ int found[2];
-  if (threadIdx.x == 0) found[0] = -1;
-  __syncthreads();
-  for (int b = threadIdx.x; b < a.kv.batch; b += kThreads) {
+__device__ inline Place find_place(const RopeArgs &a, int t, int shift) {
+  const int lane = threadIdx.x & 63;
+  Place p = {-1, -1, 0};
+  for (int b0 = 0; b0 < a.kv.batch && p.seq < 0; b0 += 64) {
+    const int b = b0 + lane;
     bool bad = false;
-    int first;
-    const int rows = kv_rows(a.q_start[b], a.q_start[b + 1], a.n, &first, &bad);
+    int first = 0, rows = 0, len = 0;
+    if (b < a.kv.batch) {
+      rows = kv_rows(a.q_start[b], a.q_start[b + 1], a.n, &first, &bad);
+      len = kv_len(a.kv, a.kv.len[b], &bad);
+    }
     if (bad) raise_status(a.kv);
-    if (t >= first && t < first + rows) atomicMax(&found[0], b);
+    const uint64_t hit = __ballot(t >= first && t < first + rows);
+    if (hit) {
+      const int w = __builtin_amdgcn_readfirstlane(__builtin_ctzll(hit));
+      p.seq = b0 + w;
+      const int entry = __builtin_amdgcn_readlane(len - rows + t - first, w);
+      if (entry >= 0) {
+        p.page = kv_page(a.kv, a.kv.table + p.seq * a.kv.table_stride, shift, entry, &p.in_page);
+        if (p.page < 0 && lane == 0) raise_status(a.kv);
+      }
+    }
   }
-  __syncthreads();
-  Place p;
-  p.seq = found[0];
-  p.entry = p.page = -1;
-  p.in_page = 0;
-  if (p.seq < 0) return p;
-  bool bad = false;
-  int first;
-  const int rows = kv_rows(a.q_start[p.seq], a.q_start[p.seq + 1], a.n, &first, &bad);
-  const int len = kv_len(a.kv, a.kv.len[p.seq], &bad);
-  p.entry = len - rows + (t - first);
-  if (p.entry >= 0) {
-    p.page = kv_page(a.kv, a.kv.table + p.seq * a.kv.table_stride, kv_shift(a.kv.page_size), p.entry, &p.in_page);
-    if (p.page < 0) bad = true;
-  }
-  if (bad && threadIdx.x == 0) raise_status(a.kv);
   return p;
 }
 
-__global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
-  __shared__ float cs[128], sn[128];
-  const int t = blockIdx.x, half = a.rot_dim / 2, D = a.head_dim;
-  Place p = {0, -1, -1, 0};
-  if (a.append) {
-    p = find_place(a, t);
-    if (p.seq < 0) return;
+// Head `hh` of a token's q, k and v heads: where it is read and written.
+struct Head {
+  const uint16_t *src;
+  void *dst;
+  float scale;   // e4m3: values are divided by it; 0: bf16
+  bool turn;
+};
+__device__ inline Head head_at(const RopeArgs &a, const Place &p, int t, int hh) {
+  Head h;
+  h.scale = 0.f;
+  h.turn = true;
+  if (hh < a.heads) {
+    h.src = a.x.p + t * a.x.row + hh * a.x.head;
+    h.dst = a.y.p + t * a.y.row + hh * a.y.head;
+    return h;
   }
-  const double pos = a.pos[t];
-  for (int i = threadIdx.x; i < half; i += kThreads) {
-    const double turns = pos * a.freq[i] * 0.15915494309189533577;
-    float s, c;
-    sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
-    cs[i] = c * a.mscale;
-    sn[i] = s * a.mscale;
+  const int k = hh - a.heads, v = k - a.kv.kv_heads;
+  const bool is_v = v >= 0, fp8 = a.kv.elem == OES_ELEM_E4M3;
+  h.src = is_v ? a.v.p + t * a.v.row + v * a.v.head : a.k.p + t * a.k.row + k * a.k.head;
+  const int64_t off = is_v ? kv_v_off(a.kv, p.page, p.in_page) + a.kv.v_head * v : kv_k_off(a.kv, p.page, p.in_page) + a.kv.k_head * k;
+  h.dst = static_cast<uint8_t *>(is_v ? a.kv.v : a.kv.k) + off * (fp8 ? 1 : 2);
+  if (fp8) h.scale = is_v ? a.kv.v_scale : a.kv.k_scale;
+  h.turn = !is_v;
+  return h;
+}
+
+// 8 values of a piece to where they go.
+__device__ inline void put8(const Head &h, int at, const float *v, u32x4 raw, bool turned) {
+  if (h.scale > 0.f) {
+    u32x2 w;
+    if (!turned)
+      for (int i = 0; i < 4; ++i) const_cast<float *>(v)[2 * i] = bf16_lo(raw[i]), const_cast<float *>(v)[2 * i + 1] = bf16_hi(raw[i]);
+    w.x = f2e4m3_pair(v[0] / h.scale, v[1] / h.scale) | f2e4m3_pair(v[2] / h.scale, v[3] / h.scale) << 16;
+    w.y = f2e4m3_pair(v[4] / h.scale, v[5] / h.scale) | f2e4m3_pair(v[6] / h.scale, v[7] / h.scale) << 16;
+    *reinterpret_cast<u32x2 *>(static_cast<uint8_t *>(h.dst) + at) = w;
+  } else {
+    if (turned) raw = u32x4{f2bf16_pair(v[0], v[1]), f2bf16_pair(v[2], v[3]), f2bf16_pair(v[4], v[5]), f2bf16_pair(v[6], v[7])};
+    *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(h.dst) + at) = raw;
   }
-  __syncthreads();
-  const int kvh = a.append && p.page >= 0 ? a.kv.kv_heads : 0;
-  const int pairs = D / 2;
-  const bool fp8 = a.kv.elem == OES_ELEM_E4M3;
-  for (int it = threadIdx.x; it < (a.heads + 2 * kvh) * pairs; it += kThreads) {
-    const int hh = it / pairs, i = it - hh * pairs;
-    // pair i: a rotated one for i < half, else two values that are copied
-    const bool rot = i < half;
-    const int e0 = rot ? (a.layout == OES_ROPE_HALF ? i : 2 * i) : 2 * i;
-    const int e1 = rot ? (a.layout == OES_ROPE_HALF ? i + half : 2 * i + 1) : 2 * i + 1;
-    const bool is_q = hh < a.heads, is_v = hh >= a.heads + kvh;
-    const int h = is_q ? hh : (is_v ? hh - a.heads - kvh : hh - a.heads);
-    const Rows &src = is_q ? a.x : (is_v ? a.v : a.k);
-    const uint16_t *sp = src.p + t * src.row + h * src.head;
-    const uint32_t b0 = sp[e0], b1 = sp[e1];
-    float x0 = bf16f(b0), x1 = bf16f(b1);
-    if (rot && !is_v) {
-      const float c = cs[i], s = sn[i], y0 = x0 * c - x1 * s, y1 = x0 * s + x1 * c;
-      x0 = y0;
-      x1 = y1;
+}
+
+template <bool INTERLEAVED, bool PIECES>
+__global__ __launch_bounds__(kWaves * 64) void rope_kernel(RopeArgs a, int parts, int shift) {
+  __shared__ __attribute__((aligned(16))) float cs[kWaves][128], sn[kWaves][128];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, D = a.head_dim, half = a.rot_dim / 2;
+  const int per = PIECES ? D / 16 : D / 2;         // items (or pairs) of a head
+  const int heads = a.heads + (a.append ? 2 * a.kv.kv_heads : 0);
+  const int per_pass = PIECES ? 64 / per : 1;      // heads that the wave takes at once
+  const int hl = PIECES ? lane / per : 0, j = PIECES ? lane - hl * per : lane;
+  const int passes = (heads + per_pass - 1) / per_pass;
+  for (int64_t it = (int64_t)blockIdx.x * kWaves + wave; it < (int64_t)a.n * parts; it += (int64_t)gridDim.x * kWaves) {
+    const int t = (int)(it / parts), part = (int)(it - (int64_t)t * parts);
+    Place p = {0, -1, 0};
+    if (a.append) p = find_place(a, t, shift);
+    if (p.seq < 0) continue;
+    const int live_heads = p.page >= 0 ? heads : a.heads;
+    const double pos = a.pos[t];
+    __builtin_amdgcn_wave_barrier();   // the last token's tables have been read
+    for (int i = lane; i < half; i += 64) {
+      const double turns = pos * a.freq[i] * 0.15915494309189533577;
+      float s, c;
+      sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+      cs[wave][i] = c * a.mscale;
+      sn[wave][i] = s * a.mscale;
     }
-    if (is_q) {
-      uint16_t *dp = a.y.p + t * a.y.row + h * a.y.head;
-      dp[e0] = (uint16_t)f2bf16(x0);
-      dp[e1] = (uint16_t)f2bf16(x1);
+    __builtin_amdgcn_wave_barrier();   // one wave's LDS operations run in order
+    const int pass0 = (int)((int64_t)passes * part / parts), pass1 = (int)((int64_t)passes * (part + 1) / parts);
+    if (PIECES) {
+      // this lane's item: pieces at p0 and p1, pairs i0 .. i0 + 7
+      const bool turns = INTERLEAVED ? 16 * j < a.rot_dim : 8 * j < half;
+      const int p0 = INTERLEAVED || !turns ? 16 * j : 8 * j, p1 = INTERLEAVED || !turns ? 16 * j + 8 : 8 * j + half;
+      float c8[8], s8[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int pr = turns ? 8 * j + i : 0;
+        c8[i] = pr < half ? cs[wave][pr] : 0.f;
+        s8[i] = pr < half ? sn[wave][pr] : 0.f;
+      }
+      for (int ps = pass0; ps < pass1; ps += kUnroll) {
+        Head h[kUnroll];
+        u32x4 r0[kUnroll], r1[kUnroll];
+        bool in[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const int hh = (ps + u) * per_pass + hl;
+          in[u] = ps + u < pass1 && hl < per_pass && hh < live_heads;
+          if (in[u]) {
+            h[u] = head_at(a, p, t, hh);
+            r0[u] = *reinterpret_cast<const u32x4 *>(h[u].src + p0);
+            r1[u] = *reinterpret_cast<const u32x4 *>(h[u].src + p1);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          if (!in[u]) continue;
+          const bool turn = turns && h[u].turn;
+          float y0[8], y1[8];
+          if (turn) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              // pair i: INTERLEAVED, the two halves of word i of the 16 values; else value i of either piece
+              const uint32_t w0 = INTERLEAVED ? (i < 4 ? r0[u][i] : r1[u][i - 4]) : r0[u][i / 2], w1 = r1[u][i / 2];
+              const float x0 = INTERLEAVED ? bf16_lo(w0) : (i & 1 ? bf16_hi(w0) : bf16_lo(w0));
+              const float x1 = INTERLEAVED ? bf16_hi(w0) : (i & 1 ? bf16_hi(w1) : bf16_lo(w1));
+              float v0 = x0 * c8[i] - x1 * s8[i], v1 = x0 * s8[i] + x1 * c8[i];
+              if (INTERLEAVED) {
+                if (8 * j + i >= half) v0 = x0, v1 = x1;   // rot_dim ends within the item
+                (i < 4 ? y0 : y1)[2 * (i & 3)] = v0;
+                (i < 4 ? y0 : y1)[2 * (i & 3) + 1] = v1;
+              } else {
+                y0[i] = v0;
+                y1[i] = v1;
+              }
+            }
+          }
+          put8(h[u], p0, y0, r0[u], turn);
+          put8(h[u], p1, y1, r1[u], turn);
+        }
+      }
     } else {
-      const int64_t off = (is_v ? kv_v_off(a.kv, p.page, p.in_page) + a.kv.v_head * h
-                                : kv_k_off(a.kv, p.page, p.in_page) + a.kv.k_head * h);
-      void *base = is_v ? a.kv.v : a.kv.k;
-      if (fp8) {
-        const float sc = is_v ? a.kv.v_scale : a.kv.k_scale;
-        const uint32_t pr = f2e4m3_pair(x0 / sc, x1 / sc);
-        static_cast<uint8_t *>(base)[off + e0] = (uint8_t)pr;
-        static_cast<uint8_t *>(base)[off + e1] = (uint8_t)(pr >> 8);
-      } else {
-        static_cast<uint16_t *>(base)[off + e0] = (uint16_t)f2bf16(x0);
-        static_cast<uint16_t *>(base)[off + e1] = (uint16_t)f2bf16(x1);
+      for (int hh = pass0; hh < min(pass1, live_heads); ++hh) {
+        const Head h = head_at(a, p, t, hh);
+        for (int i = j; i < per; i += 64) {
+          // pair i of the half layout for i < half, else two values that are copied
+          const int e0 = i < half ? i : 2 * i, e1 = i < half ? i + half : 2 * i + 1;
+          const float x0 = bf16f(h.src[e0]), x1 = bf16f(h.src[e1]);
+          float v0 = x0, v1 = x1;
+          if (i < half && h.turn) {
+            const float c = cs[wave][i], s = sn[wave][i];
+            v0 = x0 * c - x1 * s;
+            v1 = x0 * s + x1 * c;
+          }
+          if (h.scale > 0.f) {
+            const uint32_t w = f2e4m3_pair(v0 / h.scale, v1 / h.scale);
+            static_cast<uint8_t *>(h.dst)[e0] = (uint8_t)w;
+            static_cast<uint8_t *>(h.dst)[e1] = (uint8_t)(w >> 8);
+          } else {
+            static_cast<uint16_t *>(h.dst)[e0] = (uint16_t)f2bf16(v0);
+            static_cast<uint16_t *>(h.dst)[e1] = (uint16_t)f2bf16(v1);
+          }
+        }
       }
     }
   }
@@ -113,7 +204,20 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
 }  // namespace
 
 hipError_t launch_rope(const RopeArgs &a, hipStream_t s) {
-  hipLaunchKernelGGL(rope_kernel, dim3(a.n), dim3(kThreads), 0, s, a);
+  const bool inter = a.layout == OES_ROPE_INTERLEAVED, pieces = inter || a.rot_dim % 16 == 0;
+  const int heads = a.heads + (a.append ? 2 * a.kv.kv_heads : 0), per_pass = pieces ? 64 / (a.head_dim / 16) : 1;
+  const int passes = (heads + per_pass - 1) / per_pass;
+  // with few tokens, a wave to a pass of each; with many, a token to a wave, and several to each of 2048 workgroups
+  const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(passes, 4096 / a.n));
+  const int64_t blocks = std::min<int64_t>(2048, ((int64_t)a.n * parts + kWaves - 1) / kWaves);
+  const int shift = a.append ? kv_shift(a.kv.page_size) : 0;
+  const dim3 g((uint32_t)blocks), b(kWaves * 64);
+  if (inter)
+    hipLaunchKernelGGL((rope_kernel<true, true>), g, b, 0, s, a, parts, shift);
+  else if (pieces)
+    hipLaunchKernelGGL((rope_kernel<false, true>), g, b, 0, s, a, parts, shift);
+  else
+    hipLaunchKernelGGL((rope_kernel<false, false>), g, b, 0, s, a, parts, shift);
   return hipGetLastError();
 }
 
