@@ -3,15 +3,18 @@
 //   evict_select  one workgroup per (sequence, head).  Every entry gets a 32-bit key
 //                 that orders as its weight does (NaN lowest, -0 as 0); the first and
 //                 last ones are always kept.  The smallest kept key is found by a radix
-//                 select, 8 bits a pass, then one ordered pass over the entries writes the
-//                 kept ones' indices in order (equal keys: the lowest indices) and moves
-//                 their weights.
+//                 select, 8 bits a pass, on keys that stay in registers (16 a thread; more
+//                 than 16384 entries are read again in each pass).  Then the kept entries'
+//                 ranks, from one ordered sum over the waves' counts (equal keys: the
+//                 lowest indices stay), place their indices and weights.
 //   evict_move    moves the k and v rows.  Entry i comes from kept[i] >= i, so going up in
 //                 batches that are read whole before they are written is safe in place:
 //                 a row i in the batch [i0, i1) that is itself kept has a rank <= i, so
 //                 it was moved with this batch or before, and later batches read rows
-//                 from i1 on only.  Head rows are cut into 16-byte columns, and each
-//                 workgroup moves one group of columns of one (sequence, head).
+//                 from i1 on only (so the next batch's reads go out before this one's
+//                 writes).  Head rows are cut into columns of 128 bytes, and each
+//                 workgroup moves one column of one (sequence, head); bound by reading and
+//                 writing the moved rows once.
 
 #include "layer_device.h"
 #include "oes_internal.h"
@@ -20,7 +23,8 @@ namespace oes {
 
 namespace {
 
-constexpr int kSel = 1024;
+constexpr int kSel = 1024, kWaves = kSel / 64, kHold = 16, kChunk = kSel * kHold;
+constexpr int kCopies = 16;   // of the histogram, by lane: the leading digits of most keys are the same
 
 __device__ inline uint32_t weight_key(float v) {
   if (v != v) return 0u;
@@ -28,11 +32,20 @@ __device__ inline uint32_t weight_key(float v) {
   const uint32_t u = __float_as_uint(v);
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
+__device__ inline int scan64(int v) {  // inclusive, over the wave
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+  return v;
+}
 
-// ws: per (sequence, head) the first entry that moves (= the new length if none does)
+// ws: per (sequence, head) the first entry that moves and the new length (the same: none moves)
 __global__ __launch_bounds__(kSel) void evict_select_kernel(EvictArgs a) {
-  __shared__ int hist[256];
-  __shared__ int wave_gt[16], wave_eq[16], sh[4];
+  __shared__ __attribute__((aligned(16))) int hist[256 * kCopies];
+  __shared__ int counts[kHold * kWaves], sh[4];
   const int bh = blockIdx.x, b = bh / a.kv.kv_heads, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   bool bad = false;
   const int len = kv_len(a.kv, a.kv.len[b], &bad);
@@ -41,7 +54,10 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(EvictArgs a) {
   // every page that the sequence uses has to be one of the cache
   const int32_t *table = a.kv.table + b * a.kv.table_stride;
   const int cols = (int)(((int64_t)len + a.kv.page_size - 1) / a.kv.page_size);
-  if (tid == 0) sh[0] = 0;
+  if (tid == 0) {
+    sh[0] = 0;
+    sh[3] = len;
+  }
   __syncthreads();
   for (int c = tid; c < cols; c += kSel)
     if (table[c] < 0 || table[c] >= a.kv.num_pages) sh[0] = 1;
@@ -54,128 +70,182 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(EvictArgs a) {
     return;
   }
   const int mid0 = a.first, mid1 = len - a.last;    // entries that have to earn their place
-  int want = a.budget - a.first - a.last;           // of them stay
+  const int want = a.budget - a.first - a.last;     // of them stay
+  float v[kHold];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int x = 0; x < kHold; ++x) {
+      const int j = base + x * kSel + tid;
+      v[x] = j < len ? acc[j] : 0.f;
+    }
+  };
+  if (len <= kChunk) load(0);
   uint32_t prefix = 0, mask = 0;
   int left = want;                                  // still wanted among the keys of this prefix
   for (int shift = 24; shift >= 0 && want > 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kSel) hist[i] = 0;
+    for (int i = tid; i < 256 * kCopies; i += kSel) hist[i] = 0;
     __syncthreads();
-    for (int j = mid0 + tid; j < mid1; j += kSel) {
-      const uint32_t k = weight_key(acc[j]);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+    for (int base = 0; base < len; base += kChunk) {
+      if (len > kChunk) load(base);
+#pragma unroll
+      for (int x = 0; x < kHold; ++x) {
+        const int j = base + x * kSel + tid;
+        const uint32_t k = weight_key(v[x]);
+        if (j >= mid0 && j < mid1 && (k & mask) == prefix) atomicAdd(&hist[((k >> shift) & 255) * kCopies + (lane & (kCopies - 1))], 1);
+      }
     }
     __syncthreads();
-    if (tid == 0) {
-      int d = 255, n = left;
-      while (d > 0 && n > hist[d]) n -= hist[d--];
-      sh[1] = d;
-      sh[2] = n;
+    if (wave == 0) {
+      // lane l: digits 255 - 4 l down to 252 - 4 l, so that the running sum goes from the largest down
+      int n[4], sum = 0;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        n[d] = 0;
+        const int4 *h = reinterpret_cast<const int4 *>(hist + (255 - 4 * lane - d) * kCopies);
+#pragma unroll
+        for (int c = 0; c < kCopies / 4; ++c) n[d] += (h[c].x + h[c].y) + (h[c].z + h[c].w);
+        sum += n[d];
+      }
+      int above = scan64(sum) - sum;   // keys with a larger digit than the lane's
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        if (above < left && above + n[d] >= left) {
+          sh[1] = 255 - 4 * lane - d;
+          sh[2] = left - above;
+        }
+        above += n[d];
+      }
     }
     __syncthreads();
     prefix |= (uint32_t)sh[1] << shift;
     mask |= 255u << shift;
     left = sh[2];
-    __syncthreads();
   }
-  // keys above prefix stay, and the `left` lowest-indexed ones equal to it
-  int at = 0, eq_at = 0, moved = a.budget;
-  for (int j0 = 0; j0 < len; j0 += kSel) {
-    const int j = j0 + tid;
-    bool stay = false, eq = false;
-    float v = 0.f;
-    if (j < len) {
-      v = acc[j];
+  // Exclusive sum over (stretch, wave), in the order of the entries, of counts[stretch * waves + wave]; all threads.
+  auto ranks = [&](int *total) {
+    __syncthreads();
+    if (wave == 0) {
+      constexpr int kPer = kHold * kWaves / 64;
+      int n[kPer], sum = 0;
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) {
+        n[x] = counts[lane * kPer + x];
+        sum += n[x];
+      }
+      const int upto = scan64(sum);
+      int at = upto - sum;
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) {
+        counts[lane * kPer + x] = at;
+        at += n[x];
+      }
+      if (lane == 63) sh[1] = upto;
     }
-    // a weight still on its way must not be overtaken by the stores of this stretch
+    __syncthreads();
+    *total = sh[1];
+  };
+  // keys above prefix stay, and the `left` lowest-indexed ones equal to it
+  int at = 0, eq_at = 0;
+  const uint64_t below = (1ull << lane) - 1;
+  for (int base = 0; base < len; base += kChunk) {
+    if (len > kChunk) load(base);
+    uint32_t stay = 0, eq = 0;   // bit x: the thread's entry of stretch x
+#pragma unroll
+    for (int x = 0; x < kHold; ++x) {
+      const int j = base + x * kSel + tid;
+      const uint32_t k = weight_key(v[x]);
+      const bool in = j < len, mid = j >= mid0 && j < mid1;
+      if (in && (!mid || (want > 0 && k > prefix))) stay |= 1u << x;
+      const bool same = in && mid && want > 0 && k == prefix;
+      if (same) eq |= 1u << x;
+      const uint64_t m = __ballot(same);
+      if (lane == 0) counts[x * kWaves + wave] = __popcll(m);
+    }
+    int total;
+    ranks(&total);
+#pragma unroll
+    for (int x = 0; x < kHold; ++x) {
+      const uint64_t m = __ballot((eq >> x) & 1);
+      if (((eq >> x) & 1) && eq_at + counts[x * kWaves + wave] + __popcll(m & below) < left) stay |= 1u << x;
+    }
+    eq_at += total;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kHold; ++x) {
+      const uint64_t m = __ballot((stay >> x) & 1);
+      if (lane == 0) counts[x * kWaves + wave] = __popcll(m);
+      const uint64_t gone = __ballot(base + x * kSel + tid < len && !((stay >> x) & 1));
+      if (lane == 0 && gone) atomicMin(&sh[3], base + x * kSel + wave * 64 + __builtin_ctzll(gone));
+    }
+    ranks(&total);
+    // every thread has the weights of this chunk in registers, and places up to here are free
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    if (j < len) {
-      if (j < mid0 || j >= mid1) {
-        stay = true;
-      } else if (want > 0) {
-        const uint32_t k = weight_key(v);
-        stay = k > prefix;
-        eq = k == prefix;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kHold; ++x) {
+      const uint64_t m = __ballot((stay >> x) & 1);
+      if ((stay >> x) & 1) {
+        const int j = base + x * kSel + tid, pos = at + counts[x * kWaves + wave] + __popcll(m & below);
+        kept[pos] = j;
+        if (pos != j) acc[pos] = v[x];
       }
     }
-    const uint64_t below = (1ull << lane) - 1;
-    const uint64_t meq = __ballot(eq);
-    if (lane == 0) wave_eq[wave] = __popcll(meq);
-    __syncthreads();
-    int eq_rank = eq_at + __popcll(meq & below);
-    int eq_all = 0;
-    for (int w = 0; w < 16; ++w) {
-      if (w < wave) eq_rank += wave_eq[w];
-      eq_all += wave_eq[w];
-    }
-    if (eq && eq_rank < left) stay = true;
-    eq_at += eq_all;
-    const uint64_t mst = __ballot(stay);
-    if (lane == 0) wave_gt[wave] = __popcll(mst);
-    __syncthreads();
-    int pos = at + __popcll(mst & below), all = 0;
-    for (int w = 0; w < 16; ++w) {
-      if (w < wave) pos += wave_gt[w];
-      all += wave_gt[w];
-    }
-    // every thread has read its weight of this stretch; places up to here are free
-    if (stay) {
-      kept[pos] = j;
-      if (pos != j) acc[pos] = v;
-    }
-    if (all < min(kSel, len - j0) && moved == a.budget) {  // the first dropped entry is in here
-      if (tid == 0) sh[3] = kSel;
-      __syncthreads();
-      if (j < len && !stay) atomicMin(&sh[3], tid);
-      __syncthreads();
-      moved = min(a.budget, j0 + sh[3]);
-    }
-    at += all;
+    at += total;
     __syncthreads();
   }
   if (tid == 0) {
-    a.ws[2 * bh] = moved;
+    a.ws[2 * bh] = min(a.budget, sh[3]);
     a.ws[2 * bh + 1] = a.budget;
   }
 }
 
-// 16-byte columns [c0, c0 + 4) of the head rows of k and v; thread (row, column)
-constexpr int kMove = 256, kUnroll = 8;
+constexpr int kMove = 512, kUnroll = 4, kRows = kMove / 8, kBatch = kRows * kUnroll;
 
-__global__ __launch_bounds__(kMove) void evict_move_kernel(EvictArgs a, int groups) {
-  const int bh = blockIdx.x / groups, grp = blockIdx.x - bh * groups;
+__global__ __launch_bounds__(kMove) void evict_move_kernel(EvictArgs a, int columns, int shift) {
+  const int bh = blockIdx.x / columns, column = blockIdx.x - bh * columns;
   const int b = bh / a.kv.kv_heads, h = bh - b * a.kv.kv_heads;
   const int from = a.ws[2 * bh], to = a.ws[2 * bh + 1];
-  if (h == 0 && grp == 0 && threadIdx.x == 0) a.new_len[b] = to;
+  if (h == 0 && column == 0 && threadIdx.x == 0) a.new_len[b] = to;
   if (from >= to) return;
-  const int es = a.kv.elem == OES_ELEM_BF16 ? 2 : 1, per_row = a.kv.head_dim * es / 16;
-  const int kgroups = (per_row + 3) / 4;
-  const bool is_v = grp >= kgroups;
-  const int col = (is_v ? grp - kgroups : grp) * 4 + (threadIdx.x & 3);
-  const bool live = col < per_row;
-  uint8_t *base = static_cast<uint8_t *>(is_v ? a.kv.v : a.kv.k) + (is_v ? a.kv.v_head : a.kv.k_head) * h * es + col * 16;
+  const int es = a.kv.elem == OES_ELEM_BF16 ? 2 : 1, pieces = a.kv.head_dim * es / 16;
+  const bool is_v = column >= columns / 2;
+  const int piece = (is_v ? column - columns / 2 : column) * 8 + (threadIdx.x & 7), r0 = threadIdx.x >> 3;
+  const bool live = piece < pieces;
+  uint8_t *base = static_cast<uint8_t *>(is_v ? a.kv.v : a.kv.k) + (is_v ? a.kv.v_head : a.kv.k_head) * h * es + (live ? piece * 16 : 0);
   const int32_t *table = a.kv.table + b * a.kv.table_stride, *kept = a.kept + (int64_t)bh * a.budget;
-  const int shift = kv_shift(a.kv.page_size);
   auto row = [&](int j) {
     int ip = 0;
     const int p = kv_page(a.kv, table, shift, j, &ip);  // >= 0: checked for the whole sequence
     return reinterpret_cast<u32x4 *>(base + es * (is_v ? kv_v_off(a.kv, p, ip) : kv_k_off(a.kv, p, ip)));
   };
-  constexpr int kRows = kMove / 4;
-  for (int i0 = from; i0 < to; i0 += kRows * kUnroll) {
-    u32x4 v[kUnroll];
+  // rows past the last one are read again, and not written
+  const u32x4 *src[kUnroll];
+  u32x4 v[kUnroll], next[kUnroll];
+  auto sources = [&](int i0) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kRows + (threadIdx.x >> 2);
-      if (live && i < to) v[u] = *row(kept[i]);
-    }
+    for (int u = 0; u < kUnroll; ++u) src[u] = row(kept[min(i0 + u * kRows + r0, to - 1)]);
+  };
+  sources(from);
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) v[u] = *src[u];
+  for (int i0 = from; i0 < to; i0 += kBatch) {
+    const bool more = i0 + kBatch < to;
+    if (more) sources(i0 + kBatch);
+    u32x4 *dst[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) dst[u] = row(min(i0 + u * kRows + r0, to - 1));
     // the whole batch is in registers before its first row is written
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
+    if (more) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kRows + (threadIdx.x >> 2);
-      if (live && i < to) *row(i) = v[u];
+      for (int u = 0; u < kUnroll; ++u) next[u] = *src[u];
     }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (live && i0 + u * kRows + r0 < to) *dst[u] = v[u];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) v[u] = next[u];
   }
 }
 
@@ -188,9 +258,8 @@ hipError_t launch_evict(const EvictArgs &a, hipStream_t s) {
   hipLaunchKernelGGL(evict_select_kernel, dim3(bh), dim3(kSel), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int es = a.kv.elem == OES_ELEM_BF16 ? 2 : 1, per_row = a.kv.head_dim * es / 16;
-  const int groups = 2 * ((per_row + 3) / 4);
-  hipLaunchKernelGGL(evict_move_kernel, dim3(bh * groups), dim3(kMove), 0, s, a, groups);
+  const int es = a.kv.elem == OES_ELEM_BF16 ? 2 : 1, columns = 2 * ((a.kv.head_dim * es + 127) / 128);
+  hipLaunchKernelGGL(evict_move_kernel, dim3(bh * columns), dim3(kMove), 0, s, a, columns, kv_shift(a.kv.page_size));
   return hipGetLastError();
 }
 

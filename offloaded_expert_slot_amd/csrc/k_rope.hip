@@ -22,7 +22,7 @@ namespace oes {
 
 namespace {
 
-constexpr int kWaves = 4, kUnroll = 4;
+constexpr int kWaves = 4, kUnroll = 2;
 
 // Where a token's k and v go: sequence (-1: a row of none), and page (-1: no entry).  Wave-wide.
 struct Place {
