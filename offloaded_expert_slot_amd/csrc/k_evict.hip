@@ -75,6 +75,7 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(EvictArgs a) {
   auto load = [&](int base) {
 #pragma unroll
     for (int x = 0; x < kHold; ++x) {
+      if (base + x * kSel >= len) break;
       const int j = base + x * kSel + tid;
       v[x] = j < len ? acc[j] : 0.f;
     }
@@ -89,6 +90,7 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(EvictArgs a) {
       if (len > kChunk) load(base);
 #pragma unroll
       for (int x = 0; x < kHold; ++x) {
+        if (base + x * kSel >= len) break;
         const int j = base + x * kSel + tid;
         const uint32_t k = weight_key(v[x]);
         if (j >= mid0 && j < mid1 && (k & mask) == prefix) atomicAdd(&hist[((k >> shift) & 255) * kCopies + (lane & (kCopies - 1))], 1);
@@ -152,6 +154,10 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(EvictArgs a) {
     uint32_t stay = 0, eq = 0;   // bit x: the thread's entry of stretch x
 #pragma unroll
     for (int x = 0; x < kHold; ++x) {
+      if (base + x * kSel >= len) {   // (the same in every thread; the sums go over all stretches)
+        if (lane == 0) counts[x * kWaves + wave] = 0;
+        continue;
+      }
       const int j = base + x * kSel + tid;
       const uint32_t k = weight_key(v[x]);
       const bool in = j < len, mid = j >= mid0 && j < mid1;
@@ -165,6 +171,7 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(EvictArgs a) {
     ranks(&total);
 #pragma unroll
     for (int x = 0; x < kHold; ++x) {
+      if (base + x * kSel >= len) break;
       const uint64_t m = __ballot((eq >> x) & 1);
       if (((eq >> x) & 1) && eq_at + counts[x * kWaves + wave] + __popcll(m & below) < left) stay |= 1u << x;
     }
@@ -174,6 +181,7 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(EvictArgs a) {
     for (int x = 0; x < kHold; ++x) {
       const uint64_t m = __ballot((stay >> x) & 1);
       if (lane == 0) counts[x * kWaves + wave] = __popcll(m);
+      if (base + x * kSel >= len) continue;
       const uint64_t gone = __ballot(base + x * kSel + tid < len && !((stay >> x) & 1));
       if (lane == 0 && gone) atomicMin(&sh[3], base + x * kSel + wave * 64 + __builtin_ctzll(gone));
     }
@@ -183,6 +191,7 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(EvictArgs a) {
     __syncthreads();
 #pragma unroll
     for (int x = 0; x < kHold; ++x) {
+      if (base + x * kSel >= len) break;
       const uint64_t m = __ballot((stay >> x) & 1);
       if ((stay >> x) & 1) {
         const int j = base + x * kSel + tid, pos = at + counts[x * kWaves + wave] + __popcll(m & below);
@@ -199,7 +208,10 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(EvictArgs a) {
   }
 }
 
-constexpr int kMove = 512, kUnroll = 4, kRows = kMove / 8, kBatch = kRows * kUnroll;
+// 256 rows of 128 bytes in flight per workgroup.  (16 x 4 heads of 2048 bf16 rows, 256 workgroups: 28.9 us; with 512
+// threads and 4 rows a thread 37; 64-byte columns, twice the workgroups, 38.)
+constexpr int kMove = 1024, kUnroll = 2, kRows = kMove / 8, kBatch = kRows * kUnroll;
+
 
 __global__ __launch_bounds__(kMove) void evict_move_kernel(EvictArgs a, int columns, int shift) {
   const int bh = blockIdx.x / columns, column = blockIdx.x - bh * columns;
@@ -258,7 +270,7 @@ hipError_t launch_evict(const EvictArgs &a, hipStream_t s) {
   hipLaunchKernelGGL(evict_select_kernel, dim3(bh), dim3(kSel), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int es = a.kv.elem == OES_ELEM_BF16 ? 2 : 1, columns = 2 * ((a.kv.head_dim * es + 127) / 128);
+  const int columns = 2 * ((a.kv.head_dim * (a.kv.elem == OES_ELEM_BF16 ? 2 : 1) + 127) / 128);
   hipLaunchKernelGGL(evict_move_kernel, dim3(bh * columns), dim3(kMove), 0, s, a, columns, kv_shift(a.kv.page_size));
   return hipGetLastError();
 }
