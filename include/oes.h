@@ -413,7 +413,7 @@ oes_status oes_layers_ffn(oes_layers *p, int32_t layer, const void *x, const int
  * Other formats: OES_ERR_UNSUPPORTED.  x is bf16 with rows x_stride elements
  * apart, y bf16 with rows y_stride elements apart.  Sums are fp32; the weights
  * are used exactly (no rounding on the way); y is rounded to nearest even once.
- * K a positive multiple of 32 up to 2^20, N in [1, 2^25], n in [0, 2^19]
+ * K a positive multiple of 32 up to 2^20, N in [1, 2^23], n in [0, 2^19]
  * (OES_ERR_UNSUPPORTED beyond N's and n's limits); w0, w1 and the rows of
  * x 16-byte aligned, w2 and y 2-byte aligned, x_stride >= K, y_stride >= N.  y
  * must not overlap an input.  Async. */

@@ -125,7 +125,7 @@ extern "C" oes_status oes_linear(int32_t format, const void *w0, const void *w1,
     return fail(OES_ERR_UNSUPPORTED, "format %d has no 4-bit linear product", format);
   if (N < 1 || K < 32 || K % 32 || K > (1 << 20)) return fail(OES_ERR_ARG, "need N >= 1 and K a multiple of 32 up to 2^20");
   if (n < 0) return fail(OES_ERR_ARG, "n < 0");
-  if (N > (1 << 25) || n > (1 << 19)) return fail(OES_ERR_UNSUPPORTED, "N = %d, n = %d: at most 2^25 rows and 2^19 tokens", N, n);
+  if (N > (1 << 23) || n > (1 << 19)) return fail(OES_ERR_UNSUPPORTED, "N = %d, n = %d: at most 2^23 rows and 2^19 tokens", N, n);
   if (n == 0) return OES_OK;
   if (!w0 || !w1 || !x || !y || (format == OES_NVFP4 && !w2)) return fail(OES_ERR_ARG, "NULL input");
   if (format == OES_Q4_0 && w2) return fail(OES_ERR_ARG, "q4_0 has two banks: w2 must be NULL");

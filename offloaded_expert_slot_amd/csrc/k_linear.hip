@@ -68,8 +68,9 @@ struct Chunk {
 constexpr uint32_t kNowhere = 0x7ffffff0u;   // a buffer offset past every end
 constexpr int kPad = 8;                      // values behind a row of x in LDS: 16 rows spread over the banks
 
+// `bytes` from p on; none if there are none left (bytes <= 0).  kNowhere is past the end of any.
 __device__ inline __amdgpu_buffer_rsrc_t buffer(const void *p, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)(uint32_t)min(bytes, (int64_t)0x7fffffe0), 0x00027000);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)max((int64_t)0, min(bytes, (int64_t)0x7fffffe0)), 0x00027000);
 }
 
 // TAIL: K is no multiple of 256, the last step has fewer than eight blocks.
@@ -87,44 +88,46 @@ __global__ __launch_bounds__(WR * WK * 64) void linear_kernel(LinearArgs a, int 
   const int rows_left = (int)max((int64_t)0, min((int64_t)16 * R, a.N - row0));
   const int64_t codes_bytes = (int64_t)KB * 16;
 
-  // offsets of the lane's codes and scales within the wave's rows (vector) and of a step (scalar)
-  const __amdgpu_buffer_rsrc_t wb = buffer(a.w0 + row0 * codes_bytes, rows_left * codes_bytes);
-  const __amdgpu_buffer_rsrc_t sb = buffer(a.w1 + row0 * KB * 2, (int64_t)rows_left * KB * 2);
+  // Offsets of the lane's codes and scales from a step's first ones; the step is in the buffer's start and size (the
+  // range check is of the vector offset alone).
   const uint32_t w_off = ((lane >> 3) * KB + (lane & 7)) * 16, s_off = FMT == OES_MXFP4_T ? q * a.N + r : (r * KB + (FMT == OES_NVFP4 ? q : 0)) * 2;
   auto load = [&](C(&c)[R], int step) {
+    const bool any = step < steps;
     if (FMT == OES_MXFP4_T) {
-      // blocks of K are N rows apart: the buffer starts at the step's first one
-      const bool in = step < steps;
-      const int64_t at = in ? 8ll * step * a.N + row0 : 0;
-      const __amdgpu_buffer_rsrc_t wt = buffer(a.w0 + at * 16, in ? ((int64_t)KB * a.N - at) * 16 : 0), st = buffer(a.w1 + at, in ? (int64_t)KB * a.N - at : 0);
+      // blocks of K are N rows apart
+      const int64_t at = any ? 8ll * step * a.N + row0 : 0, left = any ? (int64_t)KB * a.N - at : 0;
+      const __amdgpu_buffer_rsrc_t wt = buffer(a.w0 + at * 16, left * 16), st = buffer(a.w1 + at, left);
 #pragma unroll
       for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const bool row_in = 16 * i + r < rows_left;
-          c[i].w[h] = __builtin_amdgcn_raw_buffer_load_b128(wt, row_in ? (s_off + 16 * i) * 16 : kNowhere, 4 * h * a.N * 16, 0);
-          c[i].sc[h] = __builtin_amdgcn_raw_buffer_load_b8(st, row_in ? s_off + 16 * i : kNowhere, 4 * h * a.N, 0);
+          const bool in = 16 * i + r < rows_left && (!TAIL || 8 * step + 4 * h + q < KB);
+          const uint32_t off = s_off + 16 * i + 4 * h * a.N;
+          c[i].w[h] = __builtin_amdgcn_raw_buffer_load_b128(wt, in ? off * 16 : kNowhere, 0, 0);
+          c[i].sc[h] = __builtin_amdgcn_raw_buffer_load_b8(st, in ? off : kNowhere, 0, 0);
         }
     } else {
-      const uint32_t wo = step < steps ? step * 128 : kNowhere, so = step < steps ? step * 16 : kNowhere;
+      const int64_t w_at = any ? step * 128ll : 0, s_at = any ? step * 16ll : 0;
+      const __amdgpu_buffer_rsrc_t wt = buffer(a.w0 + row0 * codes_bytes + w_at, any ? rows_left * codes_bytes - w_at : 0);
+      const __amdgpu_buffer_rsrc_t st = buffer(a.w1 + row0 * KB * 2 + s_at, any ? (int64_t)rows_left * KB * 2 - s_at : 0);
       const bool in = !TAIL || 8 * step + (lane & 7) < KB;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          c[i].w[h] = __builtin_amdgcn_raw_buffer_load_b128(wb, in ? w_off + (16 * i + 8 * h) * KB * 16 : kNowhere, wo, 0);
+          c[i].w[h] = __builtin_amdgcn_raw_buffer_load_b128(wt, in ? w_off + (16 * i + 8 * h) * KB * 16 : kNowhere, 0, 0);
           if (FMT == OES_NVFP4)
-            c[i].sc[h] = __builtin_amdgcn_raw_buffer_load_b16(sb, !TAIL || 8 * step + 4 * h + q < KB ? s_off + 16 * i * KB * 2 + 8 * h : kNowhere, so, 0);
+            c[i].sc[h] = __builtin_amdgcn_raw_buffer_load_b16(st, !TAIL || 8 * step + 4 * h + q < KB ? s_off + 16 * i * KB * 2 + 8 * h : kNowhere, 0, 0);
         }
         if (FMT == OES_Q4_0 && !TAIL) {
-          const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(sb, s_off + 16 * i * KB * 2, so, 0));
+          const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(st, s_off + 16 * i * KB * 2, 0, 0));
 #pragma unroll
           for (int b = 0; b < 4; ++b) c[i].sc[b] = v[b];
         }
         if (FMT == OES_Q4_0 && TAIL) {
 #pragma unroll
           for (int b = 0; b < 8; ++b)
-            c[i].sc[b] = __builtin_amdgcn_raw_buffer_load_b16(sb, 8 * step + b < KB ? s_off + 16 * i * KB * 2 + 2 * b : kNowhere, so, 0);
+            c[i].sc[b] = __builtin_amdgcn_raw_buffer_load_b16(st, 8 * step + b < KB ? s_off + 16 * i * KB * 2 + 2 * b : kNowhere, 0, 0);
         }
       }
     }

@@ -61,6 +61,20 @@ def test_linear(fmt, n, N, K):
     assert (wide[:, N:] == 7).all(), "written behind the row"
 
 
+@pytest.mark.parametrize("fmt", ["q4_0", "nvfp4", "mxfp4_t"])
+@pytest.mark.parametrize("n,N,K", [(23, 5529, 288), (1, 5003, 4128), (3, 9999, 2912), (2, 20005, 2080), (9, 24600, 288),
+                                   (16, 24577, 1536), (20, 24600, 800), (40, 24593, 800), (70, 24611, 256)])
+def test_linear_many_rows(fmt, n, N, K):
+    """Waves of rows past the last one, with a short last step of K; every split of the waves, x in pieces."""
+    banks = _banks(fmt, N, K, n + K)
+    x = torch.randn(n, K, generator=_gen(K)).bfloat16()
+    y = torch.full((n + 1, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    oes.linear(fmt, x.to(DEV), [b.to(DEV) for b in banks], y[:n])
+    ref, bound = R.linear(fmt, x, banks, N)
+    _within(y[:n], ref, bound, (fmt, n, N, K))
+    assert (y[n] == 7).all()
+
+
 @pytest.mark.parametrize("n", [1, 4, 9])
 def test_linear_extremes(n):
     """Large activations in one block, zero blocks, NaN and infinite scales reach their rows only."""

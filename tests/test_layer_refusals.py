@@ -114,6 +114,8 @@ def test_linear_refuses():
                 dict(x=0), dict(y=0), dict(n=-1), dict(w0=A + 8), dict(w1=A + 2), dict(w2=A + 1), dict(x=A + 2), dict(xs=68),
                 dict(xs=32), dict(ys=9), dict(y=A + 1)):
         assert linear(**bad) == oes.ERR_ARG, bad
+    for bad in (dict(N=(1 << 23) + 1, ys=1 << 24), dict(n=(1 << 19) + 1)):
+        assert linear(**bad) == oes.ERR_UNSUPPORTED, bad
 
 
 def test_empty_calls_do_nothing():
