@@ -2,9 +2,10 @@
 //
 // Bound by reading and writing the rows once.  A wave takes one token and a part of its
 // heads; the token's rot_dim / 2 sines and cosines are formed once per wave, in LDS: the
-// angle pos * freq in fp64, reduced to a fraction of a turn in fp64 (a position of a million
-// keeps 2^-30 of a turn, where an fp32 product would lose 0.06 radians), the sine and cosine
-// of that fraction in fp32.  An item is 16 values of a head: two 16-byte pieces that hold 8
+// angle pos * freq in fp64, reduced to an eighth of a turn, sine and cosine by their series in
+// fp64 and rounded to fp32 once, with mscale (a position of a million keeps 2^-30 of a turn,
+// where an fp32 product would lose 0.06 radians; with sines of fp32 more e4m3 entries came
+// out on the wrong side of a border, and the launch took as long).  An item is 16 values of a head: two 16-byte pieces that hold 8
 // pairs (values i .. i + 7 and their partners, half a rotation away or next to them), or that
 // are copied.  A lane reads both pieces before it writes them, and no other lane touches
 // them, so a call in place is safe.  Where the pairs of the half layout do not fall into whole
@@ -96,6 +97,17 @@ __device__ inline void put8(const Head &h, int at, const float *v, u32x4 raw, bo
   }
 }
 
+// Cosine and sine of `turns` turns.  |x| <= pi / 4 after the reduction: the first terms left out are x^13 / 13! < 7e-12
+// and x^14 / 14! < 4e-13.
+__device__ inline void turn_by(double turns, double *c, double *s) {
+  const double quarter = rint(4. * turns), x = (turns - 0.25 * quarter) * 6.283185307179586477, y = x * x;
+  const double sx = x * fma(y, fma(y, fma(y, fma(y, fma(y, -1. / 39916800., 1. / 362880.), -1. / 5040.), 1. / 120.), -1. / 6.), 1.);
+  const double cx = fma(y, fma(y, fma(y, fma(y, fma(y, fma(y, 1. / 479001600., -1. / 3628800.), 1. / 40320.), -1. / 720.), 1. / 24.), -0.5), 1.);
+  const int k = (int)(quarter - 4. * floor(0.25 * quarter));   // quarter turns on top: 0 .. 3
+  *c = k == 0 ? cx : (k == 1 ? -sx : (k == 2 ? -cx : sx));
+  *s = k == 0 ? sx : (k == 1 ? cx : (k == 2 ? -sx : -cx));
+}
+
 template <bool INTERLEAVED, bool PIECES>
 __global__ __launch_bounds__(kWaves * 64) void rope_kernel(RopeArgs a, int parts, int shift) {
   __shared__ __attribute__((aligned(16))) float cs[kWaves][128], sn[kWaves][128];
@@ -114,11 +126,10 @@ __global__ __launch_bounds__(kWaves * 64) void rope_kernel(RopeArgs a, int parts
     const double pos = a.pos[t];
     __builtin_amdgcn_wave_barrier();   // the last token's tables have been read
     for (int i = lane; i < half; i += 64) {
-      const double turns = pos * a.freq[i] * 0.15915494309189533577;
-      float s, c;
-      sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
-      cs[wave][i] = c * a.mscale;
-      sn[wave][i] = s * a.mscale;
+      double c, s;
+      turn_by(pos * a.freq[i] * 0.15915494309189533577, &c, &s);
+      cs[wave][i] = (float)(c * a.mscale);
+      sn[wave][i] = (float)(s * a.mscale);
     }
     __builtin_amdgcn_wave_barrier();   // one wave's LDS operations run in order
     const int pass0 = (int)((int64_t)passes * part / parts), pass1 = (int)((int64_t)passes * (part + 1) / parts);
