@@ -548,3 +548,162 @@ def test_streams_graphs_and_repeats():
         other["c"].dlen.copy_(_dev32([6, 41, 60]))
         _layer_step(other)
         assert all(torch.equal(other[k], ref[k]) for k in keys)
+
+
+# ------------------------------------------------------------------ sizes that the small cases do not reach
+def _many(batch, seed, most_q):
+    """Row counts and lengths of many sequences: empty ones, ones without rows, ones with more rows than entries."""
+    r = np.random.default_rng(seed)
+    q = [int(v) for v in r.integers(0, most_q + 1, batch)]
+    lens = [int(v) for v in r.choice([0, 1, 15, 16, 17, 40, 130, 301], batch)]
+    q[-1], lens[-1] = 1, 33
+    return q, lens
+
+
+@pytest.mark.parametrize("elem", ["bf16", "e4m3"])
+@pytest.mark.parametrize("batch,most_q", [(65, 1), (130, 4), (300, 1), (70, 60)])
+def test_many_sequences(batch, most_q, elem):
+    q_len, lens = _many(batch, batch, most_q)
+    Hq, Hkv, D, page = 8, 2, 64, 16
+    c, start, q, scale, _ = _attn_case((Hq, Hkv, D, page, elem, 0, q_len, lens), 21)
+    kv, _, out, lse = _run_attn(c, start, q, scale, 0)
+    n = start[-1]
+    ref, ref_lse, bound, p = R.attention(q, c, start, scale, 0)
+    _within(out[:n], ref[:n], bound[:n], "attention")
+    assert (out[n:] == 5).all() and (lse[n:] == 5).all()
+    acc = torch.zeros(batch, Hkv, c.cols * page, device=DEV)
+    oes.attn_weigh(q.to(DEV), lse.contiguous(), kv, _dev32(start), scale, acc)
+    for b, m in enumerate(lens):
+        add = p[b].view(p[b].shape[0], Hkv, Hq // Hkv, m).sum((0, 2))
+        # as in test_attn_weigh, with the kernel's own lse: a score's error once more
+        rel = 4 * ((D + 4) * R.U * 8 * math.sqrt(D) + 16 * R.U) + (max(1, p[b].shape[0] * 4) + 2) * R.U
+        _within(acc[b, :, :m], add, rel * add + 1e-30, b)
+        assert (acc[b, :, m:] == 0).all()
+    # the rows' own k and v: entry len - rows + i gets row i, and no other entry changes
+    k = torch.randn(n, Hkv, D, generator=_gen(2)).bfloat16()
+    freq = torch.zeros(D // 2, dtype=torch.float64, device=DEV)
+    oes.rope_append(q[:n].to(DEV), out[:n].contiguous(), k.to(DEV), k.to(DEV), freq, torch.arange(n, dtype=torch.int32, device=DEV), kv, _dev32(start))
+    want_k, want_v = c.k.clone(), c.v.clone()
+    for b, (a, m) in enumerate(zip(q_len, lens)):
+        for i in range(max(0, a - m), a):
+            j, row = m - a + i, k[start[b] + i]
+            pg, r = int(c.table[b, j // page]), j % page
+            if elem == "bf16":
+                want_k[pg, r], want_v[pg, r] = row, row
+            else:
+                want_k[pg, r] = (row.float() / torch.tensor(c.k_scale)).clamp(-448, 448).to(torch.float8_e4m3fn)
+                want_v[pg, r] = (row.float() / torch.tensor(c.v_scale)).clamp(-448, 448).to(torch.float8_e4m3fn)
+    bits = torch.int16 if elem == "bf16" else torch.uint8
+    assert torch.equal(c.dk.cpu().view(bits), want_k.view(bits)) and torch.equal(c.dv.cpu().view(bits), want_v.view(bits))
+    # and the eviction of all of them
+    budget = 40
+    kept = torch.empty(batch, Hkv, budget, dtype=torch.int32, device=DEV)
+    new_len = torch.empty(batch, dtype=torch.int32, device=DEV)
+    ws = torch.empty(oes.kv_evict_workspace_bytes(kv, budget), dtype=torch.uint8, device=DEV)
+    before = acc.cpu().clone()
+    oes.kv_evict(kv, acc, budget, kept, new_len, ws, 4, 8)
+    kv.check()
+    assert torch.equal(kept.cpu(), R.evict(before, lens, c, budget, 4, 8))
+    assert new_len.tolist() == [min(m, budget) for m in lens]
+
+
+@pytest.mark.parametrize("case", [(8, 1, 128, 16, "bf16", 0, [1], [70001]), (4, 4, 64, 64, "e4m3", 0, [2, 1], [40003, 9]),
+                                  (4, 2, 64, 1, "bf16", 0, [3, 1], [50, 190]), (2, 2, 128, 16, "bf16", 1000, [1, 1], [33333, 20])], ids=str)
+def test_attn_long(case):
+    """One row over many parts of a long cache, and pages of a single entry."""
+    c, start, q, scale, window = _attn_case(case, 23, fill=None)
+    kv, dq, out, lse = _run_attn(c, start, q, scale, window)
+    n, Hq, Hkv = start[-1], case[0], case[1]
+    ref, ref_lse, bound, p = R.attention(q, c, start, scale, window)
+    _within(out[:n], ref[:n], bound[:n], case)
+    acc = torch.zeros(len(c.lens), Hkv, c.cols * c.page, device=DEV)
+    lse32 = ref_lse.float()
+    oes.attn_weigh(dq.contiguous(), lse32.to(DEV), kv, _dev32(start), scale, acc, window)
+    D = case[2]
+    for b, m in enumerate(c.lens):
+        add = p[b].view(p[b].shape[0], Hkv, Hq // Hkv, m).sum((0, 2))
+        rel = 2 * ((D + 4) * R.U * 8 * math.sqrt(D) + 16 * R.U) + (p[b].shape[0] * Hq // Hkv + 2) * R.U
+        _within(acc[b, :, :m], add, rel * add + 1e-30, (case, b))
+
+
+@pytest.mark.parametrize("budget,first,last,lens", [(17000, 5, 100, [40000, 16384, 17001]), (60, 4, 10, [16385, 16384, 33000])])
+def test_evict_long(budget, first, last, lens):
+    """More entries than a workgroup holds in registers."""
+    c = R.Cache(29, lens, 2, 16, 64)
+    acc = torch.rand(len(lens), 2, c.cols * 64, generator=_gen(6))
+    acc[:, :, 1::2] = (acc[:, :, 1::2] * 8).round() / 8
+    kv, dacc = c.handle(oes), acc.to(DEV)
+    kept = torch.empty(len(lens), 2, budget, dtype=torch.int32, device=DEV)
+    new_len = torch.empty(len(lens), dtype=torch.int32, device=DEV)
+    ws = torch.empty(oes.kv_evict_workspace_bytes(kv, budget), dtype=torch.uint8, device=DEV)
+    oes.kv_evict(kv, dacc, budget, kept, new_len, ws, first, last)
+    kv.check()
+    ref = R.evict(acc, lens, c, budget, first, last)
+    assert torch.equal(kept.cpu(), ref) and new_len.tolist() == [min(m, budget) for m in lens]
+    for b, m in enumerate(lens):
+        if m > budget:
+            for h in range(2):
+                src, to = ref[b, h].long(), torch.arange(budget)
+                assert torch.equal(c.dk.cpu()[c.table[b, to // 64].long(), to % 64, h], c.k[c.table[b, src // 64].long(), src % 64, h])
+                assert torch.equal(dacc[b, h, :budget].cpu(), acc[b, h, src])
+
+
+def test_cache_past_32_bits():
+    """The same sequences in the first pages and in pages behind 2^32 elements: the same bits of every operator."""
+    Hq, Hkv, D, page, lens, q_len = 16, 8, 128, 64, [200, 64, 1], [9, 1, 1]
+    c = R.Cache(31, lens, Hkv, D, page)
+    total = (1 << 32) // (page * Hkv * D) + c.pages + 3
+    shift = total - c.pages
+    start, n = _dev32(_starts(q_len)), sum(q_len)
+    g = _gen(3)
+    q, k, v = (torch.randn(n, h, D, generator=g).bfloat16().to(DEV) for h in (Hq, Hkv, Hkv))
+    freq, pos = torch.from_numpy(oes.rope_freqs(D)[0]).to(DEV), torch.arange(n, dtype=torch.int32, device=DEV)
+    got = []
+    for at in (0, shift):
+        dk, dv = (torch.empty(total if at else c.pages, page, Hkv, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        dk[at:at + c.pages], dv[at:at + c.pages] = c.dk, c.dv
+        kv = oes.KvPages(dk, dv, c.dtable + at, c.dlen)
+        q_out, out, lse = torch.empty_like(q), torch.empty_like(q), torch.empty(n, Hq, device=DEV)
+        acc = torch.zeros(3, Hkv, c.cols * page, device=DEV)
+        kept, new_len = torch.empty(3, Hkv, 50, dtype=torch.int32, device=DEV), torch.empty(3, dtype=torch.int32, device=DEV)
+        oes.rope_append(q, q_out, k, v, freq, pos, kv, start)
+        oes.attn(q_out, out, kv, start, D ** -0.5, torch.empty(oes.attn_workspace_bytes(kv, Hq, n), dtype=torch.uint8, device=DEV), lse=lse)
+        oes.attn_weigh(q_out, lse, kv, start, D ** -0.5, acc)
+        oes.kv_evict(kv, acc, 50, kept, new_len, torch.empty(oes.kv_evict_workspace_bytes(kv, 50), dtype=torch.uint8, device=DEV), 4, 8)
+        kv.check()
+        got.append((q_out, out, lse, acc, kept, new_len, dk[at:at + c.pages].clone(), dv[at:at + c.pages].clone()))
+        del dk, dv, kv
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert (got[0][4][0] >= 0).all()
+
+
+def test_two_graphs_at_once():
+    """Two captured steps of two layers, with workspaces of their own, replayed on two streams at the same time."""
+    refs, layers, graphs, states = [], [], [], []
+    for i in range(2):
+        for into in (refs, layers):
+            d = _layer(40 + i)
+            d["c"].dlen.copy_(_dev32([6, 41 + i, 60]))
+            into.append(d)
+        _layer_step(refs[i])
+        d = layers[i]
+        states.append([d["acc"].clone(), d["c"].dk.clone(), d["c"].dv.clone(), d["c"].dlen.clone()])
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            _layer_step(d)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(4):
+        for d, s in zip(layers, states):
+            for to, x in zip((d["acc"], d["c"].dk, d["c"].dv, d["c"].dlen), s):
+                to.copy_(x)
+            for k in ("out", "lse", "y", "kept"):
+                d[k].zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for d, r in zip(layers, refs):
+            assert all(torch.equal(d[k], r[k]) for k in ("qkv", "out", "lse", "acc", "y", "kept"))
+            assert torch.equal(d["c"].dk, r["c"].dk) and torch.equal(d["c"].dv, r["c"].dv)
