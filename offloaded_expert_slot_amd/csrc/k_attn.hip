@@ -247,7 +247,8 @@ template <int DP, bool FP8, bool TILE>
 struct Shape {
   static constexpr int waves = TILE ? 4 : (DP == 256 ? 2 : 4);
   static constexpr int entries = TILE ? 64 : 32;            // of an LDS tile
-  static constexpr int buffers = FP8 && !TILE ? 1 : 2;
+  // (64-wide heads: loads two tiles ahead, since a tile's products take less than a load)
+  static constexpr int buffers = FP8 && !TILE ? 1 : (TILE && !FP8 && DP == 64 ? 3 : 2);
   static constexpr int copies = TILE ? 1 : waves;           // SPLIT: a tile per wave
   static constexpr int tile_bytes = entries * DP * 2;       // K; V as much again
   static constexpr int lds = copies * buffers * 2 * tile_bytes;
@@ -456,15 +457,23 @@ __global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8,
     // (0 * inf): it is cleared in LDS, and added behind the loop to the rows that see it.  Whether there was one in
     // the rows that this wave stages.
     auto clear_odd = [&](int buf) {
-      uint32_t *v = reinterpret_cast<uint32_t *>(tiles + buf * 2 * S::tile_bytes + S::tile_bytes + wave * own0 * DP * 2);
-      bool any = false;
+      uint8_t *rows = tiles + buf * 2 * S::tile_bytes + S::tile_bytes + wave * own0 * DP * 2;
+      auto odd_bits = [](uint32_t w) { return ((w & 0x7fff7fffu) + 0x00800080u) & 0x80008000u; };  // exponents of all ones
+      uint32_t any = 0;
+#pragma unroll
+      for (int i = 0; i < S::own * DP / 512; ++i) {
+        const u32x4 w = reinterpret_cast<const u32x4 *>(rows)[i * 64 + lane];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) any |= odd_bits(w[y]);
+      }
+      if (!__any(any != 0)) return false;
+      uint32_t *v = reinterpret_cast<uint32_t *>(rows);
 #pragma unroll 1
       for (int i = lane; i < S::own * DP / 2; i += 64) {
-        const uint32_t w = v[i], e = ((w & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;  // exponents of all ones
-        if (e) v[i] = w & ~((e >> 15) * 0xffffu);
-        any |= e != 0;
+        const uint32_t e = odd_bits(v[i]);
+        if (e) v[i] &= ~((e >> 15) * 0xffffu);
       }
-      return __any(any) != 0;
+      return true;
     };
 
     // ---- one tile of entries
@@ -489,12 +498,16 @@ __global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8,
         const int at = j0 + 4 * half, lo_at = lo - at, hi_at = min(hi, to) - at;
         const uint64_t bits = paged >> (4 * half);
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
+        for (int kt = 0; kt < KT; ++kt) {
+          // bit e: the row sees entry 32 kt + e.  Bit to sign to select: two operations a score, where comparing took five
+          const int l0 = min(max(lo_at - 32 * kt, 0), 32), h0 = min(max(hi_at - 32 * kt, 0), 32);
+          const uint32_t seen = (uint32_t)((1ull << h0) - 1) & ~(uint32_t)((1ull << l0) - 1) & (uint32_t)(bits >> (32 * kt));
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int e = kt * 32 + 8 * (i / 4) + i % 4;
-            if (e < lo_at || e >= hi_at || !((bits >> e) & 1)) s[kt][i] = -INFINITY;
+            const int e = 8 * (i / 4) + i % 4, keep = (int)(seen << (31 - e)) >> 31;
+            s[kt][i] = __uint_as_float((__float_as_uint(s[kt][i]) & keep) | (0xff800000u & ~keep));
           }
+        }
       }
       float mx = s[0][0];
 #pragma unroll
@@ -550,23 +563,51 @@ __global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8,
 
     // ---- the loop: loads of the next tile run under the products of this one
     bool odd = false;
-    if (j_first < to) {
+    if (TILE && j_first < to) {
+      // NB - 1 tiles are under way before the loop (FP8: one, in registers), and one more is asked for in each turn,
+      // into the buffer that the barrier has just freed
+      constexpr int AHEAD = FP8 ? 1 : NB - 1;
+      int buf = 0;
+      uint64_t paged[AHEAD + 1] = {};
+      peek(j_first);
+#pragma unroll
+      for (int x = 0; x < AHEAD; ++x) {
+        if (x == 0 || j_first + x * step < to) paged[x] = issue(j_first + x * step, x);
+        peek(j_first + (x + 1) * step);
+      }
+      for (int j0 = j_first; j0 < to; j0 += step) {
+        if (FP8)
+          store(buf);
+        else if (AHEAD > 1 && j0 + (AHEAD - 1) * step < to)
+          wait_loads<(AHEAD - 1) * 2 * LD>();
+        else
+          wait_loads<0>();
+        __syncthreads();
+        if (j0 + AHEAD * step < to) paged[AHEAD] = issue(j0 + AHEAD * step, (buf + AHEAD) % NB);
+        peek(j0 + (AHEAD + 1) * step);
+        if (t.tokens > 1 && !seen_by_all(j0)) {
+          if (clear_odd(buf)) {
+            odd = true;
+            if (lane == 0) odd_sm = 1;
+          }
+          __syncthreads();
+        }
+        compute(j0, buf, paged[0] & kAll);
+        buf = buf + 1 == NB ? 0 : buf + 1;
+#pragma unroll
+        for (int x = 0; x < AHEAD; ++x) paged[x] = paged[x + 1];
+      }
+    }
+    if (!TILE && j_first < to) {
       int buf = 0;
       peek(j_first);
       uint64_t paged = issue(j_first, 0);
       peek(j_first + step);
-      if (FP8 && !TILE) store(0);
+      if (FP8) store(0);
       for (int j0 = j_first; j0 < to; j0 += step) {
         const bool more = j0 + step < to;
         uint64_t paged_next = 0;
-        if (TILE) {
-          if (FP8)
-            store(buf);
-          else
-            wait_loads<0>();
-          __syncthreads();
-          if (more) paged_next = issue(j0 + step, buf ^ 1);
-        } else if (more) {
+        if (more) {
           paged_next = issue(j0 + step, NB == 2 ? buf ^ 1 : 0);
           if (!FP8) wait_loads<2 * LD>();
         } else if (!FP8) {
@@ -574,15 +615,9 @@ __global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8,
         }
         peek(j0 + 2 * step);
         const int at = NB == 2 ? buf : 0;
-        if (t.tokens > 1 && !seen_by_all(j0)) {
-          if (clear_odd(at)) {
-            odd = true;
-            if (TILE && lane == 0) odd_sm = 1;
-          }
-          if (TILE) __syncthreads();
-        }
+        if (t.tokens > 1 && !seen_by_all(j0)) odd |= clear_odd(at);
         compute(j0, at, paged & kAll);
-        if (!TILE && FP8 && more) store(0);
+        if (FP8 && more) store(0);
         buf ^= 1;
         paged = paged_next;
       }
