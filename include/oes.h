@@ -435,7 +435,7 @@ oes_status oes_linear(int32_t format, const void *w0, const void *w1, const void
  *              Such an entry is treated as masked and is not written; lengths
  *              and row ranges are clamped.
  * Limits: head_dim a multiple of 16 in [16, 256], page_size >= 1, kv_heads in
- * [1, 1024], batch >= 0, max_pages >= 1, max_pages * page_size <= 2^30; k, v and
+ * [1, 1024], batch in [0, 2^20], max_pages >= 1, max_pages * page_size <= 2^30; k, v and
  * their strides keep every head row 16-byte aligned; k_scale, v_scale finite
  * and positive (1 for bf16).  The struct is read during the call only. */
 typedef struct {
@@ -520,7 +520,8 @@ oes_status oes_rope_append(const oes_kv *kv, const void *q, int64_t q_row, int64
  * are fp32; the probabilities are rounded to bf16 for the product with v; out is
  * rounded to bf16 once.
  *   q, out  bf16 [n, q_heads, head_dim] with row and head strides (elements,
- *           16-byte aligned rows); lse fp32 [n, q_heads] or NULL
+ *           16-byte aligned rows); out must not overlap q or the cache; lse fp32
+ *           [n, q_heads] or NULL
  *   q_heads a multiple of kv_heads, q_heads / kv_heads <= 128; scale * k_scale
  *   in [1e-30, 1e30]; window >= 0 (0: none)
  *   workspace: device, 16-byte aligned, >= oes_attn_workspace bytes for the
@@ -556,9 +557,9 @@ oes_status oes_attn_weigh(const oes_kv *kv, const void *q, int64_t q_row, int64_
  *   new_len  int32 [batch] out: min(len, budget); may be kv->len itself
  * What stands in entries from new_len on is left as it was.  A sequence of at
  * most budget entries is left untouched (kept counts up).  Pages of a sequence
- * that is cut must not be shared with another.  A sequence with a page outside
+ * that is cut must not be shared with another, nor stand in its table twice.  A sequence with a page outside
  * the cache among its used pages keeps its entries as they are (its kept is -1,
- * its new_len is len).  budget >= 1, first, last >= 0, first + last <= budget.
+ * its new_len is len).  budget in [1, 2^30], first, last >= 0, first + last <= budget.
  * workspace: device, 16-byte aligned, >= oes_kv_evict_workspace bytes.  Async. */
 oes_status oes_kv_evict_workspace(const oes_kv *kv, int32_t budget, int64_t *bytes);
 oes_status oes_kv_evict(const oes_kv *kv, float *acc, int64_t acc_stride, int32_t budget, int32_t first,

@@ -46,6 +46,7 @@ oes_status check_kv(const oes_kv *kv, bool written) {
   if (kv->kv_heads < 1 || kv->kv_heads > 1024) return fail(OES_ERR_ARG, "kv_heads %d outside [1, 1024]", kv->kv_heads);
   if (kv->page_size < 1 || kv->max_pages < 1 || kv->num_pages < 0 || kv->batch < 0)
     return fail(OES_ERR_ARG, "need page_size >= 1, max_pages >= 1, num_pages >= 0, batch >= 0");
+  if (kv->batch > (1 << 20)) return fail(OES_ERR_ARG, "batch %d exceeds 2^20", kv->batch);
   if ((int64_t)kv->page_size * kv->max_pages > (1ll << 30))
     return fail(OES_ERR_ARG, "max_pages * page_size = %lld exceeds 2^30", (long long)kv->page_size * kv->max_pages);
   if (!(kv->k_scale > 0) || !(kv->v_scale > 0) || !isfinite(kv->k_scale) || !isfinite(kv->v_scale))
@@ -325,7 +326,7 @@ extern "C" oes_status oes_kv_evict_workspace(const oes_kv *kv, int32_t budget, i
   if (!bytes) return fail(OES_ERR_ARG, "bytes is NULL");
   oes_status st = check_kv(kv, true);
   if (st != OES_OK) return st;
-  if (budget < 1) return fail(OES_ERR_ARG, "budget < 1");
+  if (budget < 1 || budget > (1 << 30)) return fail(OES_ERR_ARG, "budget %d outside [1, 2^30]", budget);
   *bytes = evict_workspace_bytes(*kv, budget);
   return OES_OK;
 }
@@ -335,8 +336,8 @@ extern "C" oes_status oes_kv_evict(const oes_kv *kv, float *acc, int64_t acc_str
                                    int64_t workspace_bytes, void *stream) {
   oes_status st = check_kv(kv, true);
   if (st != OES_OK) return st;
-  if (budget < 1 || first < 0 || last < 0 || (int64_t)first + last > budget)
-    return fail(OES_ERR_ARG, "need budget >= 1, first, last >= 0 and first + last <= budget");
+  if (budget < 1 || budget > (1 << 30) || first < 0 || last < 0 || (int64_t)first + last > budget)
+    return fail(OES_ERR_ARG, "need budget in [1, 2^30], first, last >= 0 and first + last <= budget");
   if (kv->batch == 0) return OES_OK;
   if (!acc || !kept || !new_len) return fail(OES_ERR_ARG, "acc / kept / new_len are NULL");
   if (!aligned(acc, 4) || !aligned(kept, 4) || !aligned(new_len, 4)) return fail(OES_ERR_ARG, "acc, kept and new_len must be 4-byte aligned");

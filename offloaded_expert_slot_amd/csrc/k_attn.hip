@@ -206,8 +206,9 @@ __device__ inline int all_units(const AttnArgs &a, const Plan &p, const Scan &s0
   for (int b0 = 64; b0 < a.kv.batch; b0 += 64) total = lane_value(scan_sequences(a, p, b0, total).upto, 63);
   return total;
 }
-// Where unit `u` (there is one) stands: its tile, head and place `x` among the pair's units.  Wave-wide.
-__device__ inline void find_unit(const AttnArgs &a, const Plan &p, const Scan &s0, int u, Tile &t, int *g, int *x) {
+// Where unit `u` stands: its tile, head and place `x` among the pair's units.  Wave-wide.  (There is one, unless ranges of
+// rows that overlap have made the number of units wrap.)
+__device__ inline bool find_unit(const AttnArgs &a, const Plan &p, const Scan &s0, int u, Tile &t, int *g, int *x) {
   Scan s = s0;
   for (int b0 = 0; b0 < a.kv.batch; b0 += 64) {
     if (b0) s = scan_sequences(a, p, b0, lane_value(s.upto, 63));
@@ -224,8 +225,9 @@ __device__ inline void find_unit(const AttnArgs &a, const Plan &p, const Scan &s
     }
     *g = left / (kBegin + t.parts);
     *x = left - *g * (kBegin + t.parts);
-    return;
+    return true;
   }
+  return false;
 }
 // units of a workgroup
 __device__ inline int unit_share(const Plan &p, int total) { return (total + p.blocks - 1) / p.blocks; }
@@ -322,8 +324,8 @@ __global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8,
     } else {
       if (++g < a.kv.kv_heads)
         x = 0;   // the same tile's next head
-      else
-        find_unit(a, plan, scan, unit, t, &g, &x);
+      else if (!find_unit(a, plan, scan, unit, t, &g, &x))
+        return;
       const int n = min(kBegin + t.parts - x, unit_end - unit), x1 = x + n - kBegin;
       unit += n;
       if (x1 <= 0) break;   // the share ends before the pair's first entries
@@ -786,7 +788,7 @@ __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a, Plan plan) 
   int parts = t.parts, b_first = 0;
   int64_t at0 = (int64_t)row * a.q_heads + h, stride = (int64_t)a.n * a.q_heads;   // TILE: part s at at0 + s * stride
   if (!TILE) {
-    const int share = unit_share(plan, total);
+    const int share = max(1, unit_share(plan, total));
     start += g * (kBegin + t.parts) + kBegin;
     b_first = start / share;
     parts = (start + t.parts - 1) / share - b_first + 1;
@@ -794,6 +796,7 @@ __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a, Plan plan) 
     stride = 64;
   }
   if (parts == 1) return;  // written by its workgroup
+  if (!TILE && (b_first < 0 || parts < 1 || b_first + (int64_t)parts > plan.blocks)) return;   // as in find_unit
   auto place = [&](int s) { return at0 + s * stride + (!TILE && s == 0 ? 32 : 0); };
   float mm = -INFINITY;
   for (int s = lane; s < parts; s += 64) mm = fmaxf(mm, part_stats<TILE>(a, place(s))->x);

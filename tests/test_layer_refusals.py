@@ -22,7 +22,7 @@ def kv(**over):
 
 
 BAD_KV = [dict(elem=oes.ELEM_FP16), dict(head_dim=8), dict(head_dim=72), dict(head_dim=272), dict(kv_heads=0),
-          dict(kv_heads=1025), dict(page_size=0), dict(max_pages=0), dict(batch=-1), dict(num_pages=-1),
+          dict(kv_heads=1025), dict(page_size=0), dict(max_pages=0), dict(batch=-1), dict(batch=(1 << 20) + 1), dict(num_pages=-1),
           dict(page_size=1 << 20, max_pages=1 << 11, table_stride=1 << 11), dict(k_scale=0.0), dict(k_scale=math.nan),
           dict(v_scale=math.inf), dict(v_scale=-1.0), dict(k_scale=0.5), dict(k=0), dict(v=0), dict(table=0), dict(len=0),
           dict(table_stride=3), dict(table=A + 2), dict(status=A + 1), dict(k_head=60), dict(k_row=-128), dict(k=A + 8),
@@ -86,7 +86,7 @@ def test_attn_refuses_a_short_workspace():
 
 def test_weigh_and_evict_refuse():
     assert weigh(kv(), acc=0) == weigh(kv(), acc=A + 2) == weigh(kv(), stride=31) == weigh(kv(), lse=0) == oes.ERR_ARG
-    for bad in (dict(acc=0), dict(stride=31), dict(budget=0), dict(first=-1), dict(last=-1), dict(first=5, last=4),
+    for bad in (dict(acc=0), dict(stride=31), dict(budget=0), dict(budget=(1 << 30) + 1), dict(first=-1), dict(last=-1), dict(first=5, last=4),
                 dict(first=(1 << 31) - 1, last=(1 << 31) - 1), dict(kept=0), dict(new_len=0), dict(ws=0), dict(ws=A + 8),
                 dict(ws_bytes=1)):
         assert evict(kv(), **bad) == oes.ERR_ARG, bad
