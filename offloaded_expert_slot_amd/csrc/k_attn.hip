@@ -14,6 +14,11 @@
 // register i of lane (c, h) is entry 8 (i / 4) + 4 h + i % 4; the sum over entries may
 // run in any order, so the V operand is read in that order.)
 //
+// Bound by the matrix units with many rows (2048 tokens x 32 heads over 24111 entries of 128 values: 0.80 ms, 970
+// TFLOP/s), by reading the cache once in decode steps (32 sequences of 1 .. 16384 e4m3 entries: 30 us, 3.9 TB/s).  With
+// a window of 128 (2023 tokens x 64 heads of 64 values) a tile sees some four tiles of entries, nearly all masked in
+// part: 24 us, of them some 11 in each of two rounds of workgroups.
+//
 // Two shapes:
 //   TILE    128 rows, 32 to each of 4 waves, which share tiles of 64 entries.  With few tiles
 //           of rows the entries are split over several workgroups.
@@ -267,7 +272,7 @@ __global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8,
   constexpr uint64_t kAll = E == 64 ? ~0ull : 0xffffffffull;
   __shared__ __attribute__((aligned(16))) uint8_t sm[S::lds];
   __shared__ float jm[4][32], jl[4][32];
-  __shared__ int odd_sm;
+  __shared__ int odd_sm, j_row[32], j_head[32];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c = lane & 31, half = lane >> 5;
   const int D = a.kv.head_dim, G = a.q_heads / a.kv.kv_heads, shift = a.shift;
   const float cs = a.scale * a.kv.k_scale * kLog2e;
@@ -280,8 +285,8 @@ __global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8,
   constexpr int GR = S::own / 16, LG = 16 / RPI, NG = E / 16;   // groups of 16 rows; loads of a group
   uint8_t *tiles = sm + (TILE ? 0 : wave * NB * 2 * S::tile_bytes);
   // Whole tiles of pages of 16 entries and more: 16 rows stand in one page, so their addresses are a scalar base
-  // and an offset that the lane keeps (with an address of its own per lane and load, the long chunk of 2048 tokens
-  // at 24111 entries took 1.29 ms; see below).  Page numbers are read a tile ahead, through the scalar cache.
+  // and an offset that the lane keeps (with an address of its own per lane and load, 2048 tokens at 24111 entries took
+  // 1.29 ms).  Page numbers are read a tile ahead, through the scalar cache.
   const bool paged16 = shift >= 4 && D == DP && (a.kv.k_row | a.kv.v_row) < (1 << 22);
   // (FP8: neighbouring lanes take different rows, whose bf16 chunks go to different banks)
   auto lane_row = [](int ln) { return FP8 ? ln % RPI : ln / CPR; };
@@ -714,11 +719,16 @@ __global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8,
         jm[wave][c] = m;
         jl[wave][c] = l;
       }
+      if (wave == 0 && half == 0) {
+        j_row[c] = row_t;
+        j_head[c] = row_h;
+      }
     }
     __syncthreads();
-    for (int it = threadIdx.x; it < t.tokens * G * (D / 4); it += S::waves * 64) {
-      const int jr = it / (D / 4), d4 = (it - jr * (D / 4)) * 4;
-      const int jt = jr / G, rt = t.first + t.t0 + jt, rh_ = g * G + (jr - jt * G);
+    for (int it = threadIdx.x; it < t.tokens * G * (DP / 4); it += S::waves * 64) {
+      const int jr = it / (DP / 4), d4 = it % (DP / 4) * 4;
+      if (d4 >= D) continue;
+      const int rt = j_row[jr], rh_ = j_head[jr];
       float mm = jm[0][jr];
 #pragma unroll
       for (int w = 1; w < S::waves; ++w) mm = fmaxf(mm, jm[w][jr]);
@@ -841,7 +851,9 @@ __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a, Plan plan) 
 // of the RG waves are joined through LDS at the end.  No two workgroups share an entry, so
 // nothing is added atomically.  Bound by the exponentials (one
 // for each entry, row pair, with a multiply-add and an add) rather than by the product.
-// (With one wave for 32 entries the 8111 entries of 8 heads and 1000 new tokens took 196 us, with two 125.)
+// (8111 entries of 8 heads, 1000 new tokens: with one wave for 32 entries 196 us, with two 125.)  While a CU is busy its
+// SIMDs issue vector or matrix instructions all the time, 3 : 1.  Products of the next rows between the exponentials of
+// these, four tiles of rows under way, or the sequences with most rows first did not help (143 -> 166, 194, 187 us).
 constexpr int RG = 2;
 template <int DP>
 struct WeighShape {

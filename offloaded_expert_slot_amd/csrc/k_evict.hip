@@ -3,10 +3,12 @@
 //   evict_select  one workgroup per (sequence, head).  Every entry gets a 32-bit key
 //                 that orders as its weight does (NaN lowest, -0 as 0); the first and
 //                 last ones are always kept.  The smallest kept key is found by a radix
-//                 select, 8 bits a pass, on keys that stay in registers (16 a thread; more
-//                 than 16384 entries are read again in each pass).  Then the kept entries'
-//                 ranks, from one ordered sum over the waves' counts (equal keys: the
-//                 lowest indices stay), place their indices and weights.
+//                 select, 8 bits a pass until a digit's keys all stay, on weights that stay
+//                 in LDS (more than 16384 are read again in each pass).  Then the kept
+//                 entries' ranks, from one ordered sum over the threads' counts (equal keys:
+//                 the lowest indices stay), place their indices and weights.  Short loops: in
+//                 a launch of 10 us code that runs once waits for its instructions (with the
+//                 weights in registers and 16-fold unrolled loops the ranks alone took 3.6).
 //   evict_move    moves the k and v rows.  Entry i comes from kept[i] >= i, so going up in
 //                 batches that are read whole before they are written is safe in place:
 //                 a row i in the batch [i0, i1) that is itself kept has a rank <= i, so
@@ -15,6 +17,8 @@
 //                 writes).  Head rows are cut into columns of 128 bytes, and each
 //                 workgroup moves one column of one (sequence, head); bound by reading and
 //                 writing the moved rows once.
+// 16 sequences x 4 heads from 2080 to 2048 bf16 rows of 128: select 10.6 us, move 28.0; 4 x 8 heads from 9204 .. 15074
+// to 4099: 24 + 44.
 
 #include "layer_device.h"
 #include "oes_internal.h"
@@ -23,7 +27,7 @@ namespace oes {
 
 namespace {
 
-constexpr int kSel = 1024, kWaves = kSel / 64, kHold = 16, kChunk = kSel * kHold;
+constexpr int kSel = 1024, kWaves = kSel / 64, kChunk = 16 * kSel;
 constexpr int kCopies = 16;   // of the histogram, by lane: the leading digits of most keys are the same
 
 __device__ inline uint32_t weight_key(float v) {
@@ -44,9 +48,10 @@ __device__ inline int scan64(int v) {  // inclusive, over the wave
 
 // ws: per (sequence, head) the first entry that moves and the new length (the same: none moves)
 __global__ __launch_bounds__(kSel) void evict_select_kernel(EvictArgs a) {
-  __shared__ __attribute__((aligned(16))) int hist[256 * kCopies];
-  __shared__ int counts[kHold * kWaves], sh[4];
-  const int bh = blockIdx.x, b = bh / a.kv.kv_heads, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ __attribute__((aligned(16))) int hists[2][256 * kCopies];   // of a pass, and cleared for the next one
+  __shared__ __attribute__((aligned(16))) float vals[kChunk];                                         // the weights, a chunk at a time
+  __shared__ int sums[kWaves], sh[4];
+  const int bh = blockIdx.x, b = bh / a.kv.kv_heads, tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   bool bad = false;
   const int len = kv_len(a.kv, a.kv.len[b], &bad);
   int32_t *kept = a.kept + (int64_t)bh * a.budget;
@@ -54,10 +59,16 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(EvictArgs a) {
   // every page that the sequence uses has to be one of the cache
   const int32_t *table = a.kv.table + b * a.kv.table_stride;
   const int cols = (int)(((int64_t)len + a.kv.page_size - 1) / a.kv.page_size);
+  static_assert(256 * kCopies == 4 * kSel, "16 bytes a thread");
+  reinterpret_cast<int4 *>(hists[0])[tid] = int4{0, 0, 0, 0};
   if (tid == 0) {
     sh[0] = 0;
     sh[3] = len;
   }
+  auto load = [&](int base) {   // a chunk, to LDS
+    for (int j = tid; j < min(kChunk, len - base); j += kSel) vals[j] = acc[base + j];
+  };
+  if (len > a.budget && len <= kChunk) load(0);
   __syncthreads();
   for (int c = tid; c < cols; c += kSel)
     if (table[c] < 0 || table[c] >= a.kv.num_pages) sh[0] = 1;
@@ -71,32 +82,28 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(EvictArgs a) {
   }
   const int mid0 = a.first, mid1 = len - a.last;    // entries that have to earn their place
   const int want = a.budget - a.first - a.last;     // of them stay
-  float v[kHold];
-  auto load = [&](int base) {
-#pragma unroll
-    for (int x = 0; x < kHold; ++x) {
-      if (base + x * kSel >= len) break;
-      const int j = base + x * kSel + tid;
-      v[x] = j < len ? acc[j] : 0.f;
-    }
-  };
-  if (len <= kChunk) load(0);
   uint32_t prefix = 0, mask = 0;
   int left = want;                                  // still wanted among the keys of this prefix
   for (int shift = 24; shift >= 0 && want > 0; shift -= 8) {
-    for (int i = tid; i < 256 * kCopies; i += kSel) hist[i] = 0;
-    __syncthreads();
+    int *hist = hists[((shift >> 3) & 1) ^ 1];
     for (int base = 0; base < len; base += kChunk) {
-      if (len > kChunk) load(base);
+      if (len > kChunk) {
+        __syncthreads();
+        load(base);
+        __syncthreads();
+      }
+      for (int j0 = base + 4 * tid; j0 < min(mid1, base + kChunk); j0 += 4 * kSel) {
+        const float4 v = *reinterpret_cast<const float4 *>(vals + (j0 - base));
+        const float v4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int x = 0; x < kHold; ++x) {
-        if (base + x * kSel >= len) break;
-        const int j = base + x * kSel + tid;
-        const uint32_t k = weight_key(v[x]);
-        if (j >= mid0 && j < mid1 && (k & mask) == prefix) atomicAdd(&hist[((k >> shift) & 255) * kCopies + (lane & (kCopies - 1))], 1);
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t k = weight_key(v4[e]);
+          if (j0 + e >= mid0 && j0 + e < mid1 && (k & mask) == prefix) atomicAdd(&hist[((k >> shift) & 255) * kCopies + (lane & (kCopies - 1))], 1);
+        }
       }
     }
     __syncthreads();
+    reinterpret_cast<int4 *>(hists[(shift >> 3) & 1])[tid] = int4{0, 0, 0, 0};
     if (wave == 0) {
       // lane l: digits 255 - 4 l down to 252 - 4 l, so that the running sum goes from the largest down
       int n[4], sum = 0;
@@ -114,6 +121,7 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(EvictArgs a) {
         if (above < left && above + n[d] >= left) {
           sh[1] = 255 - 4 * lane - d;
           sh[2] = left - above;
+          sh[0] = n[d] == left - above;   // all keys of this digit stay: the others' digits are the same to it
         }
         above += n[d];
       }
@@ -122,84 +130,52 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(EvictArgs a) {
     prefix |= (uint32_t)sh[1] << shift;
     mask |= 255u << shift;
     left = sh[2];
+    if (sh[0]) break;
   }
-  // Exclusive sum over (stretch, wave), in the order of the entries, of counts[stretch * waves + wave]; all threads.
-  auto ranks = [&](int *total) {
-    __syncthreads();
-    if (wave == 0) {
-      constexpr int kPer = kHold * kWaves / 64;
-      int n[kPer], sum = 0;
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) {
-        n[x] = counts[lane * kPer + x];
-        sum += n[x];
-      }
-      const int upto = scan64(sum);
-      int at = upto - sum;
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) {
-        counts[lane * kPer + x] = at;
-        at += n[x];
-      }
-      if (lane == 63) sh[1] = upto;
-    }
-    __syncthreads();
-    *total = sh[1];
-  };
-  // keys above prefix stay, and the `left` lowest-indexed ones equal to it
-  int at = 0, eq_at = 0;
-  const uint64_t below = (1ull << lane) - 1;
+  // Keys above prefix (as far as their digits were looked at) stay, and the `left` lowest-indexed ones equal to it.  A
+  // thread takes neighbouring entries of the chunk (an odd number: different banks), so that one sum over the threads
+  // gives all ranks.
+  uint16_t *list = reinterpret_cast<uint16_t *>(hists);   // what stays of a chunk, in order
+  static_assert(sizeof(hists) == 2 * kChunk, "an index each");
+  int at = 0, eq_at = 0;   // entries that stay, and equal ones, of the chunks before
   for (int base = 0; base < len; base += kChunk) {
     if (len > kChunk) load(base);
-    uint32_t stay = 0, eq = 0;   // bit x: the thread's entry of stretch x
-#pragma unroll
-    for (int x = 0; x < kHold; ++x) {
-      if (base + x * kSel >= len) {   // (the same in every thread; the sums go over all stretches)
-        if (lane == 0) counts[x * kWaves + wave] = 0;
-        continue;
-      }
-      const int j = base + x * kSel + tid;
-      const uint32_t k = weight_key(v[x]);
-      const bool in = j < len, mid = j >= mid0 && j < mid1;
-      if (in && (!mid || (want > 0 && k > prefix))) stay |= 1u << x;
-      const bool same = in && mid && want > 0 && k == prefix;
-      if (same) eq |= 1u << x;
-      const uint64_t m = __ballot(same);
-      if (lane == 0) counts[x * kWaves + wave] = __popcll(m);
-    }
-    int total;
-    ranks(&total);
-#pragma unroll
-    for (int x = 0; x < kHold; ++x) {
-      if (base + x * kSel >= len) break;
-      const uint64_t m = __ballot((eq >> x) & 1);
-      if (((eq >> x) & 1) && eq_at + counts[x * kWaves + wave] + __popcll(m & below) < left) stay |= 1u << x;
-    }
-    eq_at += total;
     __syncthreads();
-#pragma unroll
-    for (int x = 0; x < kHold; ++x) {
-      const uint64_t m = __ballot((stay >> x) & 1);
-      if (lane == 0) counts[x * kWaves + wave] = __popcll(m);
-      if (base + x * kSel >= len) continue;
-      const uint64_t gone = __ballot(base + x * kSel + tid < len && !((stay >> x) & 1));
-      if (lane == 0 && gone) atomicMin(&sh[3], base + x * kSel + wave * 64 + __builtin_ctzll(gone));
+    const int n = min(kChunk, len - base), per = ((n + kSel - 1) / kSel) | 1, i0 = tid * per, i1 = min(n, i0 + per);
+    uint32_t sure = 0, same = 0;   // bit i - i0: stays, is equal (at most 17 entries)
+#pragma unroll 4
+    for (int i = i0; i < i1; ++i) {
+      const int j = base + i;
+      const uint32_t k = weight_key(vals[i]) & mask;
+      const bool mid = j >= mid0 && j < mid1;
+      if (!mid || (want > 0 && k > prefix)) sure |= 1u << (i - i0);
+      if (mid && want > 0 && k == prefix) same |= 1u << (i - i0);
     }
-    ranks(&total);
-    // every thread has the weights of this chunk in registers, and places up to here are free
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const int mine = __popc(sure) | __popc(same) << 16;   // (of a chunk at most 16384 each)
+    const int upto = scan64(mine);
+    if (lane == 63) sums[wave] = upto;
     __syncthreads();
-#pragma unroll
-    for (int x = 0; x < kHold; ++x) {
-      if (base + x * kSel >= len) break;
-      const uint64_t m = __ballot((stay >> x) & 1);
-      if ((stay >> x) & 1) {
-        const int j = base + x * kSel + tid, pos = at + counts[x * kWaves + wave] + __popcll(m & below);
-        kept[pos] = j;
-        if (pos != j) acc[pos] = v[x];
-      }
+    const int waves = scan64(lane < kWaves ? sums[lane] : 0), all = __builtin_amdgcn_readlane(waves, kWaves - 1);
+    const int before = upto - mine + (wave > 0 ? __builtin_amdgcn_readlane(waves, max(wave, 1) - 1) : 0);
+    int eq = eq_at + (before >> 16);
+    int pos = at + (before & 0xffff) + min(eq, left) - min(eq_at, left);
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+      if (((sure >> (i - i0)) & 1) || (((same >> (i - i0)) & 1) && eq++ < left))
+        list[pos++ - at] = (uint16_t)i;
+      else if (pos == base + i)
+        sh[3] = pos;   // the first one that goes
     }
-    at += total;
+    const int stay = (all & 0xffff) + min(eq_at + (all >> 16), left) - min(eq_at, left);
+    __syncthreads();
+#pragma unroll 2
+    for (int x = tid; x < stay; x += kSel) {
+      const int i = list[x];
+      kept[at + x] = base + i;
+      if (x + at != base + i) acc[at + x] = vals[i];   // (a place before the entry's: that one has been read)
+    }
+    at += stay;
+    eq_at += all >> 16;
     __syncthreads();
   }
   if (tid == 0) {
@@ -211,7 +187,6 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(EvictArgs a) {
 // 256 rows of 128 bytes in flight per workgroup.  (16 x 4 heads of 2048 bf16 rows, 256 workgroups: 28.9 us; with 512
 // threads and 4 rows a thread 37; 64-byte columns, twice the workgroups, 38.)
 constexpr int kMove = 1024, kUnroll = 2, kRows = kMove / 8, kBatch = kRows * kUnroll;
-
 
 __global__ __launch_bounds__(kMove) void evict_move_kernel(EvictArgs a, int columns, int shift) {
   const int bh = blockIdx.x / columns, column = blockIdx.x - bh * columns;

@@ -12,7 +12,8 @@
 // pieces (rot_dim no multiple of 16), a lane takes single pairs.
 //
 // The number of workgroups is bounded, since starting one costs some 4 ns of the launch: with
-// one for each of 8740 tokens of 80 heads, pair by pair, the launch took 182 us.
+// one for each of 8740 tokens of 80 heads, pair by pair, the launch took 182 us; it takes 83 (4.1 TB/s), and 5.7 for 32
+// decoded tokens.
 
 #include <algorithm>
 

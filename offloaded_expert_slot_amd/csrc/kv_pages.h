@@ -65,9 +65,9 @@ OES_HD int32_t kv_rows(int32_t start, int32_t end, int32_t n, int32_t *first, bo
 
 // Entries [*lo, *hi) that token i of q_len new ones sees in a cache of len entries.
 OES_HD void kv_seen(int32_t len, int32_t q_len, int32_t i, int32_t window, int32_t *lo, int32_t *hi) {
-  const int64_t at = (int64_t)len - q_len + i;  // its own entry; < 0: none
-  *hi = at < 0 ? 0 : (int32_t)(at + 1);
-  *lo = window > 0 && at - window >= 0 ? (int32_t)(at - window + 1) : 0;
+  const int32_t at = len - q_len + i;  // its own entry; < 0: none (0 <= len <= 2^30, 0 <= i < q_len: in 32 bits)
+  *hi = at < 0 ? 0 : at + 1;
+  *lo = window > 0 && at >= window ? at - window + 1 : 0;
 }
 
 }  // namespace oes
