@@ -478,7 +478,8 @@ oes_status oes_rope_freqs(int32_t scaling, int32_t rot_dim, double base, double 
  * where pair i is (i, i + rot_dim / 2) for OES_ROPE_HALF and (2 i, 2 i + 1) for
  * OES_ROPE_INTERLEAVED; values behind rot_dim are copied.  The angle is formed
  * and reduced in fp64 (positions of any size keep their accuracy), sine,
- * cosine and products are fp32, y is rounded to bf16 once.
+ * cosine and products are fp32 (or better, for k in an e4m3 cache), y is rounded to bf16
+ * once.
  *   x, y   bf16 [n, heads, head_dim]: token t, head h at t * row + h * head
  *          elements; y may be x (then with the same strides), otherwise they
  *          must not overlap

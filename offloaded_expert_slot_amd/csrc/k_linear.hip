@@ -1,7 +1,7 @@
 // y = x . W^T for 4-bit weights with group scales, in the layouts of the expert banks.
 //
 // Bound by reading the weights (4.5 bits each and nothing twice) up to some 64 tokens: nvfp4 100003 x 7168 at 16 tokens
-// 107 us, 3.8 TB/s; small ones by latency: q4_0 5120 x 2048 for one token 4.5 us.  A
+// 102 us, 4.0 TB/s; small ones by latency: q4_0 5120 x 2048 for one token 5.3 us.  A
 // wave takes R tiles of 16 weight rows and multiplies them with up to 16 NT tokens by
 // v_mfma_f32_16x16x32_bf16 (A = tokens, B = weights: a lane's accumulators are 4 tokens of
 // one weight row).  A step covers 256 of K: two 16-byte loads per lane and tile, into one of
@@ -352,7 +352,7 @@ template <int FMT>
 hipError_t launch_format(const LinearArgs &a, hipStream_t s) {
   const int64_t tiles = (a.N + 15) / 16;
   // From 1536 row tiles on: two tiles a wave, 8 waves of rows share x, up to 64 tokens at a time (nvfp4 at
-  // 100003 x 7168: 106 us at 16 tokens, 127 at 32, 167 at 64; with one tile a wave 114 at 16).
+  // 100003 x 7168: 102 us at 16 tokens, 164 at 40; with one tile a wave 114 at 16).
   if (tiles >= 1536) {
     if (a.n <= 16) return launch_shape<FMT, 2, 1, 8, 1, 2>(a, s);
     if (a.n <= 32) return launch_shape<FMT, 2, 2, 8, 1, 2>(a, s);

@@ -4,15 +4,18 @@
 // heads; the token's rot_dim / 2 sines and cosines are formed once per wave, in LDS: the
 // angle pos * freq in fp64, reduced to an eighth of a turn, sine and cosine by their series in
 // fp64 and rounded to fp32 once, with mscale (a position of a million keeps 2^-30 of a turn,
-// where an fp32 product would lose 0.06 radians; with sines of fp32 more e4m3 entries came
-// out on the wrong side of a border, and the launch took as long).  An item is 16 values of a head: two 16-byte pieces that hold 8
+// where an fp32 product would lose 0.06 radians).  Products are fp32; but for keys of an e4m3
+// cache an error of 2^-24 now and then crosses a border and costs 2^-4, so where one is near
+// they are formed anew in fp64 and rounded to fp32 once (of 4.5 million entries some 2 come
+// out on another side than in 64 bits, in place of 5; all in fp64 8740 tokens took 94 us in
+// place of 83).  An item is 16 values of a head: two 16-byte pieces that hold 8
 // pairs (values i .. i + 7 and their partners, half a rotation away or next to them), or that
 // are copied.  A lane reads both pieces before it writes them, and no other lane touches
 // them, so a call in place is safe.  Where the pairs of the half layout do not fall into whole
 // pieces (rot_dim no multiple of 16), a lane takes single pairs.
 //
 // The number of workgroups is bounded, since starting one costs some 4 ns of the launch: with
-// one for each of 8740 tokens of 80 heads, pair by pair, the launch took 182 us; it takes 83 (4.1 TB/s), and 5.7 for 32
+// one for each of 8740 tokens of 80 heads, pair by pair, the launch took 182 us; it takes 83 (4.1 TB/s), and 5.2 for 32
 // decoded tokens.
 
 #include <algorithm>
@@ -109,9 +112,14 @@ __device__ inline void turn_by(double turns, double *c, double *s) {
   *s = k == 0 ? sx : (k == 1 ? cx : (k == 2 ? -sx : -cx));
 }
 
-template <bool INTERLEAVED, bool PIECES>
-__global__ __launch_bounds__(kWaves * 64) void rope_kernel(RopeArgs a, int parts, int shift) {
+// Whether a value's e4m3 rounding (20 bits below the last one kept) depends on its last three bits.
+__device__ inline bool near_border(float v) { return (__float_as_uint(v) & 0xfffffu) - 0x7fff8u < 16u; }
+
+template <bool INTERLEAVED, bool PIECES, bool FP8>
+__global__ __launch_bounds__(kWaves * 64, 3) void rope_kernel(RopeArgs a, int parts, int shift) {
   __shared__ __attribute__((aligned(16))) float cs[kWaves][128], sn[kWaves][128];
+  __shared__ float cs_low[FP8 ? kWaves : 1][128], sn_low[FP8 ? kWaves : 1][128];   // what fp32 leaves of them
+  const float per_scale = FP8 ? 1.f / a.kv.k_scale : 0.f;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, D = a.head_dim, half = a.rot_dim / 2;
   const int per = PIECES ? D / 16 : D / 2;         // items (or pairs) of a head
   const int heads = a.heads + (a.append ? 2 * a.kv.kv_heads : 0);
@@ -129,8 +137,14 @@ __global__ __launch_bounds__(kWaves * 64) void rope_kernel(RopeArgs a, int parts
     for (int i = lane; i < half; i += 64) {
       double c, s;
       turn_by(pos * a.freq[i] * 0.15915494309189533577, &c, &s);
-      cs[wave][i] = (float)(c * a.mscale);
-      sn[wave][i] = (float)(s * a.mscale);
+      c *= a.mscale;
+      s *= a.mscale;
+      cs[wave][i] = (float)c;
+      sn[wave][i] = (float)s;
+      if (FP8) {
+        cs_low[wave][i] = (float)(c - (float)c);
+        sn_low[wave][i] = (float)(s - (float)s);
+      }
     }
     __builtin_amdgcn_wave_barrier();   // one wave's LDS operations run in order
     const int pass0 = (int)((int64_t)passes * part / parts), pass1 = (int)((int64_t)passes * (part + 1) / parts);
@@ -165,20 +179,41 @@ __global__ __launch_bounds__(kWaves * 64) void rope_kernel(RopeArgs a, int parts
           const bool turn = turns && h[u].turn;
           float y0[8], y1[8];
           if (turn) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              // pair i: INTERLEAVED, the two halves of word i of the 16 values; else value i of either piece
+            // pair i: INTERLEAVED, the two halves of word i of the 16 values; else value i of either piece
+            auto pair = [&](int i, float *x0, float *x1) {
               const uint32_t w0 = INTERLEAVED ? (i < 4 ? r0[u][i] : r1[u][i - 4]) : r0[u][i / 2], w1 = r1[u][i / 2];
-              const float x0 = INTERLEAVED ? bf16_lo(w0) : (i & 1 ? bf16_hi(w0) : bf16_lo(w0));
-              const float x1 = INTERLEAVED ? bf16_hi(w0) : (i & 1 ? bf16_hi(w1) : bf16_lo(w1));
-              float v0 = x0 * c8[i] - x1 * s8[i], v1 = x0 * s8[i] + x1 * c8[i];
+              *x0 = INTERLEAVED ? bf16_lo(w0) : (i & 1 ? bf16_hi(w0) : bf16_lo(w0));
+              *x1 = INTERLEAVED ? bf16_hi(w0) : (i & 1 ? bf16_hi(w1) : bf16_lo(w1));
+            };
+            auto put = [&](int i, float v0, float v1) {
               if (INTERLEAVED) {
-                if (8 * j + i >= half) v0 = x0, v1 = x1;   // rot_dim ends within the item
                 (i < 4 ? y0 : y1)[2 * (i & 3)] = v0;
                 (i < 4 ? y0 : y1)[2 * (i & 3) + 1] = v1;
               } else {
                 y0[i] = v0;
                 y1[i] = v1;
+              }
+            };
+            bool close = false;   // to a border of e4m3 rounding
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float x0, x1;
+              pair(i, &x0, &x1);
+              float v0 = x0 * c8[i] - x1 * s8[i], v1 = x0 * s8[i] + x1 * c8[i];
+              if (INTERLEAVED && 8 * j + i >= half) v0 = x0, v1 = x1;   // rot_dim ends within the item
+              if (FP8) close |= near_border(v0 * per_scale) | near_border(v1 * per_scale);
+              put(i, v0, v1);
+            }
+            if (FP8 && close && h[u].scale > 0.f) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                int pr = 8 * j + i;
+                asm volatile("" : "+v"(pr));   // (or the tables are read before the branch)
+                if (INTERLEAVED && pr >= half) continue;
+                float x0, x1;
+                pair(i, &x0, &x1);
+                const double c = (double)cs[wave][pr] + cs_low[wave][pr], s = (double)sn[wave][pr] + sn_low[wave][pr];
+                put(i, (float)(x0 * c - x1 * s), (float)(x0 * s + x1 * c));
               }
             }
           }
@@ -195,9 +230,15 @@ __global__ __launch_bounds__(kWaves * 64) void rope_kernel(RopeArgs a, int parts
           const float x0 = bf16f(h.src[e0]), x1 = bf16f(h.src[e1]);
           float v0 = x0, v1 = x1;
           if (i < half && h.turn) {
-            const float c = cs[wave][i], s = sn[wave][i];
-            v0 = x0 * c - x1 * s;
-            v1 = x0 * s + x1 * c;
+            if (FP8 && h.scale > 0.f) {
+              const double c = (double)cs[wave][i] + cs_low[wave][i], s = (double)sn[wave][i] + sn_low[wave][i];
+              v0 = (float)(x0 * c - x1 * s);
+              v1 = (float)(x0 * s + x1 * c);
+            } else {
+              const float c = cs[wave][i], s = sn[wave][i];
+              v0 = x0 * c - x1 * s;
+              v1 = x0 * s + x1 * c;
+            }
           }
           if (h.scale > 0.f) {
             const uint32_t w = f2e4m3_pair(v0 / h.scale, v1 / h.scale);
@@ -224,12 +265,19 @@ hipError_t launch_rope(const RopeArgs &a, hipStream_t s) {
   const int64_t blocks = std::min<int64_t>(2048, ((int64_t)a.n * parts + kWaves - 1) / kWaves);
   const int shift = a.append ? kv_shift(a.kv.page_size) : 0;
   const dim3 g((uint32_t)blocks), b(kWaves * 64);
-  if (inter)
-    hipLaunchKernelGGL((rope_kernel<true, true>), g, b, 0, s, a, parts, shift);
+  const bool fp8 = a.append && a.kv.elem == OES_ELEM_E4M3;
+  if (inter && fp8)
+    hipLaunchKernelGGL((rope_kernel<true, true, true>), g, b, 0, s, a, parts, shift);
+  else if (inter)
+    hipLaunchKernelGGL((rope_kernel<true, true, false>), g, b, 0, s, a, parts, shift);
+  else if (pieces && fp8)
+    hipLaunchKernelGGL((rope_kernel<false, true, true>), g, b, 0, s, a, parts, shift);
   else if (pieces)
-    hipLaunchKernelGGL((rope_kernel<false, true>), g, b, 0, s, a, parts, shift);
+    hipLaunchKernelGGL((rope_kernel<false, true, false>), g, b, 0, s, a, parts, shift);
+  else if (fp8)
+    hipLaunchKernelGGL((rope_kernel<false, false, true>), g, b, 0, s, a, parts, shift);
   else
-    hipLaunchKernelGGL((rope_kernel<false, false>), g, b, 0, s, a, parts, shift);
+    hipLaunchKernelGGL((rope_kernel<false, false, false>), g, b, 0, s, a, parts, shift);
   return hipGetLastError();
 }
 
