@@ -98,6 +98,13 @@ __device__ inline uint32_t fp8_bf16_pair(uint32_t w) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
 }
 
+// Masks: bit e of 32 for the entries [lo, hi) of a row; and all bits of an accumulator register's entry (see the top).
+// Bit to sign to select is two operations a score, where comparing took five.
+__device__ inline uint32_t seen_bits(int lo, int hi) {
+  return (uint32_t)((1ull << min(max(hi, 0), 32)) - 1) & ~(uint32_t)((1ull << min(max(lo, 0), 32)) - 1);
+}
+__device__ inline int seen_sign(uint32_t seen, int i) { return (int)(seen << (31 - (8 * (i / 4) + i % 4))) >> 31; }
+
 // What a launch is cut into.
 struct Plan {
   int tile_tokens;   // tokens of a tile
@@ -506,12 +513,10 @@ __global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8,
         const uint64_t bits = paged >> (4 * half);
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
-          // bit e: the row sees entry 32 kt + e.  Bit to sign to select: two operations a score, where comparing took five
-          const int l0 = min(max(lo_at - 32 * kt, 0), 32), h0 = min(max(hi_at - 32 * kt, 0), 32);
-          const uint32_t seen = (uint32_t)((1ull << h0) - 1) & ~(uint32_t)((1ull << l0) - 1) & (uint32_t)(bits >> (32 * kt));
+          const uint32_t seen = seen_bits(lo_at - 32 * kt, hi_at - 32 * kt) & (uint32_t)(bits >> (32 * kt));
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int e = 8 * (i / 4) + i % 4, keep = (int)(seen << (31 - e)) >> 31;
+            const int keep = seen_sign(seen, i);
             s[kt][i] = __uint_as_float((__float_as_uint(s[kt][i]) & keep) | (0xff800000u & ~keep));
           }
         }
@@ -1003,13 +1008,10 @@ __global__ __launch_bounds__(256 * RG, DP == 64 ? 4 : 2) void weigh_kernel(AttnA
         asm volatile("");   // (or the compiler makes selects of this, in every tile)
         int lo = 0, hi = 0;
         if (l2[x] != INFINITY) kv_seen(len, rows, i + ls_tok[x], a.window, &lo, &hi);
-        const int lo_at = lo - ew - 4 * half, hi_at = hi - ew - 4 * half;
-        const uint32_t bits = paged >> (4 * half);
+        const uint32_t seen = seen_bits(lo - ew - 4 * half, hi - ew - 4 * half) & (paged >> (4 * half));
 #pragma unroll
-        for (int y = 0; y < 16; ++y) {
-          const int e = 8 * (y / 4) + y % 4;
-          if (e >= lo_at && e < hi_at && ((bits >> e) & 1)) acc[y] += __builtin_amdgcn_exp2f(fmaf(s[x][y], cs, -l2[x]));
-        }
+        for (int y = 0; y < 16; ++y)
+          acc[y] += __uint_as_float(__float_as_uint(__builtin_amdgcn_exp2f(fmaf(s[x][y], cs, -l2[x]))) & seen_sign(seen, y));
       }
     }
     buf ^= 1;
@@ -1142,14 +1144,11 @@ __global__ __launch_bounds__(256, DP == 256 ? 2 : 4) void weigh_few_kernel(AttnA
       }
       int lo = 0, hi = 0;
       if (in && lse != -INFINITY) kv_seen(t.len, t.rows, i + tok, a.window, &lo, &hi);
-      const int lo_at = lo - ew - 4 * half, hi_at = hi - ew - 4 * half;
-      const uint32_t bits = paged >> (4 * half);
+      const uint32_t seen = seen_bits(lo - ew - 4 * half, hi - ew - 4 * half) & (paged >> (4 * half));
       const float l2 = lse * kLog2e;
 #pragma unroll
-      for (int y = 0; y < 16; ++y) {
-        const int x = 8 * (y / 4) + y % 4;
-        if (x >= lo_at && x < hi_at && ((bits >> x) & 1)) acc[y] += __builtin_amdgcn_exp2f(fmaf(s[y], cs, -l2));
-      }
+      for (int y = 0; y < 16; ++y)
+        acc[y] += __uint_as_float(__float_as_uint(__builtin_amdgcn_exp2f(fmaf(s[y], cs, -l2))) & seen_sign(seen, y));
     }
     float *join = join_sm[wave];   // the wave's own: its LDS operations run in order
     __builtin_amdgcn_wave_barrier();
