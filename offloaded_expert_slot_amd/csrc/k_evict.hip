@@ -17,8 +17,8 @@
 //                 writes).  Head rows are cut into columns of 128 bytes, and each
 //                 workgroup moves one column of one (sequence, head); bound by reading and
 //                 writing the moved rows once.
-// 16 sequences x 4 heads from 2080 to 2048 bf16 rows of 128: select 10.6 us, move 28.0; 4 x 8 heads from 9204 .. 15074
-// to 4099: 24 + 44.
+// 16 sequences x 4 heads from 2080 to 2048 bf16 rows of 128: select 10.5 us, move 24.0; 4 x 8 heads from 9204 .. 15074
+// to 4099: 24 + 30.5 (4.5 TB/s of moved rows).
 
 #include "layer_device.h"
 #include "oes_internal.h"
@@ -184,8 +184,8 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(EvictArgs a) {
   }
 }
 
-// 256 rows of 128 bytes in flight per workgroup.  (16 x 4 heads of 2048 bf16 rows, 256 workgroups: 28.9 us; with 512
-// threads and 4 rows a thread 37; 64-byte columns, twice the workgroups, 38.)
+// 256 rows of 128 bytes in flight per workgroup.  (16 x 4 heads of 2048 bf16 rows, 256 workgroups, before loads were
+// asked for ahead: 28.9 us; with 512 threads and 4 rows a thread 37; 64-byte columns, twice the workgroups, 38.)
 constexpr int kMove = 1024, kUnroll = 2, kRows = kMove / 8, kBatch = kRows * kUnroll;
 
 __global__ __launch_bounds__(kMove) void evict_move_kernel(EvictArgs a, int columns, int shift) {
@@ -200,39 +200,54 @@ __global__ __launch_bounds__(kMove) void evict_move_kernel(EvictArgs a, int colu
   const bool live = piece < pieces;
   uint8_t *base = static_cast<uint8_t *>(is_v ? a.kv.v : a.kv.k) + (is_v ? a.kv.v_head : a.kv.k_head) * h * es + (live ? piece * 16 : 0);
   const int32_t *table = a.kv.table + b * a.kv.table_stride, *kept = a.kept + (int64_t)bh * a.budget;
-  auto row = [&](int j) {
-    int ip = 0;
-    const int p = kv_page(a.kv, table, shift, j, &ip);  // >= 0: checked for the whole sequence
-    return reinterpret_cast<u32x4 *>(base + es * (is_v ? kv_v_off(a.kv, p, ip) : kv_k_off(a.kv, p, ip)));
+  // An entry's place: its page, as loaded (valid: checked for the whole sequence), and its row in the page.
+  struct Place {
+    int page, row;
   };
-  // rows past the last one are read again, and not written
-  const u32x4 *src[kUnroll];
+  auto place = [&](int j) {
+    const int col = shift >= 0 ? j >> shift : j / a.kv.page_size;
+    return Place{table[col], j - col * a.kv.page_size};
+  };
+  auto at = [&](const Place &p) {
+    return reinterpret_cast<u32x4 *>(base + es * (is_v ? kv_v_off(a.kv, p.page, p.row) : kv_k_off(a.kv, p.page, p.row)));
+  };
+  // Entry u of the thread in the batch from i0 on (past the last one, that one again, which is not written)
+  auto entry = [&](int i0, int u) { return (int)min((int64_t)i0 + u * kRows + r0, (int64_t)to - 1); };
+  // All that a batch needs is asked for ahead, before the batch before it is written: loads wait for the stores
+  // issued before them, so a chain of index, page and row behind the stores took a turn of 2.7 us.
   u32x4 v[kUnroll], next[kUnroll];
-  auto sources = [&](int i0) {
+  Place src[kUnroll], dst[kUnroll];   // sources of the next batch, places of this one
+  int index[kUnroll];                 // sources of the batch after the next
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) src[u] = row(kept[min(i0 + u * kRows + r0, to - 1)]);
-  };
-  sources(from);
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) v[u] = *src[u];
+  for (int u = 0; u < kUnroll; ++u) {
+    v[u] = *at(place(kept[entry(from, u)]));
+    src[u] = place(kept[entry(min(from + kBatch, to), u)]);
+    index[u] = kept[entry(min(from + 2 * kBatch, to), u)];
+    dst[u] = place(entry(from, u));
+  }
   for (int i0 = from; i0 < to; i0 += kBatch) {
-    const bool more = i0 + kBatch < to;
-    if (more) sources(i0 + kBatch);
-    u32x4 *dst[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) dst[u] = row(min(i0 + u * kRows + r0, to - 1));
     // the whole batch is in registers before its first row is written
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (more) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) next[u] = *src[u];
+    for (int u = 0; u < kUnroll; ++u) asm volatile("" : "+v"(src[u].page), "+v"(dst[u].page), "+v"(index[u]), "+v"(v[u]));
+    __syncthreads();
+    Place after[kUnroll], dst_next[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      next[u] = *at(src[u]);
+      after[u] = place(index[u]);
+      index[u] = kept[entry(i0 + 3 * kBatch, u)];
+      dst_next[u] = place(entry(i0 + kBatch, u));
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-      if (live && i0 + u * kRows + r0 < to) *dst[u] = v[u];
+      if (live && i0 + u * kRows + r0 < to) *at(dst[u]) = v[u];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) v[u] = next[u];
+    for (int u = 0; u < kUnroll; ++u) {
+      v[u] = next[u];
+      src[u] = after[u];
+      dst[u] = dst_next[u];
+    }
   }
 }
 
