@@ -739,15 +739,14 @@ __global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8,
       for (int w = 1; w < S::waves; ++w) mm = fmaxf(mm, jm[w][jr]);
       float ll = 0.f;
       f32x4 s4 = {0.f, 0.f, 0.f, 0.f};
-      if (mm != -INFINITY) {
+      const float mu = mm == -INFINITY ? 0.f : mm;   // no maximum: nothing was seen (sums of 0), or NaN alone (NaN)
 #pragma unroll
-        for (int w = 0; w < S::waves; ++w) {
-          const float f = __builtin_amdgcn_exp2f(jm[w][jr] - mm);
-          ll = fmaf(jl[w][jr], f, ll);
-          const f32x4 v = *reinterpret_cast<const f32x4 *>(jo + w * JS + jr * DP + d4);
+      for (int w = 0; w < S::waves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(jm[w][jr] - mu);
+        ll = fmaf(jl[w][jr], f, ll);
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(jo + w * JS + jr * DP + d4);
 #pragma unroll
-          for (int y = 0; y < 4; ++y) s4[y] = fmaf(v[y], f, s4[y]);
-        }
+        for (int y = 0; y < 4; ++y) s4[y] = fmaf(v[y], f, s4[y]);
       }
       if (direct) {
         const float inv = ll == 0.f ? 0.f : a.kv.v_scale / ll;
@@ -819,17 +818,16 @@ __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a, Plan plan) 
   f32x4 sum = {0.f, 0.f, 0.f, 0.f};
   float ll = 0.f;
   const bool live = 4 * lane < a.kv.head_dim;
-  if (mm != -INFINITY) {
+  const float mu = mm == -INFINITY ? 0.f : mm;   // as where the waves are joined
 #pragma unroll 4
-    for (int s = wave; s < parts; s += 4) {
-      const float2 st = *part_stats<TILE>(a, place(s));
-      const float f = __builtin_amdgcn_exp2f(st.x - mm);
-      ll = fmaf(st.y, f, ll);
-      if (live) {
-        const f32x4 v = *reinterpret_cast<const f32x4 *>(part_sums<TILE>(a, plan, place(s)) + 4 * lane);
+  for (int s = wave; s < parts; s += 4) {
+    const float2 st = *part_stats<TILE>(a, place(s));
+    const float f = __builtin_amdgcn_exp2f(st.x - mu);
+    ll = fmaf(st.y, f, ll);
+    if (live) {
+      const f32x4 v = *reinterpret_cast<const f32x4 *>(part_sums<TILE>(a, plan, place(s)) + 4 * lane);
 #pragma unroll
-        for (int y = 0; y < 4; ++y) sum[y] = fmaf(v[y], f, sum[y]);
-      }
+      for (int y = 0; y < 4; ++y) sum[y] = fmaf(v[y], f, sum[y]);
     }
   }
   so[wave][lane] = sum;
