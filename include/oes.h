@@ -540,7 +540,7 @@ oes_status oes_attn(const oes_kv *kv, const void *q, int64_t q_row, int64_t q_he
  *                   query heads h that read cache head g, of
  *                   exp(scale * q[t, h] . k_j - lse[t, h])
  * with q, q_start, scale and window as in oes_attn and lse as it returned it (a
- * row with lse = -inf adds nothing).  acc fp32 [batch, kv_heads, acc_stride],
+ * row with lse = -inf adds nothing, whatever its scores).  acc fp32 [batch, kv_heads, acc_stride],
  * acc_stride >= max_pages * page_size; values from len[b] on are left as they are.
  * Sums run in a fixed order (no atomics).  Async. */
 oes_status oes_attn_weigh(const oes_kv *kv, const void *q, int64_t q_row, int64_t q_head, const float *lse,

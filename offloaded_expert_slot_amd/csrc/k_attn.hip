@@ -105,6 +105,9 @@ __device__ inline uint32_t seen_bits(int lo, int hi) {
 }
 __device__ inline int seen_sign(uint32_t seen, int i) { return (int)(seen << (31 - (8 * (i / 4) + i % 4))) >> 31; }
 
+// Sign bits of the bf16 of a pair that are infinite or NaN (exponents of all ones).
+__device__ inline uint32_t odd_bits(uint32_t w) { return ((w & 0x7fff7fffu) + 0x00800080u) & 0x80008000u; }
+
 // What a launch is cut into.
 struct Plan {
   int tile_tokens;   // tokens of a tile
@@ -472,7 +475,6 @@ __global__ __launch_bounds__((Shape<DP, FP8, TILE>::waves * 64), (Shape<DP, FP8,
     // the rows that this wave stages.
     auto clear_odd = [&](int buf) {
       uint8_t *rows = tiles + buf * 2 * S::tile_bytes + S::tile_bytes + wave * own0 * DP * 2;
-      auto odd_bits = [](uint32_t w) { return ((w & 0x7fff7fffu) + 0x00800080u) & 0x80008000u; };  // exponents of all ones
       uint32_t any = 0;
 #pragma unroll
       for (int i = 0; i < S::own * DP / 512; ++i) {
@@ -914,6 +916,15 @@ __global__ __launch_bounds__(256 * RG, DP == 64 ? 4 : 2) void weigh_kernel(AttnA
       key[ks] = __builtin_bit_cast(bf16x8, w);
     }
   }
+  // whether a product with a row of zeros may not be 0: a key that is not finite
+  uint32_t odd_key = 0;
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) {
+    const u32x4 w = __builtin_bit_cast(u32x4, key[ks]);
+#pragma unroll
+    for (int y = 0; y < 4; ++y) odd_key |= odd_bits(w[y]);
+  }
+  const bool odd_keys = __any(odd_key != 0);
   float acc[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.f;
@@ -960,13 +971,13 @@ __global__ __launch_bounds__(256 * RG, DP == 64 ? 4 : 2) void weigh_kernel(AttnA
     }
   };
   float lse[2];
-  auto next_lse = [&](int i) {  // +inf in rows that add nothing: exp(-inf) = 0
+  auto next_lse = [&](int i) {  // +inf behind the rows: exp(-inf) = 0
     const float *base = a.lse + (int64_t)(first + i) * a.q_heads;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const bool in = i + ls_tok[x] < i1;
       const float v = base[in ? ls_off[x] : 0];
-      lse[x] = in && v != -INFINITY ? v : INFINITY;
+      lse[x] = in ? v : INFINITY;
     }
   };
   next_lse(i0);
@@ -994,9 +1005,11 @@ __global__ __launch_bounds__(256 * RG, DP == 64 ? 4 : 2) void weigh_kernel(AttnA
       for (int x = 0; x < 2; ++x)
         s[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key[ks], *reinterpret_cast<const bf16x8 *>(qr + x * 32 * DP * 2 + at), s[x], 0, 0, 0);
     }
-    // every row of this tile sees every entry of the wave, and all entries have pages: no masks
+    // every row of this tile sees every entry of the wave, and all entries have pages: no masks.  (But for rows that add
+    // nothing whatever their scores, and rows of zeros beside a key that is not finite: 0 inf and inf - inf are NaN.)
     const int last_tok = min(i + T, i1) - 1;
-    if (before + i >= ew + 31 && (a.window == 0 || before + last_tok - a.window < ew) && paged == ~0u) {
+    if (before + i >= ew + 31 && (a.window == 0 || before + last_tok - a.window < ew) && paged == ~0u && !odd_keys &&
+        !__any(fminf(l2[0], l2[1]) == -INFINITY)) {
 #pragma unroll
       for (int e = 0; e < 16; ++e)
         acc[e] += __builtin_amdgcn_exp2f(fmaf(s[0][e], cs, -l2[0])) + __builtin_amdgcn_exp2f(fmaf(s[1][e], cs, -l2[1]));
@@ -1005,7 +1018,7 @@ __global__ __launch_bounds__(256 * RG, DP == 64 ? 4 : 2) void weigh_kernel(AttnA
       for (int x = 0; x < 2; ++x) {
         asm volatile("");   // (or the compiler makes selects of this, in every tile)
         int lo = 0, hi = 0;
-        if (l2[x] != INFINITY) kv_seen(len, rows, i + ls_tok[x], a.window, &lo, &hi);
+        if (i + ls_tok[x] < i1 && l2[x] != -INFINITY) kv_seen(len, rows, i + ls_tok[x], a.window, &lo, &hi);
         const uint32_t seen = seen_bits(lo - ew - 4 * half, hi - ew - 4 * half) & (paged >> (4 * half));
 #pragma unroll
         for (int y = 0; y < 16; ++y)
