@@ -525,10 +525,13 @@ oes_status oes_rope_append(const oes_kv *kv, const void *q, int64_t q_row, int64
  *           16-byte aligned rows); out must not overlap q or the cache; lse fp32
  *           [n, q_heads] or NULL
  *   q_heads a multiple of kv_heads, q_heads / kv_heads <= 128; scale * k_scale
- *   in [1e-30, 1e30]; window >= 0 (0: none)
+ *   in [1e-30, 1e30]; window >= 0 (0: none); n * q_heads < 2^31
  *   workspace: device, 16-byte aligned, >= oes_attn_workspace bytes for the
  *   same kv sizes, q_heads and n (the splits of a long cache are summed through
- *   it, in a fixed order).  Async. */
+ *   it, in a fixed order)
+ * Work that a launch does not hold (2^32 work-items, n * q_heads = 2^24 where
+ * rows may be split; 2^31 units of entries) is OES_ERR_UNSUPPORTED, from both
+ * calls alike and before anything runs.  Async. */
 oes_status oes_attn_workspace(const oes_kv *kv, int32_t q_heads, int32_t n, int64_t *bytes);
 oes_status oes_attn(const oes_kv *kv, const void *q, int64_t q_row, int64_t q_head, void *out, int64_t o_row,
                     int64_t o_head, float *lse, int32_t q_heads, int32_t n, const int32_t *q_start, float scale,
@@ -542,7 +545,9 @@ oes_status oes_attn(const oes_kv *kv, const void *q, int64_t q_row, int64_t q_he
  * with q, q_start, scale and window as in oes_attn and lse as it returned it (a
  * row with lse = -inf adds nothing, whatever its scores).  acc fp32 [batch, kv_heads, acc_stride],
  * acc_stride >= max_pages * page_size; values from len[b] on are left as they are.
- * Sums run in a fixed order (no atomics).  Async. */
+ * Sums run in a fixed order (no atomics).  n * q_heads < 2^31; for chunks
+ * batch * kv_heads * max_pages * page_size / 128 (entries rounded up) < 2^23,
+ * for decode steps < 2^31 (OES_ERR_UNSUPPORTED beyond).  Async. */
 oes_status oes_attn_weigh(const oes_kv *kv, const void *q, int64_t q_row, int64_t q_head, const float *lse,
                           int32_t q_heads, int32_t n, const int32_t *q_start, float scale, int32_t window,
                           float *acc, int64_t acc_stride, void *stream);
@@ -561,7 +566,9 @@ oes_status oes_attn_weigh(const oes_kv *kv, const void *q, int64_t q_row, int64_
  * most budget entries is left untouched (kept counts up).  Pages of a sequence
  * that is cut must not be shared with another, nor stand in its table twice.  A sequence with a page outside
  * the cache among its used pages keeps its entries as they are (its kept is -1,
- * its new_len is len).  budget in [1, 2^30], first, last >= 0, first + last <= budget.
+ * its new_len is len).  budget in [1, 2^30], first, last >= 0, first + last <= budget;
+ * batch * kv_heads * 2 ceil(head row bytes / 128) < 2^22 (OES_ERR_UNSUPPORTED
+ * beyond, from both calls and before anything runs).
  * workspace: device, 16-byte aligned, >= oes_kv_evict_workspace bytes.  Async. */
 oes_status oes_kv_evict_workspace(const oes_kv *kv, int32_t budget, int64_t *bytes);
 oes_status oes_kv_evict(const oes_kv *kv, float *acc, int64_t acc_stride, int32_t budget, int32_t first,

@@ -34,9 +34,6 @@ oes_status launched(hipError_t e, const char *what) {
 inline hipStream_t as_stream(void *s) { return reinterpret_cast<hipStream_t>(s); }
 inline bool aligned(const void *p, int a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-// Grid limit of a launch; larger calls are refused rather than wrapped.
-constexpr int64_t kMaxBlocks = 0x7fffffff;
-
 oes_status check_kv(const oes_kv *kv, bool written) {
   if (!kv) return fail(OES_ERR_ARG, "kv is NULL");
   if (kv->elem != OES_ELEM_BF16 && kv->elem != OES_ELEM_E4M3)
@@ -112,6 +109,9 @@ oes_status check_attn(const oes_kv *kv, int32_t q_heads, int32_t n, float scale,
   if (!(scale > 0) || !(s >= 1e-30f) || !(s <= 1e30f)) return fail(OES_ERR_ARG, "scale (and scale * k_scale) must lie in [1e-30, 1e30]");
   return OES_OK;
 }
+
+// Larger calls are refused before their first launch.
+oes_status too_large() { return fail(OES_ERR_UNSUPPORTED, "more work than one launch holds"); }
 
 Rows rows(const void *p, int64_t row, int64_t head) {
   return Rows{static_cast<uint16_t *>(const_cast<void *>(p)), row, head};
@@ -259,7 +259,10 @@ extern "C" oes_status oes_attn_workspace(const oes_kv *kv, int32_t q_heads, int3
   oes_status st = check_kv(kv, false);
   if (st != OES_OK) return st;
   if ((st = check_attn(kv, q_heads, n, 1.f, 0)) != OES_OK) return st;
-  *bytes = n == 0 || kv->batch == 0 ? 0 : attn_workspace_bytes(*kv, q_heads, n);
+  *bytes = 0;
+  if (n == 0 || kv->batch == 0) return OES_OK;
+  if (!attn_fits(*kv, q_heads, n)) return too_large();
+  *bytes = attn_workspace_bytes(*kv, q_heads, n);
   return OES_OK;
 }
 
@@ -274,6 +277,7 @@ extern "C" oes_status oes_attn(const oes_kv *kv, const void *q, int64_t q_row, i
   if ((st = check_rows("q", q, q_row, q_head, n, q_heads, kv->head_dim, false)) != OES_OK) return st;
   if ((st = check_rows("out", out, o_row, o_head, n, q_heads, kv->head_dim, true)) != OES_OK) return st;
   if (out == q) return fail(OES_ERR_ARG, "out must not be q");
+  if (!attn_fits(*kv, q_heads, n)) return too_large();
   const int64_t need = attn_workspace_bytes(*kv, q_heads, n);
   if (workspace_bytes < need)
     return fail(OES_ERR_ARG, "workspace %lld < %lld bytes", (long long)workspace_bytes, (long long)need);
@@ -289,9 +293,7 @@ extern "C" oes_status oes_attn(const oes_kv *kv, const void *q, int64_t q_row, i
   a.scale = scale;
   a.window = window;
   a.ws = static_cast<float *>(workspace);
-  const hipError_t e = launch_attn(a, as_stream(stream));
-  if (e == hipErrorInvalidConfiguration) return fail(OES_ERR_UNSUPPORTED, "more work than one launch holds");
-  return launched(e, "oes_attn");
+  return launched(launch_attn(a, as_stream(stream)), "oes_attn");
 }
 
 extern "C" oes_status oes_attn_weigh(const oes_kv *kv, const void *q, int64_t q_row, int64_t q_head, const float *lse,
@@ -305,6 +307,7 @@ extern "C" oes_status oes_attn_weigh(const oes_kv *kv, const void *q, int64_t q_
   if (!aligned(q_start, 4) || !aligned(lse, 4) || !aligned(acc, 4)) return fail(OES_ERR_ARG, "q_start, lse and acc must be 4-byte aligned");
   if ((st = check_rows("q", q, q_row, q_head, n, q_heads, kv->head_dim, false)) != OES_OK) return st;
   if (acc_stride < (int64_t)kv->max_pages * kv->page_size) return fail(OES_ERR_ARG, "acc_stride < max_pages * page_size");
+  if (!attn_weigh_fits(*kv, q_heads, n)) return too_large();
   AttnArgs a = {};
   a.kv = *kv;
   a.q = rows(q, q_row, q_head);
@@ -316,9 +319,7 @@ extern "C" oes_status oes_attn_weigh(const oes_kv *kv, const void *q, int64_t q_
   a.window = window;
   a.acc = acc;
   a.acc_stride = acc_stride;
-  const hipError_t e = launch_attn_weigh(a, as_stream(stream));
-  if (e == hipErrorInvalidConfiguration) return fail(OES_ERR_UNSUPPORTED, "more work than one launch holds");
-  return launched(e, "oes_attn_weigh");
+  return launched(launch_attn_weigh(a, as_stream(stream)), "oes_attn_weigh");
 }
 
 // ============================================================================ eviction
@@ -327,6 +328,7 @@ extern "C" oes_status oes_kv_evict_workspace(const oes_kv *kv, int32_t budget, i
   oes_status st = check_kv(kv, true);
   if (st != OES_OK) return st;
   if (budget < 1 || budget > (1 << 30)) return fail(OES_ERR_ARG, "budget %d outside [1, 2^30]", budget);
+  if (!evict_fits(*kv)) return too_large();
   *bytes = evict_workspace_bytes(*kv, budget);
   return OES_OK;
 }
@@ -345,7 +347,7 @@ extern "C" oes_status oes_kv_evict(const oes_kv *kv, float *acc, int64_t acc_str
   const int64_t need = evict_workspace_bytes(*kv, budget);
   if (workspace_bytes < need || !workspace || !aligned(workspace, 16))
     return fail(OES_ERR_ARG, "workspace: %lld bytes, 16-byte aligned, are needed", (long long)need);
-  if ((int64_t)kv->batch * kv->kv_heads * 64 > kMaxBlocks) return fail(OES_ERR_UNSUPPORTED, "more work than one launch holds");
+  if (!evict_fits(*kv)) return too_large();
   EvictArgs a = {};
   a.kv = *kv;
   a.acc = acc;

@@ -1223,6 +1223,15 @@ hipError_t launch_dim(const AttnArgs &a, const Plan &p, bool split, uint32_t blo
 
 }  // namespace
 
+bool attn_fits(const oes_kv &kv, int q_heads, int n) {
+  const Plan p = make_plan(kv, q_heads, n);
+  const bool split = split_shape(kv, q_heads, n);
+  const int64_t cap = (int64_t)kv.max_pages * kv.page_size, rows = (int64_t)n * q_heads;
+  return launch_fits(split ? p.blocks : (int64_t)p.tiles * kv.kv_heads * p.splits, 256) &&
+         (p.splits == 1 ? rows <= 0x7fffffff : launch_fits(rows, 256)) &&
+         (int64_t)p.tiles * kv.kv_heads * (cap / 64 + 2 + kBegin) <= 0x7fffffff;   // units, counted in 32 bits
+}
+
 int64_t attn_workspace_bytes(const oes_kv &kv, int q_heads, int n) {
   const Plan p = make_plan(kv, q_heads, n);
   if (p.splits == 1) return 0;
@@ -1235,10 +1244,7 @@ hipError_t launch_attn(const AttnArgs &args, hipStream_t s) {
   a.shift = kv_shift(a.kv.page_size);
   const Plan p = make_plan(a.kv, a.q_heads, a.n);
   const bool split = split_shape(a.kv, a.q_heads, a.n);
-  const int64_t cap = (int64_t)a.kv.max_pages * a.kv.page_size;
   const int64_t blocks = split ? p.blocks : (int64_t)p.tiles * a.kv.kv_heads * p.splits;
-  if (blocks > 0x7fffffff || (int64_t)a.n * a.q_heads > 0x7fffffff || (int64_t)p.tiles * a.kv.kv_heads * (cap / 64 + 2 + kBegin) > 0x7fffffff)
-    return hipErrorInvalidConfiguration;
   const int dp = head_pad(a.kv);
   const hipError_t e = dp == 64 ? launch_dim<64>(a, p, split, (uint32_t)blocks, s)
                                 : (dp == 128 ? launch_dim<128>(a, p, split, (uint32_t)blocks, s) : launch_dim<256>(a, p, split, (uint32_t)blocks, s));
@@ -1252,11 +1258,13 @@ hipError_t launch_attn(const AttnArgs &args, hipStream_t s) {
 }
 
 namespace {
+// 128 entries each of every cache head, over the tables' width
+int64_t weigh_units(const oes_kv &kv) { return ((int64_t)kv.max_pages * kv.page_size + 127) / 128 * kv.kv_heads * kv.batch; }
+
 template <int DP, bool FP8>
 hipError_t launch_weigh(const AttnArgs &a, hipStream_t s) {
   const bool few = split_shape(a.kv, a.q_heads, a.n);
-  const int64_t cap = (int64_t)a.kv.max_pages * a.kv.page_size, blocks = (cap + 127) / 128 * a.kv.kv_heads * a.kv.batch;
-  if (blocks > 0x7fffffff || (int64_t)a.n * a.q_heads > 0x7fffffff) return hipErrorInvalidConfiguration;
+  const int64_t blocks = weigh_units(a.kv);
   if (few)
     hipLaunchKernelGGL((weigh_few_kernel<DP, FP8>), dim3((uint32_t)std::min<int64_t>(blocks, kFewBlocks)), dim3(256), 0, s, a);
   else
@@ -1264,6 +1272,12 @@ hipError_t launch_weigh(const AttnArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 }  // namespace
+
+bool attn_weigh_fits(const oes_kv &kv, int q_heads, int n) {
+  // (decode steps: units are counted in 32 bits)
+  return (split_shape(kv, q_heads, n) ? weigh_units(kv) <= 0x7fffffff : launch_fits(weigh_units(kv), 512)) &&
+         (int64_t)n * q_heads <= 0x7fffffff;
+}
 
 hipError_t launch_attn_weigh(const AttnArgs &args, hipStream_t s) {
   AttnArgs a = args;

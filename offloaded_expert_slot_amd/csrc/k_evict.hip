@@ -253,6 +253,16 @@ __global__ __launch_bounds__(kMove) void evict_move_kernel(EvictArgs a, int colu
 
 }  // namespace
 
+namespace {
+// columns of 128 bytes of a head's k and v rows
+int move_columns(const oes_kv &kv) { return 2 * ((kv.head_dim * (kv.elem == OES_ELEM_BF16 ? 2 : 1) + 127) / 128); }
+}  // namespace
+
+bool evict_fits(const oes_kv &kv) {
+  const int64_t bh = (int64_t)kv.batch * kv.kv_heads;
+  return launch_fits(bh, kSel) && launch_fits(bh * move_columns(kv), kMove);
+}
+
 int64_t evict_workspace_bytes(const oes_kv &kv, int) { return ((int64_t)kv.batch * kv.kv_heads * 8 + 255) / 256 * 256; }
 
 hipError_t launch_evict(const EvictArgs &a, hipStream_t s) {
@@ -260,7 +270,7 @@ hipError_t launch_evict(const EvictArgs &a, hipStream_t s) {
   hipLaunchKernelGGL(evict_select_kernel, dim3(bh), dim3(kSel), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int columns = 2 * ((a.kv.head_dim * (a.kv.elem == OES_ELEM_BF16 ? 2 : 1) + 127) / 128);
+  const int columns = move_columns(a.kv);
   hipLaunchKernelGGL(evict_move_kernel, dim3(bh * columns), dim3(kMove), 0, s, a, columns, kv_shift(a.kv.page_size));
   return hipGetLastError();
 }

@@ -122,6 +122,11 @@ bool prefill_supported(int H, int I, int E);
 int64_t prefill_workspace_bytes(int H, int I, int n, int k, int E);
 hipError_t launch_prefill_ffn(const PrefillArgs &a, hipStream_t s);
 
+// ---------------------------------------------------------------- launches
+// What HIP launches: at most 2^31 - 1 workgroups and 2^32 - 1 work-items.  A call of several launches has to know before
+// its first one, or it is left half done.
+inline bool launch_fits(int64_t blocks, int threads) { return blocks <= 0x7fffffff && blocks * threads <= 0xffffffffll; }
+
 // ---------------------------------------------------------------- 4-bit linear
 struct LinearArgs {
   int32_t format, N, K, n;
@@ -165,6 +170,8 @@ struct AttnArgs {
   int64_t acc_stride;
   int32_t shift;           // log2 of the page size, or -1 (set by the launches)
 };
+bool attn_fits(const oes_kv &kv, int q_heads, int n);          // every launch of oes_attn (its joining one too)
+bool attn_weigh_fits(const oes_kv &kv, int q_heads, int n);
 int64_t attn_workspace_bytes(const oes_kv &kv, int q_heads, int n);
 hipError_t launch_attn(const AttnArgs &a, hipStream_t s);
 hipError_t launch_attn_weigh(const AttnArgs &a, hipStream_t s);
@@ -177,6 +184,7 @@ struct EvictArgs {
   int32_t *kept, *new_len;
   int32_t *ws;
 };
+bool evict_fits(const oes_kv &kv);
 int64_t evict_workspace_bytes(const oes_kv &kv, int budget);
 hipError_t launch_evict(const EvictArgs &a, hipStream_t s);
 
