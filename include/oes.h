@@ -525,7 +525,7 @@ oes_status oes_rope_append(const oes_kv *kv, const void *q, int64_t q_row, int64
  *           16-byte aligned rows); out must not overlap q or the cache; lse fp32
  *           [n, q_heads] or NULL
  *   q_heads a multiple of kv_heads, q_heads / kv_heads <= 128; scale * k_scale
- *   in [1e-30, 1e30]; window >= 0 (0: none); n * q_heads < 2^31
+ *   in [1e-30, 1e30]; window >= 0 (0: none); n <= 2^30, n * q_heads < 2^31
  *   workspace: device, 16-byte aligned, >= oes_attn_workspace bytes for the
  *   same kv sizes, q_heads and n (the splits of a long cache are summed through
  *   it, in a fixed order)
@@ -545,7 +545,7 @@ oes_status oes_attn(const oes_kv *kv, const void *q, int64_t q_row, int64_t q_he
  * with q, q_start, scale and window as in oes_attn and lse as it returned it (a
  * row with lse = -inf adds nothing, whatever its scores).  acc fp32 [batch, kv_heads, acc_stride],
  * acc_stride >= max_pages * page_size; values from len[b] on are left as they are.
- * Sums run in a fixed order (no atomics).  n * q_heads < 2^31; for chunks
+ * Sums run in a fixed order (no atomics).  n <= 2^30, n * q_heads < 2^31; for chunks
  * batch * kv_heads * max_pages * page_size / 128 (entries rounded up) < 2^23,
  * for decode steps < 2^31 (OES_ERR_UNSUPPORTED beyond).  Async. */
 oes_status oes_attn_weigh(const oes_kv *kv, const void *q, int64_t q_row, int64_t q_head, const float *lse,

@@ -105,6 +105,8 @@ oes_status check_attn(const oes_kv *kv, int32_t q_heads, int32_t n, float scale,
   oes_status st = check_q_heads(kv, q_heads);
   if (st != OES_OK) return st;
   if (n < 0 || window < 0) return fail(OES_ERR_ARG, "n < 0 or window < 0");
+  // row numbers are added up in 32 bits (a tile's padding rows count as 2^30 on)
+  if (n > (1 << 30)) return fail(OES_ERR_UNSUPPORTED, "n = %d: at most 2^30 rows", n);
   const float s = scale * kv->k_scale;  // what the scores are multiplied with
   if (!(scale > 0) || !(s >= 1e-30f) || !(s <= 1e30f)) return fail(OES_ERR_ARG, "scale (and scale * k_scale) must lie in [1e-30, 1e30]");
   return OES_OK;

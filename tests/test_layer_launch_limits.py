@@ -82,3 +82,11 @@ def test_entry_weights_beyond_a_launch_are_refused():
     assert oes.lib().oes_attn_weigh(ctypes.byref(c), A, 1024, 128, A, 2, 100, A, 0.125, 0, A, 1 << 30, None) == oes.ERR_UNSUPPORTED
     c.max_pages = c.table_stride = 1 << 19        # 2^22 * 2 of 512: 2^32
     assert oes.lib().oes_attn_weigh(ctypes.byref(c), A, 1024, 128, A, 2, 100, A, 0.125, 0, A, 1 << 30, None) == oes.ERR_UNSUPPORTED
+
+
+def test_more_rows_than_the_kernels_count_are_refused():
+    """Row numbers stay below 2^30, so that a sum of two of them stays within 32 bits."""
+    c = kv()
+    for n in ((1 << 30) + 1, (1 << 31) - 1):
+        assert attn(c, 1, n) == attn_workspace(c, 1, n) == oes.ERR_UNSUPPORTED, n
+        assert oes.lib().oes_attn_weigh(ctypes.byref(c), A, 1024, 128, A, 1, n, A, 0.125, 0, A, 32, None) == oes.ERR_UNSUPPORTED, n
