@@ -411,8 +411,10 @@ oes_status oes_layers_ffn(oes_layers *p, int32_t layer, const void *x, const int
  *   OES_MXFP4_T  w0 blocks [K/32, N, 16], w1 e8m0 [K/32, N], w2 bias bf16 [N] or
  *                NULL (none)
  * Other formats: OES_ERR_UNSUPPORTED.  x is bf16 with rows x_stride elements
- * apart, y bf16 with rows y_stride elements apart.  Sums are fp32; the weights
- * are used exactly (no rounding on the way); y is rounded to nearest even once.
+ * apart, y bf16 with rows y_stride elements apart.  Sums are fp32 (nvfp4: of the
+ * products before w2's factor, so sums of those beyond 3.4e38 are infinite); the
+ * weights are used exactly (no rounding on the way); y is rounded to nearest even
+ * once.  An x that is infinite or NaN gives the row's infinity or NaN.
  * K a positive multiple of 32 up to 2^20, N in [1, 2^23], n in [0, 2^19]
  * (OES_ERR_UNSUPPORTED beyond N's and n's limits); w0, w1 and the rows of
  * x 16-byte aligned, w2 and y 2-byte aligned, x_stride >= K, y_stride >= N.  y

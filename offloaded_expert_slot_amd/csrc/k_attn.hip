@@ -105,9 +105,6 @@ __device__ inline uint32_t seen_bits(int lo, int hi) {
 }
 __device__ inline int seen_sign(uint32_t seen, int i) { return (int)(seen << (31 - (8 * (i / 4) + i % 4))) >> 31; }
 
-// Sign bits of the bf16 of a pair that are infinite or NaN (exponents of all ones).
-__device__ inline uint32_t odd_bits(uint32_t w) { return ((w & 0x7fff7fffu) + 0x00800080u) & 0x80008000u; }
-
 // What a launch is cut into.
 struct Plan {
   int tile_tokens;   // tokens of a tile

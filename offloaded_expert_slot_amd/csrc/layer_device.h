@@ -30,6 +30,9 @@ __device__ inline uint32_t f2bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, r);
 }
 
+// Sign bits of the bf16 of a pair that are infinite or NaN (exponents of all ones).
+__device__ inline uint32_t odd_bits(uint32_t w) { return ((w & 0x7fff7fffu) + 0x00800080u) & 0x80008000u; }
+
 // The value an e4m3 cache stores for x: clamped to +-448, rounded to nearest even,
 // NaN kept.
 __device__ inline uint32_t f2e4m3_pair(float a, float b) {
