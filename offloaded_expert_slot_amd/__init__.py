@@ -602,12 +602,14 @@ def _heads(name, t, device):
     return t.data_ptr(), row, head
 
 
-def _enqueue(device, fn, *args, stream=None):
-    """fn(*args, stream) on `device`: its current stream unless one is given."""
+def _enqueue(device, fn, *args, stream=None, kv=None):
+    """fn(*args, stream) on `device`: its current stream unless one is given; behind the making of `kv`."""
     if device.type != "cuda":
         _bad(f"tensors are on {device}, not on a GPU")
     th, index = _th(), device.index
     stream = th.stream(index) if stream is None else _stream(stream)
+    if kv is not None and stream not in kv._behind:
+        kv._order(stream)
     if index == th.device():
         status = fn(*args, stream)
     else:
@@ -662,7 +664,9 @@ class KvPages:
     table   int32 [batch, max_pages], len int32 [batch], both on the GPU and read by every call
 
     ``status`` is an int32 word on the GPU that a kernel sets when it meets a bad page, length or
-    row range; ``check()`` reads and clears it.
+    row range; ``check()`` reads and clears it.  It is cleared at first on the current stream: calls
+    on another one wait for that (a captured call does not: its replays come after it by the caller's
+    order, as after whatever made the cache).
     """
 
     def __init__(self, k, v, table, len, k_scale=1.0, v_scale=1.0):
@@ -682,6 +686,13 @@ class KvPages:
         self.k, self.v, self.table, self.len = k, v, table, len
         self.device = k.device
         self.status = th.torch.zeros(1, dtype=th.torch.int32, device=k.device)
+        self._behind, self._made = set(), None   # streams whose calls come behind the clearing; its event
+        if k.device.type == "cuda":
+            own = th.torch.cuda.current_stream(k.device)
+            self._behind.add(own.cuda_stream)
+            with th.torch.cuda.device(k.device):
+                if not th.torch.cuda.is_current_stream_capturing():
+                    self._made = own.record_event()
         self.kv_heads, self.head_dim, self.batch = k.shape[2], k.shape[3], table.shape[0]
         self.capacity = table.shape[1] * k.shape[1]
         ks, vs = k.stride(), v.stride()
@@ -691,11 +702,27 @@ class KvPages:
                       table.shape[0], table.shape[1], k_scale, v_scale)
         self._ref = ctypes.byref(self._kv)
 
+    def _order(self, stream):
+        """Calls on `stream` (a raw one) from now on come behind the status word's clearing."""
+        cuda = _th().torch.cuda
+        of = cuda.ExternalStream(stream, device=self.device) if stream else cuda.default_stream(self.device)
+        with cuda.device(self.device), cuda.stream(of):
+            if cuda.is_current_stream_capturing():
+                return
+            if self._made is not None:
+                cuda.current_stream().wait_event(self._made)
+        self._behind.add(stream)
+
     def check(self):
-        """Syncs; raises OesError if a call since the last check met a bad page, length or row range."""
+        """Waits for the GPU (calls on every stream); raises OesError if one since the last check met a bad page,
+        length or row range."""
+        if self.device.type == "cuda":
+            _th().torch.cuda.synchronize(self.device)
         bad = int(self.status.item())
-        self.status.zero_()
         if bad:
+            self.status.zero_()
+            if self.device.type == "cuda":   # a later call's word is not cleared, whatever its stream
+                _th().torch.cuda.synchronize(self.device)
             raise OesError(bad, "a page, length or row range outside the cache")
 
 
@@ -736,7 +763,7 @@ def rope_append(q, q_out, k, v, freq, pos, kv, q_start, layout="half", mscale=1.
         _bad("q_out has the shape of q; k and v are [n, kv_heads, head_dim], with no more rows than q")
     _enqueue(dev, lib().oes_rope_append, kv._ref, *qp, *op, heads, *kp, *vp, n, _q_start(kv, q_start),
              2 * freq.numel(), ROPE_LAYOUTS.get(layout, layout), _typed("freq", freq, th.f64, None, dev), mscale,
-             _typed("pos", pos, th.i32, (n,), dev), stream=stream)
+             _typed("pos", pos, th.i32, (n,), dev), stream=stream, kv=kv)
 
 
 def attn_workspace_bytes(kv, q_heads, n):
@@ -754,7 +781,7 @@ def attn(q, out, kv, q_start, scale, workspace, window=0, lse=None, stream=None)
         _bad(f"q and out: [n, q_heads, {kv.head_dim}], not {tuple(q.shape)} and {tuple(out.shape)}")
     lsep = None if lse is None else _typed("lse", lse, _th().f32, (n, heads), dev)
     _enqueue(dev, lib().oes_attn, kv._ref, *qp, *op, lsep, heads, n, _q_start(kv, q_start), scale, window,
-             *_workspace(workspace, dev), stream=stream)
+             *_workspace(workspace, dev), stream=stream, kv=kv)
 
 
 def _workspace(ws, dev):
@@ -777,7 +804,7 @@ def attn_weigh(q, lse, kv, q_start, scale, acc, window=0, stream=None):
     if D != kv.head_dim:
         _bad(f"q: head_dim {D}, not {kv.head_dim}")
     _enqueue(dev, lib().oes_attn_weigh, kv._ref, *qp, _typed("lse", lse, _th().f32, (n, heads), dev), heads, n,
-             _q_start(kv, q_start), scale, window, *_acc(kv, acc), stream=stream)
+             _q_start(kv, q_start), scale, window, *_acc(kv, acc), stream=stream, kv=kv)
 
 
 def kv_evict_workspace_bytes(kv, budget):
@@ -791,4 +818,4 @@ def kv_evict(kv, acc, budget, kept, new_len, workspace, first=0, last=0, stream=
     th, dev = _th(), kv.device
     _enqueue(dev, lib().oes_kv_evict, kv._ref, *_acc(kv, acc), budget, first, last,
              _typed("kept", kept, th.i32, (kv.batch, kv.kv_heads, budget), dev),
-             _typed("new_len", new_len, th.i32, (kv.batch,), dev), *_workspace(workspace, dev), stream=stream)
+             _typed("new_len", new_len, th.i32, (kv.batch,), dev), *_workspace(workspace, dev), stream=stream, kv=kv)
