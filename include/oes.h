@@ -517,11 +517,12 @@ oes_status oes_rope_append(const oes_kv *kv, const void *q, int64_t q_row, int64
  *   out[t, h] = sum_j p_j v_j,  p = softmax_j(scale * q[t, h] . k_j)
  *   lse[t, h] = ln sum_j exp(scale * q[t, h] . k_j)     (natural log)
  * Query head h reads head h / (q_heads / kv_heads) of the cache.  A row that
- * sees nothing gets out = 0 and lse = -inf, and one with a NaN among its scores
- * NaN for both.  Rows from q_start[batch] on are
- * left as they were.  Entries that a row does not see do not reach it, whatever
- * they hold (infinities and NaN included).  Scores, softmax statistics and sums
- * are fp32; the probabilities are rounded to bf16 for the product with v; out is
+ * sees nothing, or scores of -inf alone over finite values, gets out = 0 and
+ * lse = -inf, and one with a NaN or +inf among its scores NaN for both.  Rows
+ * from q_start[batch] on are left as they were.  Entries that a row does not see
+ * do not reach it, whatever they hold (infinities and NaN included).  Scores,
+ * softmax statistics and sums are fp32; the probabilities are rounded to bf16 for
+ * the product with v (half a step each, about the error of rounding out); out is
  * rounded to bf16 once.
  *   q, out  bf16 [n, q_heads, head_dim] with row and head strides (elements,
  *           16-byte aligned rows); out must not overlap q or the cache; lse fp32

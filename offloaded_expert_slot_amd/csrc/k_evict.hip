@@ -17,8 +17,8 @@
 //                 writes).  Head rows are cut into columns of 128 bytes, and each
 //                 workgroup moves one column of one (sequence, head); bound by reading and
 //                 writing the moved rows once.
-// 16 sequences x 4 heads from 2080 to 2048 bf16 rows of 128: select 10.5 us, move 24.0; 4 x 8 heads from 9204 .. 15074
-// to 4099: 24 + 30.5 (4.5 TB/s of moved rows).
+// 16 sequences x 4 heads from 2080 to 2048 bf16 rows of 128: select 10.5 us, move 23.7; 4 x 8 heads from 9204 .. 15074
+// to 4099: 23.3 + 29.6 (4.6 TB/s of moved rows).
 
 #include "layer_device.h"
 #include "oes_internal.h"

@@ -1,7 +1,10 @@
 // y = x . W^T for 4-bit weights with group scales, in the layouts of the expert banks.
 //
-// Bound by reading the weights (4.5 bits each and nothing twice) up to some 64 tokens: nvfp4 100003 x 7168 at 16 tokens
-// 102 us, 4.0 TB/s; small ones by latency: q4_0 5120 x 2048 for one token 5.3 us.  A
+// Bound by reading the weights (4.5 bits each) up to some 16 tokens: nvfp4 100003 x 7168 at 16 tokens 100 - 110 us a
+// call, 3.7 - 4.0 TB/s (114 - 127 in a kernel trace, 100 at best; it asks memory for 1.14 times its operands); with more
+// tokens widening the codes and the products add to it: 164 us at 40.  Small ones are bound by latency: q4_0 5120 x 2048
+// for one token 5.4 us.  A workgroup reads its weights once for 16 NT tokens (16, or up to 64 from 1536 row tiles on),
+// so a call of more tokens reads and widens them again.  A
 // wave takes R tiles of 16 weight rows and multiplies them with up to 16 NT tokens by
 // v_mfma_f32_16x16x32_bf16 (A = tokens, B = weights: a lane's accumulators are 4 tokens of
 // one weight row).  A step covers 256 of K: two 16-byte loads per lane and tile, into one of
@@ -412,8 +415,9 @@ hipError_t launch_shape(const LinearArgs &a, hipStream_t s) {
 template <int FMT>
 hipError_t launch_format(const LinearArgs &a, hipStream_t s) {
   const int64_t tiles = (a.N + 15) / 16;
-  // From 1536 row tiles on: two tiles a wave, 8 waves of rows share x, up to 64 tokens at a time (nvfp4 at
-  // 100003 x 7168: 102 us at 16 tokens, 164 at 40; with one tile a wave 114 at 16).
+  // From 1536 row tiles on: two tiles a wave, 8 waves of rows share x, up to 64 tokens at a time (100003 x 7168 a call,
+  // us, at 16 and 40 tokens: nvfp4 102 - 113 and 164, q4_0 96 - 115 and 221, mxfp4 72 and 129; with one tile a wave
+  // nvfp4 took 114 at 16 where two took 102).
   if (tiles >= 1536) {
     if (a.n <= 16) return launch_shape<FMT, 2, 1, 8, 1, 2>(a, s);
     if (a.n <= 32) return launch_shape<FMT, 2, 2, 8, 1, 2>(a, s);

@@ -84,3 +84,23 @@ def test_a_sequence_of_nan_keys_is_nan(elem, q_len, lens):
     a = q_len[0]
     assert out[:a].isnan().all() and lse[:a].isnan().all()
     assert torch.equal(out[a:], clean[a:]) and torch.equal(lse[a:], lse0[a:])
+
+
+@pytest.mark.parametrize("q_len,lens", [([1], [40]), ([1, 1], [3000, 90]), ([70], [70]), ([150], [4000])], ids=str)
+def test_infinite_scores(q_len, lens):
+    """Scores of -inf alone: as for a row that sees nothing.  +inf among them: NaN."""
+    Hq, Hkv, D, page = 4, 2, 64, 16
+    c = R.Cache(55, lens, Hkv, D, page)
+    c.dk[..., 0] = c.dk[..., 0].abs().clamp(min=0.125)
+    start = [0]
+    for a in q_len:
+        start.append(start[-1] + a)
+    dstart = torch.tensor(start, dtype=torch.int32, device=DEV)
+    q = torch.randn(start[-1], Hq, D, generator=torch.Generator().manual_seed(56)).bfloat16().to(DEV)
+    clean, lse0 = _attn(q, c.handle(oes), dstart, 0.125)
+    q[-1, 0, 0], q[-1, 1, 0] = -math.inf, math.inf
+    out, lse = _attn(q, c.handle(oes), dstart, 0.125)
+    assert (out[-1, 0] == 0).all() and lse[-1, 0] == -math.inf
+    assert out[-1, 1].isnan().all() and lse[-1, 1].isnan()
+    out[-1, :2], lse[-1, :2] = clean[-1, :2], lse0[-1, :2]
+    assert torch.equal(out, clean) and torch.equal(lse, lse0)
