@@ -16,7 +16,7 @@ launch stream at its two ends; value = 1000 / (L * ms_per_step) at the
 headline miss rate.  A second pass with events between the four parts gives
 the breakdown and the copy's time.
 
-Every workload is measured the same way (`configs` in the JSON line): the tiny
+Every workload is measured the same way (`configs` in the record): the tiny
 bf16 one (H=256, 16 experts, top-2, 8 slots, bs 1 and 4), bf16 H=2048, block
 fp8 H=4096 (256 experts, 2048 slots), NVFP4 H=7168 (256 experts, 1536 slots),
 GGUF Q4_0 at the bf16 model's shape, and the MXFP4 prefill layer:
@@ -83,6 +83,24 @@ def parse():
 
 def _r(d):
     return {k: (round(v, 4) if isinstance(v, float) else v) for k, v in d.items()}
+
+
+def _line(out):
+    """The line for stdout: the headline, its rooflines and parity, and every workload's times in short.
+
+    The full record (some 50 KB: every row of every workload) goes to stderr; a reader that keeps the last few
+    thousand characters of stdout still gets a whole line.
+    """
+    line = {k: v for k, v in out.items() if k not in ("decode_per_miss_rate", "copy_sweep", "configs", "hybrid", "resize",
+                                                      "prefill", "parity", "kernels")}
+    line["parity"] = {**out["parity"], "failed": out["parity"]["failed"][:20]}
+    line["kernels"] = {n: {k: v for k, v in d.items() if k != "instruction"} for n, d in out["kernels"].items()}
+    line["ms_per_step_by_workload"] = {
+        n: {f"bs={r['bs']} mr={r['miss_rate']}": round(r["ms_per_step"], 4) for r in c["decode"]}
+        for n, c in out["configs"].items() if "decode" in c}
+    if out["prefill"] is not None:
+        line["prefill"] = {k: out["prefill"][k] for k in ("tokens", "ffn_ms", "ffn_TFLOPs", "layer_copy_ms", "overlapped_ms_per_layer")}
+    return line
 
 
 def main():
@@ -194,7 +212,8 @@ def main():
         out["value"] = None
     if failed:
         out["invalid"] = f"{len(failed)} measured row(s) differ from the oracle (see parity.failed)"
-    print(json.dumps(out), flush=True)
+    log("record", json.dumps(out))
+    print(json.dumps(_line(out)), flush=True)
     if failed:
         sys.exit(1)
 
