@@ -578,6 +578,105 @@ oes_status oes_kv_evict(const oes_kv *kv, float *acc, int64_t acc_stride, int32_
                         int32_t last, int32_t *kept, int32_t *new_len, void *workspace, int64_t workspace_bytes,
                         void *stream);
 
+/* ------------------------------------------------------------------ between the blocks */
+/*
+ * What a decode step runs between its blocks: the norms with the residual sum, the
+ * products whose weights are bf16, and the choice of the next token (FreeToken
+ * benchmark harness: sampling by temperature, top_p and top_k).  As above, these
+ * calls only enqueue kernels on `stream` and may be captured into a HIP graph.
+ */
+
+/* A norm over rows of `dim` values v (sums in fp32):
+ *   OES_NORM_RMS    v / sqrt(mean(v^2) + eps) * gain + b
+ *   OES_NORM_LAYER  (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * gain + b
+ * gain = offset + w, or 1 where w is NULL; b = 0 where it is NULL.  w and b are
+ * [dim], both of type elem (OES_ELEM_BF16 or OES_ELEM_F32), 16-byte aligned; eps
+ * finite and >= 0, offset finite. */
+enum { OES_NORM_RMS = 0, OES_NORM_LAYER = 1 };
+typedef struct {
+  const void *w, *b;
+  int32_t kind, elem;
+  float eps, offset;
+} oes_norm_spec;
+
+/* The output x of a block on its way into the next one:
+ *   r = res + scale * act(gate) * post(x)       y = pre(r)
+ * with every part optional: res NULL counts as 0, gate NULL as 1, post or pre NULL
+ * as the identity.  r is stored to res_out (res_elem, rounded to nearest even once)
+ * and y to y (bf16, rounded once); either may be NULL, not both.  Where res_out is
+ * given, y is the norm of r as it is stored, so that later readers of the residual
+ * see the row that y belongs to; otherwise of r in fp32.
+ *   x      [n, heads, dim] bf16 or fp32 (x_elem): token t, head h at t * x_row + h * x_head
+ *          elements; rows are normalised one by one (heads = 1 for hidden states)
+ *   gate   bf16: the value of (t, h, c) at t * gate_row + h * gate_head + c * gate_col,
+ *          gate_col 0 or 1 (0: one value a row; gate_row = gate_head = 0: one a column);
+ *          act: OES_GATE_PLAIN, OES_GATE_SIGMOID, OES_GATE_SILU (v / (1 + exp(-v)))
+ *   res    as x, of type res_elem; res_out may be res (then with the same strides)
+ *   y      as x, bf16; y may be x if x is bf16 (then with the same strides)
+ * Otherwise outputs must not overlap inputs or each other.  n >= 0, heads >= 1, n *
+ * heads < 2^31, dim a multiple of 8 in [8, 32768]; rows of x, res, res_out and y
+ * 16-byte aligned, of gate too where gate_col is 1 (else 2-byte); strides >= 0; scale
+ * finite.  A row whose squares add up to more than 3.4e38 has a norm of 0 (NaN where
+ * it is infinite); NaN gives NaN.  Async. */
+enum { OES_GATE_PLAIN = 0, OES_GATE_SIGMOID = 1, OES_GATE_SILU = 2 };
+typedef struct {
+  const oes_norm_spec *post, *pre;
+  const void *x, *gate, *res;
+  void *res_out, *y;
+  int64_t x_row, x_head, gate_row, gate_head, gate_col, res_row, res_head, ro_row, ro_head, y_row, y_head;
+  int32_t n, heads, dim, x_elem, res_elem, gate_act;
+  float scale;
+  int32_t reserved;        /* 0 */
+} oes_norm_args;
+oes_status oes_norm(const oes_norm_args *args, void *stream);
+
+/* y = res + scale * act(x . W^T + bias) for bf16 weights in the [out, in] convention:
+ * x bf16 [n, K], W bf16 [N, K] with rows w_row elements apart, bias bf16 [N] or NULL,
+ * res (of y's type) [n, N] or NULL (0), y [n, N] of type y_elem, OES_ELEM_BF16 or
+ * OES_ELEM_F32.
+ *   OES_ACT_NONE     v
+ *   OES_ACT_SIGMOID  1 / (1 + exp(-v))
+ *   OES_ACT_SILU     v / (1 + exp(-v))
+ *   OES_ACT_GELU     v / 2 * (1 + tanh(sqrt(2 / pi) * (v + 0.044715 v^3)))
+ *   OES_ACT_SWIGLU   silu(g) * u: W and bias have 2 N rows, [0, N) for g and [N, 2 N) for u,
+ *                    as in the gate_up banks
+ * Sums and the epilogue are fp32, y is rounded to nearest even once.  Rows of x reach
+ * their own row of y only, rows of W their own column.  K a multiple of 8 in [8,
+ * 2^20], N in [1, 2^22], n in [0, 2^19]; x, W and their rows 16-byte aligned, bias
+ * 2-byte, y and res aligned to their elements; x_row, w_row >= K, y_row, res_row >=
+ * N; scale finite.  y may be res (then with the same stride), and must not overlap an
+ * input otherwise.  Async. */
+enum { OES_ACT_NONE = 0, OES_ACT_SIGMOID = 1, OES_ACT_SILU = 2, OES_ACT_GELU = 3, OES_ACT_SWIGLU = 4 };
+oes_status oes_linear_bf16(const void *w, int64_t w_row, const void *bias, int32_t N, int32_t K, const void *x,
+                           int64_t x_row, int32_t n, int32_t act, float scale, const void *res, int64_t res_row,
+                           void *y, int64_t y_row, int32_t y_elem, void *stream);
+
+/* One token of every row of logits, from a given uniform number.  With temperature T,
+ * weights w_i = exp((l_i - max l) / T), in the order of descending l (equal ones by
+ * ascending index):
+ *   top_k   the first k (k <= 0: all)
+ *   top_p   of those, the shortest run from the start whose weights add up to at least
+ *           top_p times the weight of all of those (>= 1 or NaN: all; at least one)
+ *   min_p   of those, the ones with w_i >= min_p (<= 0 or NaN: all; counts as 1 above 1)
+ * ids[t] is the lowest index at which the running sum, over ascending indices, of what
+ * is left exceeds u[t] times its total (the last one for u >= 1, the first for u < 0 or NaN),
+ * and logprob[t] = ln(w of that index / total).  T <= 0 or NaN: the first index of the
+ * largest logit, logprob 0.  A logit of -inf or NaN is never chosen, +inf leaves the
+ * rows' +inf alone; a row with nothing to choose from gets -1 and -inf.
+ * Weights are formed in fp64 and added in integers of 2^-43 (so that the order of
+ * additions does not matter, and weights below 2^-44 count as 0).
+ *   logits      [n, vocab] bf16 or fp32 (elem), rows `row` elements apart
+ *   temperature, top_p, min_p  fp32 [n] device or NULL (1, 1, 0); top_k int32 [n] device or NULL (0)
+ *   u           fp32 [n] device
+ *   ids         int32 [n] device out, logprob fp32 [n] device out or NULL
+ *   workspace   device, 16-byte aligned, >= oes_sample_workspace bytes
+ * n in [0, 2^16], vocab in [1, 2^20], row >= vocab; pointers aligned to their elements.
+ * Async. */
+oes_status oes_sample_workspace(int32_t n, int32_t vocab, int64_t *bytes);
+oes_status oes_sample(const void *logits, int32_t elem, int64_t row, int32_t n, int32_t vocab, const float *temperature,
+                      const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *ids,
+                      float *logprob, void *workspace, int64_t workspace_bytes, void *stream);
+
 /* ------------------------------------------------------------------ measurement probes */
 /* Ceilings the benchmark divides by.  All sync and return times in ms.
  * oes_probe_h2d_dma: one hipMemcpyAsync of `bytes` from pinned host to device.

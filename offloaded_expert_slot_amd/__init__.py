@@ -23,10 +23,17 @@ and, for the layer around the expert step:
     rope_freqs(rot_dim, ...) / rope(x, y, ...) / rope_append(q, q_out, k, v, ..., kv, q_start)
     attn(q, out, kv, q_start, scale, workspace) / attn_weigh(q, lse, kv, q_start, scale, acc)
     kv_evict(kv, acc, budget, kept, new_len, workspace)
+
+and between the blocks:
+
+    Norm(weight, bias, kind, eps, offset) / norm(x, y, pre, post, gate, ..., res, res_out)
+    linear_bf16(x, w, y, bias, act, scale, res)
+    sample(logits, u, ids, workspace, temperature, top_k, top_p, min_p, logprob)
 """
 import ctypes
 import os
 import re
+import struct
 
 import numpy as np
 
@@ -44,6 +51,9 @@ OK, ERR_ARG, ERR_CAPACITY, ERR_HIP, ERR_NOMEM, ERR_STATE, ERR_UNSUPPORTED = 0, -
 FFN_NOALLOC_SCRATCH_BYTES = 16 << 20   # OES_FFN_NOALLOC_SCRATCH_BYTES of include/oes.h
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+NORM_KINDS = {"rms": 0, "layer": 1}
+GATE_ACTS = {"plain": 0, "sigmoid": 1, "silu": 2}
+ACTS = {"none": 0, "sigmoid": 1, "silu": 2, "gelu": 3, "swiglu": 4}
 MAX_BANKS = 6
 MAX_SLOTS = 4096
 
@@ -93,6 +103,23 @@ class Kv(ctypes.Structure):
                                               "max_pages")] + \
                [("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
+
+class NormSpec(ctypes.Structure):
+    """oes_norm_spec of include/oes.h."""
+    _fields_ = [("w", ctypes.c_void_p), ("b", ctypes.c_void_p), ("kind", ctypes.c_int32), ("elem", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("offset", ctypes.c_float)]
+
+
+class NormArgs(ctypes.Structure):
+    """oes_norm_args of include/oes.h."""
+    _fields_ = [(f, ctypes.c_void_p) for f in ("post", "pre", "x", "gate", "res", "res_out", "y")] + \
+               [(f, ctypes.c_int64) for f in ("x_row", "x_head", "gate_row", "gate_head", "gate_col", "res_row", "res_head",
+                                              "ro_row", "ro_head", "y_row", "y_head")] + \
+               [(f, ctypes.c_int32) for f in ("n", "heads", "dim", "x_elem", "res_elem", "gate_act")] + \
+               [("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+_NORM_ARGS = struct.Struct("=7Q11q6ifi")   # a NormArgs in one go
 
 _lib = None
 _P = ctypes.c_void_p
@@ -163,6 +190,11 @@ _SIGS = {
     "oes_attn_weigh": (_I32, [_P, _P, _I64, _I64, _P, _I32, _I32, _P, ctypes.c_float, _I32, _P, _I64, _P]),
     "oes_kv_evict_workspace": (_I32, [_P, _I32, _PI64]),
     "oes_kv_evict": (_I32, [_P, _P, _I64, _I32, _I32, _I32, _P, _P, _P, _I64, _P]),
+    "oes_norm": (_I32, [_P, _P]),
+    "oes_linear_bf16": (_I32, [_P, _I64, _P, _I32, _I32, _P, _I64, _I32, _I32, ctypes.c_float, _P, _I64, _P, _I64, _I32,
+                               _P]),
+    "oes_sample_workspace": (_I32, [_I32, _I32, _PI64]),
+    "oes_sample": (_I32, [_P, _I32, _I64, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P]),
     "oes_hybrid_workspace": (_I32, [_P, _I32, _I32, _PI64, _PI64]),
     "oes_hybrid_step": (_I32, [_P, _P, _I32, _P, _P, _P, _I32, _I32, _P, _P, _P, _I64, _P, _I64, _P, _I64, _I32,
                                ctypes.c_double, _P]),
@@ -819,3 +851,163 @@ def kv_evict(kv, acc, budget, kept, new_len, workspace, first=0, last=0, stream=
     _enqueue(dev, lib().oes_kv_evict, kv._ref, *_acc(kv, acc), budget, first, last,
              _typed("kept", kept, th.i32, (kv.batch, kv.kv_heads, budget), dev),
              _typed("new_len", new_len, th.i32, (kv.batch,), dev), *_workspace(workspace, dev), stream=stream, kv=kv)
+
+
+# ---------------------------------------------------------------- between the blocks
+class Norm:
+    """A norm's weights and kind (oes_norm_spec): gain = offset + weight, or 1 without a weight; then + bias.
+
+    weight, bias: [dim], bf16 or float32 alike; kind "rms" or "layer".
+    """
+
+    def __init__(self, weight=None, bias=None, kind="rms", eps=1e-6, offset=0.0):
+        th = _th()
+        some = weight if weight is not None else bias
+        f32 = some is not None and some.dtype == th.torch.float32
+        for name, t in (("weight", weight), ("bias", bias)):
+            if t is not None:
+                _typed(name, t, th.f32 if f32 else th.bf16, some.shape, some.device)
+                if t.dim() != 1:
+                    _bad(f"{name}: [dim], not {tuple(t.shape)}")
+        self.weight, self.bias = weight, bias
+        self.dim = None if some is None else some.shape[0]
+        self.device = None if some is None else some.device
+        self._spec = NormSpec(_ptr(weight), _ptr(bias), NORM_KINDS.get(kind, kind), ELEM_F32 if f32 else ELEM_BF16, eps,
+                              offset)
+        self._at = ctypes.addressof(self._spec)
+
+
+def _spec(name, s, dim, dev):
+    if s is None:
+        return 0
+    if s.dim is not None and (s.dim != dim or s.device != dev):
+        _bad(f"{name}: {s.dim} weights on {s.device}, not {dim} on {dev}")
+    return s._at
+
+
+def _norm_rows(name, t, shape, dev):
+    """(address, row stride, head stride) of [n, dim] or [n, heads, dim] rows."""
+    if t.shape != shape:
+        _bad(f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.device != dev:
+        _bad(f"{name}: on {t.device}, not {dev}")
+    st = t.stride()
+    if st[-1] != 1:
+        _bad(f"{name}: the values of a row must be adjacent")
+    return t.data_ptr(), st[0], st[1] if len(st) == 3 else 0
+
+
+def norm(x, y=None, pre=None, post=None, gate=None, gate_act="plain", scale=1.0, res=None, res_out=None, stream=None):
+    """r = res + scale * act(gate) * post(x) into res_out, y = pre(r) (oes_norm); every part may be left out.
+
+    x      [n, dim] or [n, heads, dim], bf16 or float32; y like x, bf16 (y may be x)
+    pre, post   Norm objects;  res, res_out like x, both bf16 or both float32 (res_out may be res)
+    gate   bf16 that broadcasts to x's shape
+    """
+    th, dev, shape = _th(), x.device, x.shape
+    if len(shape) not in (2, 3):
+        _bad(f"x: [n, dim] or [n, heads, dim], not {tuple(shape)}")
+    n, heads, dim = shape[0], shape[1] if len(shape) == 3 else 1, shape[-1]
+    kind = x.dtype
+    if kind not in th.bf16 and kind != th.torch.float32:
+        _bad(f"x: element type {kind}, not bfloat16 (or its bits as int16) or float32")
+    xp, xr, xh = _norm_rows("x", x, shape, dev)
+    rp = rr = rh = op = orow = oh = yp = yr = yh = gp = gr = gh = gc = rkind = 0
+    if res is not None or res_out is not None:
+        some = res if res is not None else res_out
+        rkind = ELEM_F32 if some.dtype == th.torch.float32 else ELEM_BF16
+        if rkind == ELEM_BF16 and some.dtype not in th.bf16:
+            _bad(f"res and res_out: element type {some.dtype}, not bfloat16 (or its bits as int16) or float32")
+        if res is not None:
+            rp, rr, rh = _norm_rows("res", res, shape, dev)
+        if res_out is not None:
+            if res_out.dtype != some.dtype:
+                _bad(f"res_out: element type {res_out.dtype}, not {some.dtype}")
+            op, orow, oh = _norm_rows("res_out", res_out, shape, dev)
+    if y is not None:
+        if y.dtype not in th.bf16:
+            _bad(f"y: element type {y.dtype}, not bfloat16 (or its bits as int16)")
+        yp, yr, yh = _norm_rows("y", y, shape, dev)
+    if gate is not None:
+        if gate.dtype not in th.bf16 or gate.device != dev:
+            _bad(f"gate: {gate.dtype} on {gate.device}, not bfloat16 (or its bits as int16) on {dev}")
+        if gate.shape != shape:
+            try:
+                gate = gate.expand(shape)
+            except RuntimeError:
+                _bad(f"gate: shape {tuple(gate.shape)} does not broadcast to {tuple(shape)}")
+        gs = gate.stride()
+        gp, gr, gh, gc = gate.data_ptr(), gs[0], gs[1] if len(gs) == 3 else 0, gs[-1]
+        if gc not in (0, 1):
+            _bad("gate: the values of a row must be adjacent, or one")
+    args = _NORM_ARGS.pack(_spec("post", post, dim, dev), _spec("pre", pre, dim, dev), xp, gp, rp, op, yp, xr, xh, gr, gh,
+                           gc, rr, rh, orow, oh, yr, yh, n, heads, dim, ELEM_F32 if kind == th.torch.float32 else ELEM_BF16,
+                           rkind, GATE_ACTS.get(gate_act, gate_act), scale, 0)
+    _enqueue(dev, lib().oes_norm, args, stream=stream)
+
+
+def linear_bf16(x, w, y, bias=None, act="none", scale=1.0, res=None, stream=None):
+    """y[n, N] = res + scale * act(x[n, K] . W^T + bias) with bf16 weights W [N, K] (oes_linear_bf16).
+
+    act: none, sigmoid, silu, gelu (its tanh form), or swiglu (w and bias have 2 N rows: gate, then up).
+    y and res: bf16 or float32 alike; y may be res.
+    """
+    th, a = _th(), ACTS.get(act, act)
+    if x.dim() != 2 or w.dim() != 2 or y.dim() != 2:
+        _bad("x [n, K], w [N, K] and y [n, N]")
+    (n, K), (rows, wk), (yn, N), dev = x.shape, w.shape, y.shape, x.device
+    if x.dtype not in th.bf16 or w.dtype not in th.bf16:
+        _bad(f"x and w: element types {x.dtype} and {w.dtype}, not bfloat16 (or its bits as int16)")
+    f32 = y.dtype == th.torch.float32
+    if not f32 and y.dtype not in th.bf16:
+        _bad(f"y: element type {y.dtype}, not bfloat16 (or its bits as int16) or float32")
+    if wk != K or yn != n or rows != (2 * N if a == 4 else N):
+        _bad(f"x {tuple(x.shape)}, w {tuple(w.shape)} and y {tuple(y.shape)} do not belong together (act {act})")
+    if w.device != dev or y.device != dev:
+        _bad(f"w on {w.device} and y on {y.device}, not {dev}")
+    xs, ws, ys = x.stride(), w.stride(), y.stride()
+    if (xs[1] != 1 and K > 1) or (ws[1] != 1 and K > 1) or (ys[1] != 1 and N > 1):
+        _bad("the values of a row of x, w or y must be adjacent")
+    bp = None if bias is None else _typed("bias", bias, th.bf16, (rows,), dev)
+    rp = rr = 0
+    if res is not None:
+        if res.shape != y.shape or res.dtype != y.dtype or res.device != dev:
+            _bad(f"res: {tuple(res.shape)} {res.dtype} on {res.device}, not as y")
+        rs = res.stride()
+        if rs[1] != 1 and N > 1:
+            _bad("the values of a row of res must be adjacent")
+        rp, rr = res.data_ptr(), rs[0]
+    _enqueue(dev, lib().oes_linear_bf16, w.data_ptr(), ws[0], bp, N, K, x.data_ptr(), xs[0], n, a, scale, rp, rr,
+             y.data_ptr(), ys[0], ELEM_F32 if f32 else ELEM_BF16, stream=stream)
+
+
+def sample_workspace_bytes(n, vocab):
+    b = _I64()
+    _check(lib().oes_sample_workspace(n, vocab, ctypes.byref(b)))
+    return b.value
+
+
+def sample(logits, u, ids, workspace, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None, stream=None):
+    """One token of every row of logits [n, vocab] from the uniform numbers u [n] into ids [n] (oes_sample).
+
+    temperature, top_p, min_p: float32 [n] or None; top_k: int32 [n] or None; logprob: float32 [n] out or None.
+    """
+    th, dev = _th(), logits.device
+    if logits.dim() != 2:
+        _bad(f"logits: [n, vocab], not {tuple(logits.shape)}")
+    n, vocab = logits.shape
+    f32 = logits.dtype == th.torch.float32
+    if not f32 and logits.dtype not in th.bf16:
+        _bad(f"logits: element type {logits.dtype}, not bfloat16 (or its bits as int16) or float32")
+    ls = logits.stride()
+    if ls[1] != 1 and vocab > 1:
+        _bad("the values of a row of logits must be adjacent")
+    rows = (n,)
+
+    def each(name, t, kinds):
+        return None if t is None else _typed(name, t, kinds, rows, dev)
+
+    _enqueue(dev, lib().oes_sample, logits.data_ptr(), ELEM_F32 if f32 else ELEM_BF16, ls[0], n, vocab,
+             each("temperature", temperature, th.f32), each("top_k", top_k, th.i32), each("top_p", top_p, th.f32),
+             each("min_p", min_p, th.f32), _typed("u", u, th.f32, rows, dev), _typed("ids", ids, th.i32, rows, dev),
+             each("logprob", logprob, th.f32), *_workspace(workspace, dev), stream=stream)

@@ -1,6 +1,7 @@
 // Host side of the operators around the expert step: argument checks and launches of
 // the 4-bit linear product, the rotary positions, attention over the paged cache, the
-// weights its entries receive, and the eviction by them.
+// weights its entries receive, and the eviction by them; of the norms between the
+// blocks, the bf16 product with its epilogue, and sampling.
 
 #include <math.h>
 #include <stdarg.h>
@@ -361,4 +362,160 @@ extern "C" oes_status oes_kv_evict(const oes_kv *kv, float *acc, int64_t acc_str
   a.new_len = new_len;
   a.ws = static_cast<int32_t *>(workspace);
   return launched(launch_evict(a, as_stream(stream)), "oes_kv_evict");
+}
+
+// ============================================================================ norms between the blocks
+namespace {
+
+oes_status check_spec(const char *what, const oes_norm_spec *s, NormSpec &out) {
+  out = NormSpec{};
+  if (!s) return OES_OK;
+  if (s->kind != OES_NORM_RMS && s->kind != OES_NORM_LAYER) return fail(OES_ERR_ARG, "%s: unknown kind %d", what, s->kind);
+  if (s->elem != OES_ELEM_BF16 && s->elem != OES_ELEM_F32) return fail(OES_ERR_UNSUPPORTED, "%s: w and b are bf16 or fp32", what);
+  if (!(s->eps >= 0) || !isfinite(s->eps) || !isfinite(s->offset)) return fail(OES_ERR_ARG, "%s: eps must be finite and >= 0, offset finite", what);
+  if (!aligned(s->w, 16) || !aligned(s->b, 16)) return fail(OES_ERR_ARG, "%s: w and b must be 16-byte aligned", what);
+  out = NormSpec{s->w, s->b, 1, s->kind == OES_NORM_LAYER, s->elem == OES_ELEM_F32, s->eps, s->offset};
+  return OES_OK;
+}
+
+// [n, heads, dim] rows of elements of `size` bytes; the stride over a single row or head counts as 0
+oes_status check_norm_rows(const char *what, const void *p, int64_t &row, int64_t &head, const oes_norm_args *a, int size, bool written) {
+  const int64_t per = 16 / size;
+  if (a->n == 1) row = 0;
+  if (a->heads == 1) head = 0;
+  if (!aligned(p, 16) || row < 0 || head < 0 || row % per || head % per)
+    return fail(OES_ERR_ARG, "%s: rows must be 16-byte aligned, strides >= 0", what);
+  if (written && ((a->n > 1 && row < a->dim) || (a->heads > 1 && head < a->dim)))
+    return fail(OES_ERR_ARG, "%s: rows that are written must not overlap", what);
+  return OES_OK;
+}
+
+}  // namespace
+
+extern "C" oes_status oes_norm(const oes_norm_args *a, void *stream) {
+  if (!a) return fail(OES_ERR_ARG, "args is NULL");
+  if (a->n < 0 || a->heads < 1 || (int64_t)a->n * a->heads > 0x7fffffff) return fail(OES_ERR_ARG, "need n >= 0, heads >= 1 and n * heads < 2^31");
+  if (a->dim < 8 || a->dim > 32768 || a->dim % 8) return fail(OES_ERR_ARG, "dim %d: a multiple of 8 in [8, 32768]", a->dim);
+  if (a->reserved != 0) return fail(OES_ERR_ARG, "reserved must be 0");
+  if (a->x_elem != OES_ELEM_BF16 && a->x_elem != OES_ELEM_F32) return fail(OES_ERR_UNSUPPORTED, "x is bf16 or fp32");
+  if ((a->res || a->res_out) && a->res_elem != OES_ELEM_BF16 && a->res_elem != OES_ELEM_F32) return fail(OES_ERR_UNSUPPORTED, "the residual is bf16 or fp32");
+  if (!isfinite(a->scale)) return fail(OES_ERR_ARG, "scale must be finite");
+  if (a->gate && (a->gate_act < OES_GATE_PLAIN || a->gate_act > OES_GATE_SILU)) return fail(OES_ERR_ARG, "unknown gate_act %d", a->gate_act);
+  NormArgs r = {};
+  oes_status st;
+  if ((st = check_spec("post", a->post, r.post)) != OES_OK) return st;
+  if ((st = check_spec("pre", a->pre, r.pre)) != OES_OK) return st;
+  if (a->n == 0) return OES_OK;
+  if (!a->res_out && !a->y) return fail(OES_ERR_ARG, "neither res_out nor y is given");
+  if (a->pre && !a->y) return fail(OES_ERR_ARG, "pre without y");
+  if (!a->x) return fail(OES_ERR_ARG, "x is NULL");
+  r.x = a->x, r.gate = a->gate, r.res = a->res, r.res_out = a->res_out, r.y = a->y;
+  r.x_row = a->x_row, r.x_head = a->x_head, r.gate_row = a->gate_row, r.gate_head = a->gate_head, r.gate_col = a->gate_col;
+  r.res_row = a->res_row, r.res_head = a->res_head, r.ro_row = a->ro_row, r.ro_head = a->ro_head, r.y_row = a->y_row, r.y_head = a->y_head;
+  const int xs = a->x_elem == OES_ELEM_F32 ? 4 : 2, rs = a->res_elem == OES_ELEM_F32 ? 4 : 2;
+  if ((st = check_norm_rows("x", a->x, r.x_row, r.x_head, a, xs, false)) != OES_OK) return st;
+  if (a->res && (st = check_norm_rows("res", a->res, r.res_row, r.res_head, a, rs, false)) != OES_OK) return st;
+  if (a->res_out && (st = check_norm_rows("res_out", a->res_out, r.ro_row, r.ro_head, a, rs, true)) != OES_OK) return st;
+  if (a->y && (st = check_norm_rows("y", a->y, r.y_row, r.y_head, a, 2, true)) != OES_OK) return st;
+  if (a->gate) {
+    if (a->n == 1) r.gate_row = 0;
+    if (a->heads == 1) r.gate_head = 0;
+    if (r.gate_row < 0 || r.gate_head < 0 || (r.gate_col != 0 && r.gate_col != 1))
+      return fail(OES_ERR_ARG, "gate: strides >= 0, and 0 or 1 over the columns");
+    if (r.gate_col ? !aligned(a->gate, 16) || r.gate_row % 8 || r.gate_head % 8 : !aligned(a->gate, 2))
+      return fail(OES_ERR_ARG, "gate: rows must be 16-byte aligned (one value a row: 2-byte)");
+  }
+  if (a->res_out == a->x || (a->res_out && a->res_out == a->y)) return fail(OES_ERR_ARG, "res_out must be neither x nor y");
+  if (a->res_out && a->res_out == a->res && (r.ro_row != r.res_row || r.ro_head != r.res_head))
+    return fail(OES_ERR_ARG, "in place, res_out has the strides of res");
+  if (a->y && a->y == a->x && (a->x_elem != OES_ELEM_BF16 || r.y_row != r.x_row || r.y_head != r.x_head))
+    return fail(OES_ERR_ARG, "in place, y has the type and the strides of x");
+  if (a->y && (a->y == a->res || a->y == a->gate)) return fail(OES_ERR_ARG, "y must be neither res nor gate");
+  if (a->res_out && a->res_out == a->gate) return fail(OES_ERR_ARG, "res_out must not be gate");
+  r.n = a->n, r.heads = a->heads, r.dim = a->dim;
+  r.x_f32 = a->x_elem == OES_ELEM_F32, r.res_f32 = a->res_elem == OES_ELEM_F32;
+  r.gate_act = a->gate_act, r.scale = a->scale;
+  return launched(launch_norm(r, as_stream(stream)), "oes_norm");
+}
+
+// ============================================================================ bf16 product with an epilogue
+extern "C" oes_status oes_linear_bf16(const void *w, int64_t w_row, const void *bias, int32_t N, int32_t K, const void *x,
+                                      int64_t x_row, int32_t n, int32_t act, float scale, const void *res, int64_t res_row,
+                                      void *y, int64_t y_row, int32_t y_elem, void *stream) {
+  if (N < 1 || K < 8 || K % 8 || K > (1 << 20)) return fail(OES_ERR_ARG, "need N >= 1 and K a multiple of 8 up to 2^20");
+  if (n < 0) return fail(OES_ERR_ARG, "n < 0");
+  if (N > (1 << 22) || n > (1 << 19)) return fail(OES_ERR_UNSUPPORTED, "N = %d, n = %d: at most 2^22 rows and 2^19 tokens", N, n);
+  if (act < OES_ACT_NONE || act > OES_ACT_SWIGLU) return fail(OES_ERR_ARG, "unknown act %d", act);
+  if (y_elem != OES_ELEM_BF16 && y_elem != OES_ELEM_F32) return fail(OES_ERR_UNSUPPORTED, "y is bf16 or fp32");
+  if (!isfinite(scale)) return fail(OES_ERR_ARG, "scale must be finite");
+  if (n == 0) return OES_OK;
+  if (!w || !x || !y) return fail(OES_ERR_ARG, "NULL input");
+  if (n == 1) x_row = y_row = res_row = 0;   // the stride over a single row does not count
+  if (N == 1 && act != OES_ACT_SWIGLU) w_row = 0;
+  const int size = y_elem == OES_ELEM_F32 ? 4 : 2;
+  if (!aligned(w, 16) || !aligned(x, 16) || w_row % 8 || x_row % 8) return fail(OES_ERR_ARG, "the rows of w and x must be 16-byte aligned");
+  if (!aligned(bias, 2) || !aligned(y, size) || !aligned(res, size)) return fail(OES_ERR_ARG, "bias, y and res must be aligned to their elements");
+  if (w_row < 0 || x_row < 0 || y_row < 0 || res_row < 0) return fail(OES_ERR_ARG, "strides must be >= 0");
+  if (((N > 1 || act == OES_ACT_SWIGLU) && w_row < K) || (n > 1 && (x_row < K || y_row < N || (res && res_row < N))))
+    return fail(OES_ERR_ARG, "w_row, x_row < K or y_row, res_row < N");
+  if (y == res && y_row != res_row) return fail(OES_ERR_ARG, "in place, y has the stride of res");
+  if (y == x || y == w || y == bias) return fail(OES_ERR_ARG, "y must not be an input other than res");
+  DenseArgs a = {};
+  a.w = static_cast<const uint16_t *>(w);
+  a.bias = static_cast<const uint16_t *>(bias);
+  a.x = static_cast<const uint16_t *>(x);
+  a.res = res;
+  a.y = y;
+  a.w_row = w_row, a.x_row = x_row, a.res_row = res_row, a.y_row = y_row;
+  a.N = N, a.K = K, a.n = n, a.act = act, a.y_f32 = y_elem == OES_ELEM_F32;
+  a.scale = scale;
+  if (!linear_bf16_fits(a)) return too_large();
+  return launched(launch_linear_bf16(a, as_stream(stream)), "oes_linear_bf16");
+}
+
+// ============================================================================ sampling
+namespace {
+oes_status check_sample(int32_t n, int32_t vocab) {
+  if (n < 0 || vocab < 1) return fail(OES_ERR_ARG, "need n >= 0 and vocab >= 1");
+  if (n > (1 << 16) || vocab > (1 << 20)) return fail(OES_ERR_UNSUPPORTED, "n = %d, vocab = %d: at most 2^16 rows of 2^20", n, vocab);
+  return OES_OK;
+}
+}  // namespace
+
+extern "C" oes_status oes_sample_workspace(int32_t n, int32_t vocab, int64_t *bytes) {
+  if (!bytes) return fail(OES_ERR_ARG, "bytes is NULL");
+  oes_status st = check_sample(n, vocab);
+  if (st != OES_OK) return st;
+  *bytes = sample_workspace_bytes(n, vocab);
+  return OES_OK;
+}
+
+extern "C" oes_status oes_sample(const void *logits, int32_t elem, int64_t row, int32_t n, int32_t vocab,
+                                 const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                                 const float *u, int32_t *ids, float *logprob, void *workspace, int64_t workspace_bytes,
+                                 void *stream) {
+  oes_status st = check_sample(n, vocab);
+  if (st != OES_OK) return st;
+  if (elem != OES_ELEM_BF16 && elem != OES_ELEM_F32) return fail(OES_ERR_UNSUPPORTED, "logits are bf16 or fp32");
+  if (n == 0) return OES_OK;
+  if (!logits || !u || !ids) return fail(OES_ERR_ARG, "logits / u / ids are NULL");
+  if (!aligned(logits, elem == OES_ELEM_F32 ? 4 : 2) || !aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) ||
+      !aligned(min_p, 4) || !aligned(u, 4) || !aligned(ids, 4) || !aligned(logprob, 4))
+    return fail(OES_ERR_ARG, "pointers must be aligned to their elements");
+  if (n > 1 && row < vocab) return fail(OES_ERR_ARG, "row < vocab");
+  if (n == 1) row = 0;
+  const int64_t need = sample_workspace_bytes(n, vocab);
+  if (workspace_bytes < need) return fail(OES_ERR_ARG, "workspace %lld < %lld bytes", (long long)workspace_bytes, (long long)need);
+  if (need > 0 && (!workspace || !aligned(workspace, 16))) return fail(OES_ERR_ARG, "workspace is NULL or not 16-byte aligned");
+  SampleArgs a = {};
+  a.logits = logits;
+  a.row = row;
+  a.f32 = elem == OES_ELEM_F32;
+  a.n = n, a.vocab = vocab;
+  a.temperature = temperature, a.top_p = top_p, a.min_p = min_p, a.u = u;
+  a.top_k = top_k;
+  a.ids = ids;
+  a.logprob = logprob;
+  a.ws = static_cast<uint8_t *>(workspace);
+  return launched(launch_sample(a, as_stream(stream)), "oes_sample");
 }

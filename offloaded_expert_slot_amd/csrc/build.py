@@ -13,7 +13,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 PKG = os.path.dirname(HERE)
 ROOT = os.path.dirname(PKG)
 SOURCES = ["api.hip", "k_lru.hip", "k_copy.hip", "k_route.hip", "k_ffn.hip", "k_prefill.hip", "api_layer.hip",
-           "k_linear.hip", "k_rope.hip", "k_attn.hip", "k_evict.hip", "cpu_moe.cpp", "host_common.cpp"]
+           "k_linear.hip", "k_rope.hip", "k_attn.hip", "k_evict.hip", "k_norm.hip", "k_linear_bf16.hip",
+           "k_sample.hip", "cpu_moe.cpp", "host_common.cpp"]
 OUT = os.path.join(PKG, "liboes.so")
 BUILD = os.path.join(HERE, "_build")
 

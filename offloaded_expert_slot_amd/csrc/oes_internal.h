@@ -188,6 +188,46 @@ bool evict_fits(const oes_kv &kv);
 int64_t evict_workspace_bytes(const oes_kv &kv, int budget);
 hipError_t launch_evict(const EvictArgs &a, hipStream_t s);
 
+// ---------------------------------------------------------------- between the blocks
+struct NormSpec {         // a norm, by value
+  const void *w, *b;
+  int32_t on, layer, f32;  // on: 0 = the identity; f32: w and b are fp32
+  float eps, offset;
+};
+struct NormArgs {
+  NormSpec post, pre;
+  const void *x, *gate, *res;
+  void *res_out, *y;
+  int64_t x_row, x_head, gate_row, gate_head, gate_col, res_row, res_head, ro_row, ro_head, y_row, y_head;
+  int32_t n, heads, dim, x_f32, res_f32, gate_act;
+  float scale;
+};
+hipError_t launch_norm(const NormArgs &a, hipStream_t s);
+
+struct DenseArgs {        // oes_linear_bf16
+  const uint16_t *w, *bias, *x;
+  const void *res;
+  void *y;
+  int64_t w_row, x_row, res_row, y_row;
+  int32_t N, K, n, act, y_f32;
+  float scale;
+};
+bool linear_bf16_fits(const DenseArgs &a);
+hipError_t launch_linear_bf16(const DenseArgs &a, hipStream_t s);
+
+struct SampleArgs {
+  const void *logits;
+  int64_t row;
+  int32_t f32, n, vocab;
+  const float *temperature, *top_p, *min_p, *u;
+  const int32_t *top_k;
+  int32_t *ids;
+  float *logprob;
+  uint8_t *ws;
+};
+int64_t sample_workspace_bytes(int n, int vocab);
+hipError_t launch_sample(const SampleArgs &a, hipStream_t s);
+
 // ---------------------------------------------------------------- probes
 hipError_t launch_stream_copy(uint8_t *dst, const uint8_t *src, int64_t bytes, int blocks,
                               hipStream_t s);
