@@ -79,6 +79,8 @@ def test_product_refuses():
     for bad in (dict(N=(1 << 22) + 1, y_row=1 << 23), dict(n=(1 << 19) + 1), dict(y_elem=oes.ELEM_FP16)):
         assert product(**bad) == oes.ERR_UNSUPPORTED, bad
     assert product(n=0, w=0, x=0, y=0) == oes.OK
+    # more workgroups than a launch holds
+    assert product(N=1 << 22, n=1 << 19, act=4, y_row=1 << 22) == oes.ERR_UNSUPPORTED
 
 
 def sample(logits=A, elem=oes.ELEM_F32, row=100, n=3, vocab=100, t=0, k=0, p=0, m=0, u=A, ids=A, lp=0, ws=A, ws_bytes=None):
