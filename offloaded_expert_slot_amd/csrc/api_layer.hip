@@ -395,7 +395,7 @@ oes_status check_norm_rows(const char *what, const void *p, int64_t &row, int64_
 extern "C" oes_status oes_norm(const oes_norm_args *a, void *stream) {
   if (!a) return fail(OES_ERR_ARG, "args is NULL");
   if (a->n < 0 || a->heads < 1 || (int64_t)a->n * a->heads > 0x7fffffff) return fail(OES_ERR_ARG, "need n >= 0, heads >= 1 and n * heads < 2^31");
-  if (a->dim < 8 || a->dim > 32768 || a->dim % 8) return fail(OES_ERR_ARG, "dim %d: a multiple of 8 in [8, 32768]", a->dim);
+  if (a->dim < 8 || a->dim > 16384 || a->dim % 8) return fail(OES_ERR_ARG, "dim %d: a multiple of 8 in [8, 16384]", a->dim);
   if (a->reserved != 0) return fail(OES_ERR_ARG, "reserved must be 0");
   if (a->x_elem != OES_ELEM_BF16 && a->x_elem != OES_ELEM_F32) return fail(OES_ERR_UNSUPPORTED, "x is bf16 or fp32");
   if ((a->res || a->res_out) && a->res_elem != OES_ELEM_BF16 && a->res_elem != OES_ELEM_F32) return fail(OES_ERR_UNSUPPORTED, "the residual is bf16 or fp32");

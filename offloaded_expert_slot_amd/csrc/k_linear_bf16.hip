@@ -425,7 +425,7 @@ __global__ __launch_bounds__(256) void row_kernel(DenseArgs a) {
 }
 
 template <typename P>
-Tiles tiles_of(const DenseArgs &a, int band = 8) {
+Tiles tiles_of(const DenseArgs &a, int band = 4) {
   Tiles t;
   t.tiles_n = (int)(((a.act == OES_ACT_SWIGLU ? 2ll : 1ll) * a.N + P::BN - 1) / P::BN);
   t.tiles_m = (a.n + P::BM - 1) / P::BM;
@@ -434,7 +434,7 @@ Tiles tiles_of(const DenseArgs &a, int band = 8) {
 }
 
 template <typename P>
-hipError_t launch_shape(const DenseArgs &a, hipStream_t s, int band = 8) {
+hipError_t launch_shape(const DenseArgs &a, hipStream_t s, int band = 4) {
   const Tiles t = tiles_of<P>(a, band);
   const dim3 g((uint32_t)t.tiles_n * (uint32_t)t.tiles_m), b(P::threads);
   const bool swiglu = a.act == OES_ACT_SWIGLU;

@@ -28,7 +28,7 @@ def norm(pre=None, post=None, **over):
     return oes.lib().oes_norm(ctypes.byref(args), None)
 
 
-NORM_BAD = [dict(n=-1), dict(heads=0), dict(n=1 << 30, heads=4), dict(dim=0), dict(dim=60), dict(dim=32776), dict(dim=-8),
+NORM_BAD = [dict(n=-1), dict(heads=0), dict(n=1 << 30, heads=4), dict(dim=0), dict(dim=60), dict(dim=16392), dict(dim=-8),
             dict(reserved=1), dict(x=0), dict(x=A + 8), dict(x_row=124), dict(x_row=-128), dict(x_head=60), dict(res=A + 4),
             dict(res_row=4), dict(ro_row=56), dict(ro_head=32), dict(res_out=3 * A + 2), dict(y=4 * A + 8), dict(y_row=32),
             dict(y_head=56), dict(res_out=0, y=0), dict(y=0), dict(scale=math.nan), dict(scale=math.inf), dict(res_out=A),
