@@ -670,7 +670,8 @@ oes_status oes_linear_bf16(const void *w, int64_t w_row, const void *bias, int32
  *   u           fp32 [n] device
  *   ids         int32 [n] device out, logprob fp32 [n] device out or NULL
  *   workspace   device, 16-byte aligned, >= oes_sample_workspace bytes
- * n in [0, 2^16], vocab in [1, 2^20], row >= vocab; pointers aligned to their elements.
+ * n in [0, 2^16], vocab in [1, 2^20] (OES_ERR_UNSUPPORTED beyond, and for n * vocab rounded
+ * up to 8192s >= 2^36, from both calls); row >= vocab; pointers aligned to their elements.
  * Async. */
 oes_status oes_sample_workspace(int32_t n, int32_t vocab, int64_t *bytes);
 oes_status oes_sample(const void *logits, int32_t elem, int64_t row, int32_t n, int32_t vocab, const float *temperature,

@@ -478,6 +478,7 @@ namespace {
 oes_status check_sample(int32_t n, int32_t vocab) {
   if (n < 0 || vocab < 1) return fail(OES_ERR_ARG, "need n >= 0 and vocab >= 1");
   if (n > (1 << 16) || vocab > (1 << 20)) return fail(OES_ERR_UNSUPPORTED, "n = %d, vocab = %d: at most 2^16 rows of 2^20", n, vocab);
+  if (n > 0 && !sample_fits(n, vocab)) return too_large();
   return OES_OK;
 }
 }  // namespace

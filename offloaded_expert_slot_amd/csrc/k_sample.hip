@@ -5,8 +5,9 @@
 //   weigh   a workgroup per slice of a row: its largest logit, the sum of its weights, and (as far as the row's settings
 //           ask for them) numbers and weights of its entries by bins of 1 / 8 in logit / T
 //   choose  a workgroup per row: from the slices' bins the bin in which the last entry stands; if no more than kList
-//           entries stand up to there, they are gathered in LDS and everything is decided among them; otherwise the
-//           entries of that bin alone are gathered, and the token is looked for in the slice that the bins' sums name
+//           entries stand up to there, they are gathered in LDS and everything is decided among them;
+//           otherwise the entries of that bin alone are, and the token is looked for in the slice that the bins' sums
+//           name
 // Weights are formed in fp64 and are integers of 2^-43 of the largest weight of the slice (or row), so that sums by
 // atomics do not depend on their order.  fp32 would not do: over 100000 entries its sums are off by more than the
 // share of many tokens.
@@ -21,53 +22,119 @@ namespace oes {
 namespace {
 
 typedef unsigned long long u64;
+// Functions of the kernel below have barriers and take much of the workgroup's state: no calls, no stack.
+#define INLINE __attribute__((always_inline))
 constexpr int kBins = 256, kPer = 16;        // bins below the largest logit; entries of a thread of `weigh`
-constexpr int kList = 4096, kThreads = 1024;  // `choose`
-constexpr int kPairs = 512;                  // entries that are compared with one another, each with each
-constexpr int kCopies = 4;                   // of the bins in LDS, for lanes side by side
+constexpr int kList = 8192, kThreads = 512, kDigit = 9;   // `choose`: entries in LDS, threads, and their logarithm
 constexpr uint32_t kNegInf = 0x007fffffu, kPosInf = 0xff800000u;   // keys of -inf and +inf
 constexpr int kIndexBits = 20;
 constexpr u64 kNowhere = ~0ull;
 
+// A value that is the same in all lanes, kept in scalar registers.
+__device__ INLINE inline uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+__device__ INLINE inline u64 uniform(u64 v) { return (u64)uniform((uint32_t)(v >> 32)) << 32 | uniform((uint32_t)v); }
+__device__ INLINE inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ INLINE inline float uniform(float v) { return __uint_as_float(uniform(__float_as_uint(v))); }
+__device__ INLINE inline double uniform(double v) { return __builtin_bit_cast(double, uniform(__builtin_bit_cast(u64, v))); }
+
 // floats as integers of the same order; NaN below everything, -0 as 0
-__device__ inline uint32_t key_of(float v) {
+__device__ INLINE inline uint32_t key_of(float v) {
   if (v != v) return 0;
   const uint32_t b = __float_as_uint(v + 0.f);
   return b >> 31 ? ~b : b | 0x80000000u;
 }
-__device__ inline float of_key(uint32_t k) { return __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k); }
-__device__ inline u64 place_of(uint32_t key, int index) { return (u64)~key << kIndexBits | (uint32_t)index; }
-__device__ inline uint32_t key_at(u64 place) { return ~(uint32_t)(place >> kIndexBits); }
-__device__ inline int index_at(u64 place) { return (int)(place & ((1u << kIndexBits) - 1)); }
+__device__ INLINE inline float of_key(uint32_t k) { return __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k); }
+__device__ INLINE inline u64 place_of(uint32_t key, int index) { return (u64)~key << kIndexBits | (uint32_t)index; }
+__device__ INLINE inline uint32_t key_at(u64 place) { return ~(uint32_t)(place >> kIndexBits); }
+__device__ INLINE inline int index_at(u64 place) { return (int)(place & ((1u << kIndexBits) - 1)); }
 
-// exp(x) for x <= 0: x = n ln 2 + rest (ln 2 in two parts, so that n times the first is exact), |rest| <= ln 2 / 2, and
-// the Taylor series of exp(rest) to its 11th power: the next term is below 2^-47
-__device__ inline double exp_of(double x) {
-  if (!(x > -40.)) return 0.;   // below 2^-57
-  const double n = rint(x * 1.4426950408889634);
-  const double r = fma(n, -1.9082149292705877e-10, fma(n, -0.6931471803691238, x));
-  double s = 1. / 39916800;
-  const double c[] = {1. / 3628800, 1. / 362880, 1. / 40320, 1. / 5040, 1. / 720, 1. / 120, 1. / 24, 1. / 6, 0.5, 1., 1.};
+// 2^y for -45 <= y <= 0 as s 2^n, s within [0.7, 1.42]: y = n + f, and s = 2^f by a polynomial 1 + f q(f) whose q goes
+// through the values of (2^f - 1) / f at the nine Chebyshev nodes of [-1/2, 1/2]; off by 4e-14 at most, and 1 for f = 0.
+__device__ INLINE inline double exp2_parts(double y, int &n) {
+  const double magic = 0x1.8p52, t = y + magic;   // rounds y to a whole number, and leaves it in the low bits
+  n = (int)(uint32_t)__builtin_bit_cast(u64, t);
+  const double f = y - (t - magic);
+  const double c[] = {0.6931471805599453, 0.2402265069581299, 0.055504108664760424, 0.009618129159402558, 0.0013333558179043112,
+                      0.00015403455852453838, 1.525268684626772e-05, 1.3255224878668817e-06, 1.0203121063391729e-07};
+  double s = c[8];
 #pragma unroll
-  for (int i = 0; i < 11; ++i) s = fma(s, r, c[i]);
-  return ldexp(s, (int)n);
+  for (int i = 7; i >= 0; --i) s = fma(s, f, c[i]);
+  return fma(s, f, 1.);
 }
 
-// A row's logits and how they weigh against a largest one.
+// Logits in memory: rows may start at any entry, whatever its alignment, and are read by 16 bytes that are aligned.
+struct F32 {
+  typedef float elem;
+  static constexpr int n = 4;   // entries of 16 bytes
+  static __device__ INLINE float value(u32x4 w, int e) { return __uint_as_float(w[e]); }
+  static __device__ INLINE float value(float v) { return v; }
+  static __device__ INLINE void put(u32x4 &w, int e, float v) { w[e] = __float_as_uint(v); }
+};
+struct B16 {
+  typedef uint16_t elem;
+  static constexpr int n = 8;
+  static __device__ INLINE float value(u32x4 w, int e) { return e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]); }
+  static __device__ INLINE float value(uint16_t v) { return bf16f(v); }
+  static __device__ INLINE void put(u32x4 &w, int e, uint16_t v) { w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | (uint32_t)v << 16 : (w[e / 2] & 0xffff0000u) | v; }
+};
+
+// A row, and how its logits weigh against a largest one.
+template <typename L>
 struct Row {
-  const void *p;
-  int f32;
-  double inv_t;
-  __device__ uint32_t key(int i) const {
-    return key_of(f32 ? static_cast<const float *>(p)[i] : bf16f(static_cast<const uint16_t *>(p)[i]));
+  const typename L::elem *p;
+  int vocab, off;      // entries; those of the first 16 bytes that stand before the row
+  double inv_t, per;   // 1 / T, and what makes a difference of logits a power of 2
+  __device__ INLINE Row(const SampleArgs &a, int t) {
+    p = static_cast<const typename L::elem *>(a.logits) + t * a.row;
+    vocab = a.vocab;
+    off = (int)(reinterpret_cast<uintptr_t>(p) % 16 / sizeof(typename L::elem));
+  }
+  __device__ INLINE void heat(float temperature) {
+    inv_t = uniform(1. / (double)temperature);
+    per = uniform(inv_t * 1.4426950408889634);
+  }
+  __device__ INLINE uint32_t key(int i) const { return key_of(L::value(p[i])); }
+  // The entries from i + j * step on, which are 16-byte aligned; NaN outside of the row.  All are asked for at once: the
+  // words that the row has in part only are put together afterwards, since a load that hangs on a condition has the
+  // next one wait (a row of 100003 at 14.8 in place of 6.7 us).
+  template <int COUNT>
+  __device__ INLINE void words(int i, int step, u32x4 (&w)[COUNT]) const {
+    const int some = off ? L::n - off : 0;   // a word that is whole, in rows of two words and more
+#pragma unroll
+    for (int j = 0; j < COUNT; ++j) {
+      const int at = i + j * step;
+      w[j] = u32x4{~0u, ~0u, ~0u, ~0u};
+      if (vocab >= 2 * L::n) w[j] = *reinterpret_cast<const u32x4 *>(p + (at >= 0 && at + L::n <= vocab ? at : some));
+    }
+#pragma unroll
+    for (int j = 0; j < COUNT; ++j) {
+      const int at = i + j * step;
+      if (vocab >= 2 * L::n && at >= 0 && at + L::n <= vocab) continue;
+      w[j] = u32x4{~0u, ~0u, ~0u, ~0u};
+      if (at + L::n <= 0 || at >= vocab) continue;
+#pragma unroll
+      for (int e = 0; e < L::n; ++e)
+        if (at + e >= 0 && at + e < vocab) L::put(w[j], e, p[at + e]);
+    }
   }
   // the bin's number as a whole number in fp64: exact however large, and ascending with the key
-  __device__ double bin(uint32_t k) const { return k == kPosInf ? 1e300 : floor((double)of_key(k) * inv_t * 8.); }
-  __device__ double weight(uint32_t k, uint32_t top) const {
+  __device__ INLINE double bin(uint32_t k) const { return k == kPosInf ? 1e300 : floor((double)of_key(k) * inv_t * 8.); }
+  __device__ INLINE double weight(uint32_t k, uint32_t top) const {
     if (top == kPosInf || k <= kNegInf) return k == top && k > kNegInf ? 1. : 0.;
-    return exp_of(((double)of_key(k) - (double)of_key(top)) * inv_t);
+    const double y = ((double)of_key(k) - (double)of_key(top)) * per;
+    int n;
+    const double s = exp2_parts(fmax(y, -45.), n);
+    return y < -45. ? 0. : ldexp(s, n);
   }
-  __device__ u64 mass(uint32_t k, uint32_t top) const { return (u64)(weight(k, top) * 0x1p43 + 0.5); }
+  // weight in units of 2^-43, to the nearest: 2^52 more, it is the low bits of its fp64
+  __device__ INLINE u64 mass(uint32_t k, uint32_t top) const {
+    const double y = ((double)of_key(k) - (double)of_key(top)) * per;
+    int n;
+    const double s = exp2_parts(fmax(y, -45.), n);
+    const double v = fma(s, __builtin_bit_cast(double, (u64)(n + 43 + 1023) << 52), 0x1p52);
+    const u64 m = __builtin_bit_cast(u64, v) & ((1ull << 52) - 1);
+    return top == kPosInf || k <= kNegInf ? (k == top && k > kNegInf ? 1ull << 43 : 0) : y < -45. ? 0 : m;
+  }
 };
 
 // Settings of a row.
@@ -75,21 +142,22 @@ struct Rules {
   float t, p, least, u;
   int k;
   bool by_k, by_p, by_min;
-  __device__ Rules(const SampleArgs &a, int row) {
-    t = a.temperature ? a.temperature[row] : 1.f;
-    p = a.top_p ? a.top_p[row] : 1.f;
-    least = a.min_p ? a.min_p[row] : 0.f;
+  __device__ INLINE Rules(const SampleArgs &a, int row) {
+    t = uniform(a.temperature ? a.temperature[row] : 1.f);
+    p = uniform(a.top_p ? a.top_p[row] : 1.f);
+    least = uniform(a.min_p ? a.min_p[row] : 0.f);
     least = least > 1.f ? 1.f : least;   // NaN stays, and counts as none
-    k = a.top_k ? a.top_k[row] : 0;
-    u = a.u[row];
+    k = uniform(a.top_k ? a.top_k[row] : 0);
+    u = uniform(a.u[row]);
     by_k = k > 0 && k < a.vocab;
     by_p = p < 1.f;
     by_min = least > 0.f;
   }
-  __device__ bool greedy() const { return !(t > 0.f); }
-  // up to half a list the entries by k and those beside the last one nearly always fit, and no bin's weight is needed
-  __device__ bool counts() const { return !greedy() && (by_k || by_p || by_min); }
-  __device__ bool masses() const { return counts() && !(by_k && k <= kList / 2); }
+  __device__ INLINE bool greedy() const { return !(t > 0.f); }
+  __device__ INLINE bool counts() const { return !greedy() && (by_k || by_p || by_min); }
+  // up to a quarter of a list the entries by k and those beside the last one nearly always fit, and no bin's weight is
+  // needed
+  __device__ INLINE bool masses() const { return counts() && !(by_k && k <= kList / 4); }
 };
 
 // Workspace: per row and slice the first place, the sum of weights, numbers and weights by bins.
@@ -98,7 +166,7 @@ struct Slices {
   u64 *first, *sum, *mass;
   uint32_t *number;
 };
-__host__ __device__ inline Slices slices_of(const SampleArgs &a, int count, int size) {
+__device__ INLINE inline Slices slices_of(const SampleArgs &a, int count, int size) {
   Slices s;
   const int64_t all = (int64_t)a.n * count;
   s.count = count;
@@ -109,124 +177,55 @@ __host__ __device__ inline Slices slices_of(const SampleArgs &a, int count, int 
   s.number = reinterpret_cast<uint32_t *>(s.mass + all * kBins);
   return s;
 }
-// Slices of 4096, or up to 16384 entries where there would be more than 2048 of them.
+// Slices of 4096, or of 8192 entries where there would be more than 2048 of them; a row may begin with up to 7 entries of
+// another one's.
 inline int slice_threads(int n, int vocab) {
-  int threads = 256;
-  while (threads < 1024 && (int64_t)n * ((vocab + threads * kPer - 1) / (threads * kPer)) > 2048) threads *= 2;
-  return threads;
+  return (int64_t)n * ((vocab + 7 + 256 * kPer - 1) / (256 * kPer)) > 2048 ? 512 : 256;
 }
+inline int slice_count(int threads, int vocab) { return (vocab + 7 + threads * kPer - 1) / (threads * kPer); }
 
-__device__ inline u64 wave_min(u64 v) {
+__device__ INLINE inline u64 wave_min(u64 v) {
 #pragma unroll
   for (int d = 32; d; d >>= 1) v = min(v, (u64)__shfl_xor(v, d, 64));
   return v;
 }
-__device__ inline u64 wave_sum(u64 v) {
+__device__ INLINE inline u64 wave_sum(u64 v) {
 #pragma unroll
   for (int d = 32; d; d >>= 1) v += (u64)__shfl_xor(v, d, 64);
   return v;
 }
 
-__device__ inline Row row_of(const SampleArgs &a, int t, const Rules &r) {
-  Row row;
-  row.p = a.f32 ? (const void *)(static_cast<const float *>(a.logits) + t * a.row) : (const void *)(static_cast<const uint16_t *>(a.logits) + t * a.row);
-  row.f32 = a.f32;
-  row.inv_t = 1. / (double)r.t;
-  return row;
-}
-
-// Entries as they stand in memory, 16 bytes a load; rows may start at any entry, whatever its alignment.
-struct __attribute__((packed, aligned(4))) Words32 {
-  float v[4];
-  static constexpr int n = 4;
-  __device__ uint32_t key(int e) const { return key_of(v[e]); }
-  __device__ void none(int e) { v[e] = -INFINITY; }
-  __device__ void one(const void *p, int i, int e) { v[e] = static_cast<const float *>(p)[i]; }
-  static __device__ const Words32 *at(const void *p, int i) { return reinterpret_cast<const Words32 *>(static_cast<const float *>(p) + i); }
-};
-struct __attribute__((packed, aligned(2))) Words16 {
-  uint16_t v[8];
-  static constexpr int n = 8;
-  __device__ uint32_t key(int e) const { return key_of(bf16f(v[e])); }
-  __device__ void none(int e) { v[e] = 0xff80; }
-  __device__ void one(const void *p, int i, int e) { v[e] = static_cast<const uint16_t *>(p)[i]; }
-  static __device__ const Words16 *at(const void *p, int i) { return reinterpret_cast<const Words16 *>(static_cast<const uint16_t *>(p) + i); }
-};
-// entries i ...; -inf from `to` on
-template <typename W>
-__device__ inline W load_words(const void *p, int i, int to) {
-  W w;
-#pragma unroll
-  for (int e = 0; e < W::n; ++e) w.none(e);
-  if (i + W::n <= to) {
-    w = *W::at(p, i);
-  } else {
-#pragma unroll
-    for (int e = 0; e < W::n; ++e)
-      if (i + e < to) w.one(p, i + e, e);
-  }
-  return w;
-}
-// f(index, key) for all entries of a row
-template <typename W, int T, typename F>
-__device__ inline void each_word(const void *p, int to, F f) {
-  constexpr int AHEAD = 4;
-  for (int i = W::n * (int)threadIdx.x; i < to; i += W::n * T * AHEAD) {
-    W w[AHEAD];
-#pragma unroll
-    for (int j = 0; j < AHEAD; ++j) w[j] = load_words<W>(p, i + j * W::n * T, to);
-#pragma unroll
-    for (int j = 0; j < AHEAD; ++j)
-#pragma unroll
-      for (int e = 0; e < W::n; ++e) f(i + j * W::n * T + e, w[j].key(e));
-  }
-}
-template <int T, typename F>
-__device__ inline void each_entry(const Row &row, int to, F f) {
-  if (row.f32)
-    each_word<Words32, T>(row.p, to, f);
-  else
-    each_word<Words16, T>(row.p, to, f);
-}
-
 // ---------------------------------------------------------------- weigh
-template <int T>
+template <typename L, int T>
 __global__ __launch_bounds__(T) void weigh_kernel(SampleArgs a, int count) {
-  __shared__ u64 mass[kBins][kCopies], wave_first[T / 64], wave_total[T / 64];
-  __shared__ uint32_t number[kBins][kCopies];
-  const int t = blockIdx.y, slice = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ u64 mass[kBins], wave_first[T / 64], wave_total[T / 64];
+  __shared__ uint32_t number[kBins];
+  const int t = blockIdx.x / count, slice = blockIdx.x % count, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const Slices s = slices_of(a, count, T * kPer);
   const int64_t at = (int64_t)t * count + slice;
+  Row<L> row(a, t);
+  constexpr int N = L::n, WORDS = kPer / N;
+  const int from = slice * s.size - row.off + N * (int)threadIdx.x;
+  uint32_t key[WORDS][N];
+  u32x4 w[WORDS];
+  row.words(from, N * T, w);
   const Rules rules(a, t);
-  const Row row = row_of(a, t, rules);
-  const int from = slice * s.size, to = min(a.vocab, from + s.size);
+  row.heat(rules.t);
   const bool counts = rules.counts(), masses = rules.masses();
-  if (counts) {
-    for (int i = threadIdx.x; i < kBins * kCopies; i += T) {
-      mass[i / kCopies][i % kCopies] = 0;
-      number[i / kCopies][i % kCopies] = 0;
-    }
+  {
+#pragma unroll
+    for (int j = 0; j < WORDS; ++j)
+#pragma unroll
+      for (int e = 0; e < N; ++e) key[j][e] = key_of(L::value(w[j], e));
   }
-  uint32_t key[kPer];
-  auto load = [&](auto W) {
-    typedef decltype(W) Words;
-    Words w[kPer / Words::n];
-#pragma unroll
-    for (int j = 0; j < kPer / Words::n; ++j) w[j] = load_words<Words>(row.p, from + Words::n * ((int)threadIdx.x + j * T), to);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) key[i] = w[i / Words::n].key(i % Words::n);
-  };
-  if (row.f32)
-    load(Words32());
-  else
-    load(Words16());
+  if (counts)
+    for (int i = threadIdx.x; i < kBins; i += T) mass[i] = 0, number[i] = 0;
   u64 first = kNowhere;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int per = a.f32 ? 4 : 8;
-    const int index = from + per * ((int)threadIdx.x + (i / per) * T) + i % per;
-    if (key[i] > kNegInf) first = min(first, place_of(key[i], index));
-  }
+  for (int j = 0; j < WORDS; ++j)
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (key[j][e] > kNegInf) first = min(first, place_of(key[j][e], from + j * N * T + e));
   first = wave_min(first);
   if (lane == 0) wave_first[wave] = first;
   __syncthreads();
@@ -235,21 +234,12 @@ __global__ __launch_bounds__(T) void weigh_kernel(SampleArgs a, int count) {
   if (threadIdx.x == 0) s.first[at] = first;
   if (first == kNowhere || rules.greedy()) return;   // the same for the whole workgroup
   const uint32_t top = key_at(first);
-  const double top_bin = row.bin(top);
-  u64 total = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (key[i] <= kNegInf) continue;
-    if (!counts) {
-      total += row.mass(key[i], top);
-      continue;
-    }
-    const double d = top_bin - row.bin(key[i]);
-    if (!(d < kBins)) continue;
-    atomicAdd(&number[(int)d][lane % kCopies], 1u);
-    if (masses) atomicAdd(&mass[(int)d][lane % kCopies], row.mass(key[i], top));
-  }
   if (!counts) {
+    u64 total = 0;
+#pragma unroll
+    for (int j = 0; j < WORDS; ++j)
+#pragma unroll
+      for (int e = 0; e < N; ++e) total += row.mass(key[j][e], top);
     total = wave_sum(total);
     if (lane == 0) wave_total[wave] = total;
     __syncthreads();
@@ -259,20 +249,28 @@ __global__ __launch_bounds__(T) void weigh_kernel(SampleArgs a, int count) {
     }
     return;
   }
+  const double top_bin = row.bin(top);
+#pragma unroll
+  for (int j = 0; j < WORDS; ++j)
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const double d = key[j][e] > kNegInf ? top_bin - row.bin(key[j][e]) : 1e300;
+      const u64 m = masses ? row.mass(key[j][e], top) : 0;
+      if (d < kBins) {
+        atomicAdd(&number[(int)d], 1u);
+        if (m) atomicAdd(&mass[(int)d], m);
+      }
+    }
   __syncthreads();
   for (int i = threadIdx.x; i < kBins; i += T) {
-    u64 m = 0;
-    uint32_t c = 0;
-#pragma unroll
-    for (int g = 0; g < kCopies; ++g) m += mass[i][g], c += number[i][g];
-    s.number[at * kBins + i] = c;
-    if (masses) s.mass[at * kBins + i] = m;
+    s.number[at * kBins + i] = number[i];
+    if (masses) s.mass[at * kBins + i] = mass[i];
   }
 }
 
 // ---------------------------------------------------------------- choose
 // f * total for 0 <= f < 1 and total < 2^63, rounded down or up
-__device__ inline u64 share(float f, u64 total, bool up) {
+__device__ INLINE inline u64 share(float f, u64 total, bool up) {
   const uint32_t b = __float_as_uint(f);
   const int e = b >> 23;
   const u64 m = e ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
@@ -284,20 +282,22 @@ __device__ inline u64 share(float f, u64 total, bool up) {
 }
 
 struct Shared {
-  u64 place[kList], mass[kList];
+  u64 list[kList];                // places
+  u64 mass[kList];                // and weights
   u64 bin[kThreads];
+  uint32_t bin_number[kThreads];
   u64 row_mass[kBins];
   uint32_t row_number[kBins];
-  u64 slice_mass[kBins];          // at most 2^20 / 4096 slices
-  double slice_share[kBins];      // a slice's weights in those of the row
-  int slice_shift[kBins];         // bins between the row's largest logit and the slice's
+  u64 slice_mass[kBins + 1];      // at most 2^20 / 4096 slices and one
+  double slice_share[kBins + 1];  // a slice's weights in those of the row
+  int slice_shift[kBins + 1];     // bins between the row's largest logit and the slice's
   u64 wave[kThreads / 64];
-  u64 a, b, at;
+  u64 before, at;
+  uint32_t key;
   int listed;
 };
 
-// Sum, or minimum, over the workgroup.
-__device__ inline u64 all_sum(Shared &sm, u64 v) {
+__device__ INLINE inline u64 all_sum(Shared &sm, u64 v) {
   v = wave_sum(v);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) sm.wave[threadIdx.x >> 6] = v;
@@ -305,22 +305,21 @@ __device__ inline u64 all_sum(Shared &sm, u64 v) {
   v = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 64; ++w) v += sm.wave[w];
-  return v;
+  return uniform(v);
 }
-__device__ inline u64 all_min(Shared &sm, u64 v) {
+__device__ INLINE inline u64 all_min(Shared &sm, u64 v) {
   v = wave_min(v);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) sm.wave[threadIdx.x >> 6] = v;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kThreads / 64; ++w) v = min(v, sm.wave[w]);
-  return v;
+  return uniform(v);
 }
 
-// The thread whose amount `own` takes the running sum over threads, from `before` on, to target or more leaves its
-// number in sm.at and the sums before and after it in sm.a and sm.b; sm.at is kNowhere if there is none.  Returns
-// the sum of all.
-__device__ inline u64 cross(Shared &sm, u64 own, u64 before, u64 target) {
+// Where a running sum over threads reaches `target`: the thread whose amount `own` takes it there gets its number into
+// sm.at and the sum before it into sm.before; sm.at is kNowhere if none does.
+__device__ INLINE inline void cross(Shared &sm, u64 own, u64 before, u64 target) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   u64 sum = own;
 #pragma unroll
@@ -332,133 +331,255 @@ __device__ inline u64 cross(Shared &sm, u64 own, u64 before, u64 target) {
   if (lane == 63) sm.wave[wave] = sum;
   if (threadIdx.x == 0) sm.at = kNowhere;
   __syncthreads();
-  u64 all = before;
 #pragma unroll
-  for (int w = 0; w < kThreads / 64; ++w) {
+  for (int w = 0; w < kThreads / 64; ++w)
     if (w < wave) sum += sm.wave[w];
-    all += sm.wave[w];
-  }
   const u64 end = before + sum, start = end - own;
   if (start < target && end >= target) {
     sm.at = threadIdx.x;
-    sm.a = start;
-    sm.b = end;
+    sm.before = start;
   }
   __syncthreads();
-  return all;
 }
 
-// The smallest number in [lo, hi] up to which amounts add up to `target` or more, `before` counted in (hi if they never
-// do): over(f) calls f(number, amount) for the entries of the thread, and the range shrinks to 2^-10 a time.
-template <typename Over>
-__device__ u64 find(Shared &sm, u64 lo, u64 hi, u64 before, u64 target, Over over) {
+// The first of `count` entries at which the running sum of amount(i), from `before` on, reaches `target`; count - 1 if none.
+template <typename F>
+__device__ INLINE inline int locate(Shared &sm, int count, u64 before, u64 target, F amount) {
+  const int per = (count + kThreads - 1) / kThreads, from = per * (int)threadIdx.x, to = min(from + per, count);
+  u64 own = 0;
+  for (int i = from; i < to; ++i) own += amount(i);
+  cross(sm, own, before, target);
+  if (uniform(sm.at) == kNowhere) return count - 1;
+  if (sm.at == threadIdx.x) {
+    u64 sum = sm.before;
+    int i = from;
+    for (; i < to - 1; ++i) {
+      sum += amount(i);
+      if (sum >= target) break;
+    }
+    sm.listed = i;
+  }
+  __syncthreads();
+  return uniform(sm.listed);
+}
+
+// The smallest number among the list's m entries up to which amounts add up to `target`, `before` counted in (the largest
+// one if they never do); numbers are places, or indices, and lie in [lo, hi].  Histograms over the range, which shrinks
+// to 2^-9 a time, until one entry is left in it.
+enum { BY_NUMBER, BY_WEIGHT, BY_INDEX };   // one each by place, weights by place, weights by index
+__device__ INLINE inline u64 find(Shared &sm, int m, int by, u64 lo, u64 hi, u64 before, u64 target) {
+  const int tid = threadIdx.x;
   for (;;) {
     const u64 range = hi - lo;
-    const int bits = range ? 64 - __clzll(range) : 0, shift = bits > 10 ? bits - 10 : 0;
+    const int bits = range ? 64 - __clzll(range) : 0, shift = bits > kDigit ? bits - kDigit : 0;
     __syncthreads();
-    sm.bin[threadIdx.x] = 0;
+    sm.bin[tid] = 0, sm.bin_number[tid] = 0;
     __syncthreads();
-    over([&](u64 number, u64 amount) {
-      if (number >= lo && number <= hi && amount) atomicAdd(&sm.bin[(number - lo) >> shift], amount);
-    });
+    for (int i = tid; i < m; i += kThreads) {
+      const u64 number = by == BY_INDEX ? (u64)index_at(sm.list[i]) : sm.list[i], amount = by == BY_NUMBER ? 1 : sm.mass[i];
+      if (number < lo || number > hi || !amount) continue;
+      const int bin = (int)((number - lo) >> shift);
+      atomicAdd(&sm.bin_number[bin], 1u);
+      if (by != BY_NUMBER) atomicAdd(&sm.bin[bin], amount);
+    }
     __syncthreads();
-    cross(sm, sm.bin[threadIdx.x], before, target);
-    const u64 bin = sm.at, start = sm.a;
+    cross(sm, by == BY_NUMBER ? sm.bin_number[tid] : sm.bin[tid], before, target);
+    const u64 bin = uniform(sm.at);
     if (bin == kNowhere) return hi;
     lo += bin << shift;
     if (shift == 0) return lo;
     hi = min(hi, lo + (1ull << shift) - 1);
-    before = start;
+    before = uniform(sm.before);
+    if (uniform(sm.bin_number[bin]) == 1) {
+      __syncthreads();
+      for (int i = tid; i < m; i += kThreads) {
+        const u64 number = by == BY_INDEX ? (u64)index_at(sm.list[i]) : sm.list[i];
+        if (number >= lo && number <= hi && (by == BY_NUMBER || sm.mass[i])) sm.at = number;
+      }
+      __syncthreads();
+      return uniform(sm.at);
+    }
   }
 }
 
+// A pass over a row's entries: f(first index, values, which of them have keys in [from, to]) for every word of which a
+// wave has such an entry.  Comparing values tells most words apart at an operation an entry, keys at six.
+template <int AHEAD, typename L, typename F>
+__device__ INLINE inline void scan_words(const Row<L> &row, uint32_t from, uint32_t to, F f) {
+  constexpr int N = L::n;
+  const float low = of_key(from), high = of_key(to);
+  for (int i = N * (int)threadIdx.x - row.off; i < row.vocab + N * 64; i += N * kThreads * AHEAD) {
+    u32x4 w[AHEAD];
+    row.words(i, N * kThreads, w);
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      float v[N];
+      bool in[N], any = false;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        v[e] = L::value(w[j], e);
+        in[e] = v[e] >= low && v[e] <= high;
+        any |= in[e];
+      }
+      if (__any(any)) f(i + j * N * kThreads, v, in);
+    }
+  }
+}
+// f(index, key) for each of them
+template <typename L, typename F>
+__device__ INLINE inline void scan(const Row<L> &row, uint32_t from, uint32_t to, F f) {
+  scan_words<4>(row, from, to, [&](int i, const auto &v, const auto &in) INLINE {
+#pragma unroll
+    for (int e = 0; e < L::n; ++e)
+      if (in[e]) f(i + e, key_of(v[e]));
+  });
+}
+
+template <typename L>
 __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int count, int size) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   Shared &sm = *reinterpret_cast<Shared *>(lds);
-  const int t = blockIdx.x;
+  const int t = blockIdx.x, tid = threadIdx.x;
   const Slices s = slices_of(a, count, size);
   const int64_t at = (int64_t)t * count;
+  const u64 of_mine = tid < count ? s.first[at + tid] : kNowhere;
   const Rules rules(a, t);
-  const Row row = row_of(a, t, rules);
-  const u64 first = all_min(sm, (int)threadIdx.x < count ? s.first[at + threadIdx.x] : kNowhere);
+  const u64 first = all_min(sm, of_mine);
   const uint32_t top = key_at(first);
-  auto answer = [&](int id, float logprob) {
-    if (threadIdx.x == 0) {
-      a.ids[t] = id;
-      if (a.logprob) a.logprob[t] = logprob;
+  if (first == kNowhere || rules.greedy()) {
+    if (tid == 0) {
+      a.ids[t] = first == kNowhere ? -1 : index_at(first);
+      if (a.logprob) a.logprob[t] = first == kNowhere ? -INFINITY : 0.f;
     }
-  };
-  if (first == kNowhere) return answer(-1, -INFINITY);
-  if (rules.greedy()) return answer(index_at(first), 0.f);
-  const double top_bin = row.bin(top);
-  auto found = [&](int id, u64 total) {
-    const uint32_t k = row.key(id);
+    return;
+  }
+  Row<L> row(a, t);
+  row.heat(rules.t);
+  const double top_bin = uniform(row.bin(top));
+  const u64 end = place_of(kNegInf + 1, (1 << kIndexBits) - 1);   // the last place that counts
+  const u64 index_mask = (1ull << kIndexBits) - 1;
+  auto found = [&](int id, uint32_t k, u64 total) INLINE {
+    if (tid != 0) return;
     const double z = top == kPosInf ? 0. : ((double)of_key(k) - (double)of_key(top)) * row.inv_t;
-    answer(id, (float)(z - log((double)total * 0x1p-43)));
+    a.ids[t] = id;
+    if (a.logprob) a.logprob[t] = (float)(z - log((double)total * 0x1p-43));
   };
-  auto aim = [&](u64 total) {   // the running sum that the token's must reach
+  auto aim = [&](u64 total) INLINE {   // the running sum that the token's must reach
     const float u = rules.u >= 0.f ? rules.u : 0.f;   // NaN too
     return u < 1.f ? share(u, total, false) + 1 : total;
   };
-  if ((int)threadIdx.x < count) {
-    const u64 f = s.first[at + threadIdx.x];
+  auto by_p = [&](u64 total) INLINE { return rules.p > 0.f ? max(share(rules.p, total, true), 1ull) : 1ull; };
+  if (tid < count) {
+    const u64 f = of_mine;
     double d = f == kNowhere ? kBins : top_bin - row.bin(key_at(f));
     d = d < kBins ? d : kBins;
-    sm.slice_shift[threadIdx.x] = (int)d;
-    sm.slice_share[threadIdx.x] = d < kBins ? row.weight(key_at(f), top) : 0.;
+    sm.slice_shift[tid] = (int)d;
+    sm.slice_share[tid] = d < kBins ? row.weight(key_at(f), top) : 0.;
   }
+  if (tid < kBins) sm.row_mass[tid] = 0, sm.row_number[tid] = 0;
+  if (tid <= kBins) sm.slice_mass[tid] = 0;
   __syncthreads();
-  // the smallest key of bins 0 ... j, by 64 places at a time
-  auto key_from = [&](int j) {
-    if (j < 0) return top + 1;
-    uint32_t lo = kNegInf + 1, hi = top;   // the answer is in [lo, hi]
-    while (lo < hi) {
-      const uint32_t step = (hi - lo + 63) / 64, mine = lo + step * (threadIdx.x & 63);
-      const u64 in = __ballot(mine >= hi || mine < lo || top_bin - row.bin(mine) <= j);
-      const int at = __ffsll(in) - 1;   // the first place that is in; -1: behind all of them
-      const uint32_t below = at < 0 ? lo + step * 63 + 1 : at == 0 ? lo : lo + step * (at - 1) + 1;
-      if (at >= 0) hi = min(hi, lo + step * at);
-      lo = min(below, hi);
+  // The smallest key of bins 0 ... j: the first wave looks at 64 places at a time.
+  auto key_from = [&](int j) INLINE {
+    __syncthreads();
+    if (tid < 64) {
+      uint32_t lo = kNegInf + 1, hi = top;   // the answer is in [lo, hi]
+      while (lo < hi) {
+        const uint32_t step = (hi - lo + 63) / 64, mine = lo + step * tid;
+        const u64 in = __ballot(mine >= hi || top_bin - row.bin(mine) <= j);
+        const int n = __ffsll(in) - 1;   // the first place that is in; -1: behind all of them
+        const uint32_t below = n < 0 ? lo + step * 63 + 1 : n == 0 ? lo : lo + step * (n - 1) + 1;
+        if (n >= 0) hi = min(hi, lo + step * n);
+        lo = min(below, hi);
+      }
+      if (tid == 0) sm.key = j < 0 ? top + 1 : lo;
     }
-    return lo;
+    __syncthreads();
+    return uniform(sm.key);
   };
-  // what bin j of the row has from slice i, in the row's weights
-  auto part = [&](int i, int j) {
-    const int from = j - sm.slice_shift[i];
-    return from < 0 ? 0ull : (u64)((double)s.mass[(at + i) * kBins + from] * sm.slice_share[i] + 0.5);
+  // a weight of slice i in those of the row
+  auto in_row = [&](u64 v, int i) INLINE { return (u64)((double)v * sm.slice_share[i] + 0.5); };
+  auto heavy = [&](u64 place) INLINE { return !rules.by_min || row.weight(key_at(place), top) >= (double)rules.least; };
+  // The places in [lo, hi] into the list, in no order, and their weights; returns how many.
+  auto gather = [&](u64 lo, u64 hi) INLINE {
+    __syncthreads();
+    if (tid == 0) sm.listed = 0;
+    __syncthreads();
+    scan_words<64 / L::n>(row, key_at(hi), key_at(lo), [&](int i, const auto &v, const auto &in) INLINE {
+      // one addition a wave and word: lanes take their places by what the lanes before them have
+      u64 place[L::n], lanes[L::n];
+      int all = 0;
+#pragma unroll
+      for (int e = 0; e < L::n; ++e) {
+        place[e] = place_of(key_of(v[e]), i + e);
+        lanes[e] = __ballot(in[e] && place[e] >= lo && place[e] <= hi);
+        all += __popcll(lanes[e]);
+      }
+      const u64 before = (1ull << (tid & 63)) - 1;
+      int slot = 0;
+      if ((tid & 63) == 0) slot = atomicAdd(&sm.listed, all);
+      slot = uniform(slot);
+#pragma unroll
+      for (int e = 0; e < L::n; ++e) {
+        const int mine = slot + __popcll(lanes[e] & before);
+        if ((lanes[e] >> (tid & 63) & 1) && mine < kList) sm.list[mine] = place[e];
+        slot += __popcll(lanes[e]);
+      }
+    });
+    __syncthreads();
+    const int m = uniform(min(sm.listed, kList));
+    for (int i = tid; i < m; i += kThreads) sm.mass[i] = row.mass(key_at(sm.list[i]), top);
+    __syncthreads();
+    return m;
   };
+  auto listed_sum = [&](int m, u64 border) INLINE {
+    u64 v = 0;
+    for (int i = tid; i < m; i += kThreads) v += sm.list[i] <= border ? sm.mass[i] : 0;
+    return all_sum(sm, v);
+  };
+
   const bool masses = rules.masses();
-  u64 last = kNowhere, all = 0;   // the last place by k and p, the weight of all
-  int edge = kBins;               // the bin of the last place; entries of the bins before it stay whole
+  u64 last = end;        // the last place by k and p
+  int edge = kBins;      // entries of the bins before it stay whole
+  int edge_listed = -1;  // entries of the list, if it has all of bin `edge`
   if (rules.counts()) {
-    if (threadIdx.x < kBins) {
-      sm.row_mass[threadIdx.x] = 0;
-      sm.row_number[threadIdx.x] = 0;
+    {
+      const int j = tid % kBins, group = tid / kBins;
+      u64 m = 0;
+      uint32_t c = 0;
+      constexpr int GROUPS = kThreads / kBins, AHEAD = 16;
+      for (int i0 = group; i0 < count; i0 += GROUPS * AHEAD) {
+        u64 mv[AHEAD];
+        uint32_t cv[AHEAD];
+#pragma unroll
+        for (int b = 0; b < AHEAD; ++b) {
+          const int i = i0 + GROUPS * b, from = i < count ? j - sm.slice_shift[i] : -1;
+          mv[b] = cv[b] = 0;
+          if (from >= 0) {
+            cv[b] = s.number[(at + i) * kBins + from];
+            if (masses) mv[b] = s.mass[(at + i) * kBins + from];
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < AHEAD; ++b) {
+          c += cv[b];
+          if (mv[b]) m += in_row(mv[b], i0 + GROUPS * b);
+        }
+      }
+      if (c) atomicAdd(&sm.row_number[j], c);
+      if (m) atomicAdd(&sm.row_mass[j], m);
     }
     __syncthreads();
-    const int j = threadIdx.x % kBins;
-    u64 m = 0;
-    uint32_t c = 0;
-    for (int i = threadIdx.x / kBins; i < count; i += kThreads / kBins) {
-      const int from = j - sm.slice_shift[i];
-      if (from >= 0) c += s.number[(at + i) * kBins + from];
-      if (masses) m += part(i, j);
-    }
-    if (c) atomicAdd(&sm.row_number[j], c);
-    if (m) atomicAdd(&sm.row_mass[j], m);
-    __syncthreads();
-    if (masses) all = all_sum(sm, threadIdx.x < kBins ? sm.row_mass[threadIdx.x] : 0);
-    // the bin up to which an amount is reached (the last one if it is not)
-    auto bin_of = [&](bool mass, u64 target) {
-      __syncthreads();
-      cross(sm, threadIdx.x >= kBins ? 0 : mass ? sm.row_mass[threadIdx.x] : sm.row_number[threadIdx.x], 0, target);
-      return sm.at == kNowhere ? kBins - 1 : (int)sm.at;
+    const u64 all = masses ? all_sum(sm, tid < kBins ? sm.row_mass[tid] : 0) : 0;
+    // the bin up to which a number or a weight is reached (kBins if it is not)
+    auto bin_of = [&](bool mass, u64 target) INLINE {
+      cross(sm, tid >= kBins ? 0 : mass ? sm.row_mass[tid] : sm.row_number[tid], 0, target);
+      return uniform((int)min(sm.at, (u64)kBins));
     };
-    const int k_bin = rules.by_k ? bin_of(false, rules.k) : kBins - 1;
-    int upto = k_bin;
+    int upto = rules.by_k ? bin_of(false, rules.k) : kBins;
     if (rules.by_p && !rules.by_k) {
       // a little further, since a bin's weight and its entries' are rounded apart
-      const u64 want = rules.p > 0.f ? share(rules.p, all, true) : 1;
+      const u64 want = by_p(all);
       upto = bin_of(true, min(all, want + (want >> 36)));
     }
     int min_bin = kBins;   // one bin further than the smallest weight's, which is off by less
@@ -467,205 +588,160 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
       min_bin = d < kBins ? (int)d : kBins;
       if (!(rules.by_k && rules.by_p)) upto = min(upto, min_bin);   // p takes its share of all that k leaves
     }
-    __syncthreads();
-    const u64 listed = all_sum(sm, threadIdx.x <= (uint32_t)upto && threadIdx.x < kBins ? sm.row_number[threadIdx.x] : 0);
-    auto gather = [&](int low, int high) {   // places of the entries of bins low ... high, and their weights, into LDS
-      if (threadIdx.x == 0) sm.listed = 0;
-      __syncthreads();
-      const uint32_t from = key_from(high), to = key_from(low - 1);
-      each_entry<kThreads>(row, a.vocab, [&](int i, uint32_t k) {
-        if (k >= from && k < to) {
-          const int slot = atomicAdd(&sm.listed, 1);
-          if (slot < kList) {
-            sm.place[slot] = place_of(k, i);
-            sm.mass[slot] = row.mass(k, top);
-          }
+    if (all_sum(sm, tid <= upto && tid < kBins ? sm.row_number[tid] : 0) <= kList) {
+      const int m = gather(first, place_of(key_from(min(upto, kBins - 1)), index_mask));
+      u64 total = all;
+#pragma unroll 1
+      for (int by = rules.by_k ? BY_NUMBER : rules.by_p ? BY_WEIGHT : BY_INDEX;; ++by) {
+        if (by == BY_WEIGHT && !rules.by_p) continue;
+        u64 lo = first, hi = last, target = rules.k;
+        if (by == BY_WEIGHT) {
+          if (rules.by_k) total = listed_sum(m, last);
+          target = by_p(total);
+        } else if (by == BY_INDEX) {
+          for (int i = tid; i < m; i += kThreads)
+            if (sm.list[i] > last || !heavy(sm.list[i])) sm.mass[i] = 0;
+          __syncthreads();
+          total = listed_sum(m, kNowhere);
+          target = aim(total);
+          lo = 0, hi = a.vocab - 1;
         }
-      });
-      __syncthreads();
-      return min(sm.listed, kList);
-    };
-    if (listed <= kList) {
-      const int m = gather(0, upto);
-      if (m <= kPairs) {
-        // each with each: g threads an entry
-        int g = 2;
-        while (g < 16 && kThreads / g / 2 >= m) g *= 2;
-        const int i = threadIdx.x / g, sub = threadIdx.x % g;
-        const bool live = i < m;
-        const u64 me = live ? sm.place[i] : kNowhere, own = live ? sm.mass[i] : 0;
-        u64 before = 0;
-        int rank = 0;
-        for (int o = sub; o < m; o += g)
-          if (sm.place[o] < me) before += sm.mass[o], ++rank;
-        for (int d = 1; d < g; d <<= 1) before += (u64)__shfl_xor(before, d, 64), rank += __shfl_xor(rank, d, 64);
-        const bool in_k = live && (!rules.by_k || rank < rules.k);
-        bool stays = in_k;
-        if (rules.by_p) {
-          const u64 sum = rules.by_k ? all_sum(sm, in_k && sub == 0 ? own : 0) : all;
-          stays &= before < (rules.p > 0.f ? max(share(rules.p, sum, true), 1ull) : 1ull);
-        }
-        if (rules.by_min) stays &= live && row.weight(key_at(me), top) >= (double)rules.least;
-        const u64 total = all_sum(sm, stays && sub == 0 ? own : 0);
-        if (live && !stays && sub == 0) sm.mass[i] = 0;
-        __syncthreads();
-        u64 sum = 0;
-        for (int o = sub; o < m; o += g)
-          if (index_at(sm.place[o]) <= index_at(me)) sum += sm.mass[o];
-        for (int d = 1; d < g; d <<= 1) sum += (u64)__shfl_xor(sum, d, 64);
-        const u64 id = all_min(sm, stays && sum >= aim(total) ? (u64)index_at(me) : kNowhere);
-        return found((int)id, total);
+        const u64 border = find(sm, m, by, lo, hi, 0, target);
+        if (by == BY_INDEX) return found((int)border, row.key((int)border), total);
+        last = border;
       }
-      auto each = [&](auto f) {
-        for (int i = threadIdx.x; i < m; i += kThreads) f(sm.place[i], sm.mass[i]);
-      };
-      auto sum_to = [&](u64 border) {
-        u64 v = 0;
-        each([&](u64 place, u64 mass) { v += place <= border ? mass : 0; });
-        return all_sum(sm, v);
-      };
-      const u64 end = place_of(kNegInf + 1, 0) | ((1u << kIndexBits) - 1);
-      last = end;
-      if (rules.by_k) last = find(sm, first, last, 0, rules.k, [&](auto f) { each([&](u64 place, u64) { f(place, 1ull); }); });
-      if (rules.by_p) {
-        const u64 sum = rules.by_k ? sum_to(last) : all;
-        last = find(sm, first, last, 0, rules.p > 0.f ? max(share(rules.p, sum, true), 1ull) : 1ull, [&](auto f) { each(f); });
-      }
-      for (int i = threadIdx.x; i < m; i += kThreads)
-        if (sm.place[i] > last || (rules.by_min && row.weight(key_at(sm.place[i]), top) < (double)rules.least)) sm.mass[i] = 0;
-      const u64 total = sum_to(end);
-      const u64 id = find(sm, 0, a.vocab - 1, 0, aim(total), [&](auto f) { each([&](u64 place, u64 mass) { f((u64)index_at(place), mass); }); });
-      return found((int)id, total);
     }
 
-    // Too many entries.  The last place by k, and then by p, among the entries of its bin: gathered if they fit, read
-    // from the row each time if not.
-    auto over_row = [&](bool mass) {
-      return [&, mass](auto f) { each_entry<kThreads>(row, a.vocab, [&](int i, uint32_t k) {
-        if (k > kNegInf) f(place_of(k, i), mass ? row.mass(k, top) : 1ull);
-      }); };
-    };
-    auto border = [&](int bin, bool mass, u64 target) {
-      u64 before = 0;
-      if ((int)threadIdx.x < bin && threadIdx.x < kBins) before = mass ? sm.row_mass[threadIdx.x] : sm.row_number[threadIdx.x];
-      before = all_sum(sm, before);
-      const u64 end = place_of(kNegInf + 1, 0) | ((1u << kIndexBits) - 1);
-      if (sm.row_number[bin] <= kList) {
-        const int m = gather(bin, bin);
-        if (m == 0) return kNowhere;   // the amount is not reached
-        u64 lo = kNowhere, hi = 0;
-        for (int i = threadIdx.x; i < m; i += kThreads) lo = min(lo, sm.place[i]), hi = max(hi, sm.place[i]);
-        lo = all_min(sm, lo);
-        hi = ~all_min(sm, ~hi);
-        return find(sm, lo, hi, before, target, [&](auto f) {
-          for (int i = threadIdx.x; i < m; i += kThreads) f(sm.place[i], mass ? sm.mass[i] : 1ull);
+    // Too many entries.  The last place by k, and then by p, among those of its bin; if they do not fit into the list
+    // either, their places are narrowed down to 2^-9 a time by their numbers and weights.
+    auto border = [&](u64 lo, u64 hi, u64 before, u64 number, bool one, u64 target) INLINE {
+      while (number > kList) {
+        const u64 range = hi - lo;
+        const int bits = 64 - __clzll(range), shift = bits > kDigit ? bits - kDigit : 0;
+        __syncthreads();
+        sm.bin[tid] = 0, sm.bin_number[tid] = 0;
+        __syncthreads();
+        scan(row, key_at(hi), key_at(lo), [&](int i, uint32_t k) INLINE {
+          const u64 place = place_of(k, i);
+          if (place < lo || place > hi) return;
+          atomicAdd(&sm.bin_number[(place - lo) >> shift], 1u);
+          if (!one) atomicAdd(&sm.bin[(place - lo) >> shift], row.mass(k, top));
         });
+        __syncthreads();
+        cross(sm, one ? sm.bin_number[tid] : sm.bin[tid], before, target);
+        const u64 bin = uniform(sm.at);
+        if (bin == kNowhere) return hi;   // not reached
+        before = uniform(sm.before);
+        number = uniform(sm.bin_number[bin]);
+        lo += bin << shift;
+        hi = min(hi, lo + (1ull << shift) - 1);
       }
-      return mass ? find(sm, first, end, 0, target, over_row(true)) : find(sm, first, end, 0, target, over_row(false));
+      const int m = gather(lo, hi);
+      edge_listed = m;
+      return find(sm, m, one ? BY_NUMBER : BY_WEIGHT, lo, hi, before, target);
     };
-    if (rules.by_k) last = border(k_bin, false, rules.k);
-    if (rules.by_p) {
-      u64 sum = all;
-      if (rules.by_k) {
-        sum = 0;
-        each_entry<kThreads>(row, a.vocab, [&](int i, uint32_t k) { sum += k > kNegInf && place_of(k, i) <= last ? row.mass(k, top) : 0; });
-        sum = all_sum(sm, sum);
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      const bool one = pass == 0;
+      if (!(one ? rules.by_k : rules.by_p)) continue;
+      u64 target = rules.k;
+      if (!one) {
+        u64 sum = all;
+        if (rules.by_k) {
+          u64 v = 0;
+          scan(row, kNegInf + 1, top, [&](int i, uint32_t k) INLINE { v += place_of(k, i) <= last ? row.mass(k, top) : 0; });
+          sum = all_sum(sm, v);
+        }
+        target = by_p(sum);
       }
-      const u64 want = rules.p > 0.f ? max(share(rules.p, sum, true), 1ull) : 1ull;
-      if (masses) {
-        last = min(last, border(bin_of(true, want), true, want));
-      } else {
-        last = min(last, find(sm, first, last, 0, want, over_row(true)));
+      u64 lo = first, hi = last, before = 0, number = kNowhere;
+      if (one || masses) {
+        const int bin = bin_of(!one, target);
+        if (bin == kBins) continue;   // not reached: all stay
+        before = all_sum(sm, tid >= bin ? 0 : one ? sm.row_number[tid] : sm.row_mass[tid]);
+        lo = place_of(key_from(bin - 1) - 1, 0);
+        hi = place_of(key_from(bin), index_mask);
+        number = uniform(sm.row_number[bin]);
       }
+      last = min(last, border(lo, hi, before, number, one, target));
+      if (number > kList) edge_listed = -1;
     }
-    edge = last == kNowhere ? kBins : min(upto, (int)fmin(top_bin - row.bin(key_at(last)), (double)kBins));
-    if (rules.by_min) edge = min(edge, max(0, min_bin - 2));
+    edge = last >= end ? kBins : (int)fmin(top_bin - row.bin(key_at(last)), (double)kBins);
+    if (rules.by_min) edge = min(edge, max(0, min_bin - 2)), edge_listed = -1;
+    // (the list is that of the smaller of two borders, or has been given up)
+    if (rules.by_k && rules.by_p) edge_listed = -1;
   }
 
   // The slices' sums: whole bins, and what stays of the others' entries.
-  auto stays = [&](int i, uint32_t k) {
-    return k > kNegInf && place_of(k, i) <= last && !(rules.by_min && row.weight(k, top) < (double)rules.least);
-  };
-  __syncthreads();
-  for (int i = threadIdx.x; i < kBins; i += kThreads) sm.slice_mass[i] = 0;
   __syncthreads();
   if (!rules.counts()) {
-    if ((int)threadIdx.x < count) sm.slice_mass[threadIdx.x] = s.first[at + threadIdx.x] == kNowhere ? 0 : (u64)((double)s.sum[at + threadIdx.x] * sm.slice_share[threadIdx.x] + 0.5);
+    if (tid < count && sm.slice_share[tid] > 0.) sm.slice_mass[tid] = in_row(s.sum[at + tid], tid);
   } else {
     const int whole = masses ? edge : 0;
-    for (int u = threadIdx.x; u < count * kBins; u += kThreads) {
-      const int i = u / kBins, j = u % kBins;
-      const u64 v = j < whole ? part(i, j) : 0;
-      if (v) atomicAdd(&sm.slice_mass[i], v);
+    for (int u = tid; u < count * kBins; u += kThreads) {
+      const int i = u / kBins, from = u % kBins - sm.slice_shift[i];
+      const u64 v = from >= 0 && u % kBins < whole ? in_row(s.mass[(at + i) * kBins + from], i) : 0;
+      const u64 w = wave_sum(v);   // a wave's bins are of one slice
+      if ((tid & 63) == 0 && w) atomicAdd(&sm.slice_mass[i], w);
     }
-    if (whole < kBins) {
-      const uint32_t below = key_from(whole - 1);
-      each_entry<kThreads>(row, a.vocab, [&](int i, uint32_t k) {
-        if (k >= below || !stays(i, k)) return;
-        const u64 v = row.mass(k, top);
-        if (v) atomicAdd(&sm.slice_mass[i / s.size], v);
+    if (masses && edge_listed >= 0) {
+      for (int i = tid; i < edge_listed; i += kThreads)
+        if (sm.list[i] <= last) atomicAdd(&sm.slice_mass[(index_at(sm.list[i]) + row.off) / s.size], sm.mass[i]);
+    } else if (whole < kBins) {
+      const uint32_t to = key_from(whole - 1) - 1;
+      if (to > kNegInf) scan(row, kNegInf + 1, to, [&](int i, uint32_t k) INLINE {
+        if (place_of(k, i) <= last && heavy(place_of(k, i))) atomicAdd(&sm.slice_mass[(i + row.off) / s.size], row.mass(k, top));
       });
     }
   }
   __syncthreads();
-  const u64 of_slice = (int)threadIdx.x < count ? sm.slice_mass[threadIdx.x] : 0;
-  const u64 total = all_sum(sm, of_slice), target = aim(total);
+  const u64 total = all_sum(sm, tid < count ? sm.slice_mass[tid] : 0), target = aim(total);
+  cross(sm, tid < count ? sm.slice_mass[tid] : 0, 0, target);
+  const int slice = uniform((int)min(sm.at, (u64)count - 1));
+  const u64 before = uniform(sm.before);
   __syncthreads();
-  cross(sm, of_slice, 0, target);
-  const int slice = (int)min(sm.at, (u64)count - 1);
-  u64 before = sm.a;
-  __syncthreads();
-  // within the slice, entries side by side; their sum may miss the slice's by what was rounded: then the last one
-  const int per = s.size / kThreads, from = slice * s.size + per * threadIdx.x;
-  u64 own = 0, end_id = kNowhere;
-  for (int i = from; i < min(from + per, a.vocab); ++i) {
-    const uint32_t k = row.key(i);
-    const u64 v = stays(i, k) ? row.mass(k, top) : 0;
-    own += v;
-    if (v) end_id = ~(u64)i;
-  }
-  end_id = ~all_min(sm, end_id);
-  __syncthreads();
-  cross(sm, own, before, target);
-  if (sm.at == kNowhere) return found(end_id == ~kNowhere ? index_at(first) : (int)end_id, total);
-  if (sm.at == threadIdx.x) {
-    u64 sum = sm.a;
-    int id = from;
-    for (int i = from; i < min(from + per, a.vocab); ++i) {
-      const uint32_t k = row.key(i);
-      sum += stays(i, k) ? row.mass(k, top) : 0;
-      if (sum >= target) {
-        id = i;
-        break;
-      }
-    }
-    sm.b = id;
-  }
-  __syncthreads();
-  found((int)sm.b, total);
+  // within the slice, entries side by side; their sum may miss the slice's by what was rounded: then its last one
+  const int from = slice * s.size - row.off, to = min(from + s.size, a.vocab);
+  auto of_entry = [&](int i) INLINE {
+    if (from + i < 0) return 0ull;
+    const uint32_t k = row.key(from + i);
+    return k > kNegInf && place_of(k, from + i) <= last && heavy(place_of(k, from + i)) ? row.mass(k, top) : 0ull;
+  };
+  u64 behind = kNowhere;
+  for (int i = tid; i < to - from; i += kThreads)
+    if (of_entry(i)) behind = ~(u64)(from + i);
+  behind = all_min(sm, behind);
+  int id = from + locate(sm, to - from, before, target, of_entry);
+  if (uniform(sm.at) == kNowhere) id = behind == kNowhere ? index_at(first) : (int)~behind;
+  found(id, row.key(id), total);
+}
+
+template <typename L>
+hipError_t launch_logits(const SampleArgs &a, hipStream_t s) {
+  const int threads = slice_threads(a.n, a.vocab), count = slice_count(threads, a.vocab);
+  const dim3 g((uint32_t)count * (uint32_t)a.n);
+  if (threads == 256)
+    hipLaunchKernelGGL((weigh_kernel<L, 256>), g, dim3(256), 0, s, a, count);
+  else
+    hipLaunchKernelGGL((weigh_kernel<L, 512>), g, dim3(512), 0, s, a, count);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(choose_kernel<L>, dim3(a.n), dim3(kThreads), sizeof(Shared), s, a, count, threads * kPer);
+  return hipGetLastError();
 }
 
 }  // namespace
 
+bool sample_fits(int n, int vocab) {
+  const int threads = slice_threads(n, vocab);
+  return launch_fits((int64_t)n * slice_count(threads, vocab), threads) && launch_fits(n, kThreads);
+}
+
 int64_t sample_workspace_bytes(int n, int vocab) {
-  const int size = slice_threads(n, vocab) * kPer;
-  const int64_t all = (int64_t)n * ((vocab + size - 1) / size);
+  const int64_t all = (int64_t)n * slice_count(slice_threads(n, vocab), vocab);
   return (all * (16 + kBins * 12) + 15) / 16 * 16;
 }
 
-hipError_t launch_sample(const SampleArgs &a, hipStream_t s) {
-  const int threads = slice_threads(a.n, a.vocab), size = threads * kPer, count = (a.vocab + size - 1) / size;
-  const dim3 g(count, a.n);
-  if (threads == 256)
-    hipLaunchKernelGGL(weigh_kernel<256>, g, dim3(256), 0, s, a, count);
-  else if (threads == 512)
-    hipLaunchKernelGGL(weigh_kernel<512>, g, dim3(512), 0, s, a, count);
-  else
-    hipLaunchKernelGGL(weigh_kernel<1024>, g, dim3(1024), 0, s, a, count);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(choose_kernel, dim3(a.n), dim3(kThreads), sizeof(Shared), s, a, count, size);
-  return hipGetLastError();
-}
+hipError_t launch_sample(const SampleArgs &a, hipStream_t s) { return a.f32 ? launch_logits<F32>(a, s) : launch_logits<B16>(a, s); }
 
 }  // namespace oes

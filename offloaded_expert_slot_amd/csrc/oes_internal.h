@@ -225,6 +225,7 @@ struct SampleArgs {
   float *logprob;
   uint8_t *ws;
 };
+bool sample_fits(int n, int vocab);
 int64_t sample_workspace_bytes(int n, int vocab);
 hipError_t launch_sample(const SampleArgs &a, hipStream_t s);
 

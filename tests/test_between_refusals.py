@@ -99,6 +99,7 @@ def test_sample_refuses():
         assert sample(**bad) == oes.ERR_ARG, bad
     for bad in (dict(elem=oes.ELEM_FP16), dict(n=(1 << 16) + 1), dict(vocab=(1 << 20) + 1, row=1 << 21)):
         assert sample(**bad) == oes.ERR_UNSUPPORTED, bad
+    assert sample(n=1 << 16, vocab=1 << 20, row=1 << 20, ws_bytes=1 << 50) == oes.ERR_UNSUPPORTED   # beyond a launch
     assert sample(n=0, logits=0, u=0, ids=0, ws=0, ws_bytes=0) == oes.OK
     b = ctypes.c_int64()
     assert oes.lib().oes_sample_workspace(3, 100, None) == oes.lib().oes_sample_workspace(-1, 100, ctypes.byref(b)) == oes.ERR_ARG
