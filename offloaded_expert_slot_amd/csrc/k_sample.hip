@@ -68,6 +68,7 @@ struct F32 {
   static constexpr int n = 4;   // entries of 16 bytes
   static __device__ INLINE float value(u32x4 w, int e) { return __uint_as_float(w[e]); }
   static __device__ INLINE float value(float v) { return v; }
+  static __device__ INLINE float pick(u32x4 w, int e) { return __uint_as_float(e & 2 ? (e & 1 ? w.w : w.z) : e & 1 ? w.y : w.x); }
   static __device__ INLINE void put(u32x4 &w, int e, float v) { w[e] = __float_as_uint(v); }
 };
 struct B16 {
@@ -75,6 +76,10 @@ struct B16 {
   static constexpr int n = 8;
   static __device__ INLINE float value(u32x4 w, int e) { return e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]); }
   static __device__ INLINE float value(uint16_t v) { return bf16f(v); }
+  static __device__ INLINE float pick(u32x4 w, int e) {
+    const uint32_t two = e & 4 ? (e & 2 ? w.w : w.z) : e & 2 ? w.y : w.x;
+    return e & 1 ? bf16_hi(two) : bf16_lo(two);
+  }
   static __device__ INLINE void put(u32x4 &w, int e, uint16_t v) { w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | (uint32_t)v << 16 : (w[e / 2] & 0xffff0000u) | v; }
 };
 
@@ -402,37 +407,38 @@ __device__ INLINE inline u64 find(Shared &sm, int m, int by, u64 lo, u64 hi, u64
   }
 }
 
-// A pass over a row's entries: f(first index, values, which of them have keys in [from, to]) for every word of which a
-// wave has such an entry.  Comparing values tells most words apart at an operation an entry, keys at six.
-template <int AHEAD, typename L, typename F>
-__device__ INLINE inline void scan_words(const Row<L> &row, uint32_t from, uint32_t to, F f) {
-  constexpr int N = L::n;
-  const float low = of_key(from), high = of_key(to);
-  for (int i = N * (int)threadIdx.x - row.off; i < row.vocab + N * 64; i += N * kThreads * AHEAD) {
-    u32x4 w[AHEAD];
-    row.words(i, N * kThreads, w);
-#pragma unroll
-    for (int j = 0; j < AHEAD; ++j) {
-      float v[N];
-      bool in[N], any = false;
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        v[e] = L::value(w[j], e);
-        in[e] = v[e] >= low && v[e] <= high;
-        any |= in[e];
-      }
-      if (__any(any)) f(i + j * N * kThreads, v, in);
-    }
-  }
-}
-// f(index, key) for each of them
+// A pass over a row's entries: f(index, key) for those with keys in [from, to].  Comparing values tells the words without
+// such an entry apart; the others' entries are taken one a round.
 template <typename L, typename F>
 __device__ INLINE inline void scan(const Row<L> &row, uint32_t from, uint32_t to, F f) {
-  scan_words<4>(row, from, to, [&](int i, const auto &v, const auto &in) INLINE {
+  constexpr int N = L::n, AHEAD = 8;
+  const float low = of_key(from), high = of_key(to);
+#pragma unroll 1
+  for (int first = -row.off; first < row.vocab; first += N * kThreads * AHEAD) {
+    const int i = first + N * (int)threadIdx.x;
+    u32x4 w[AHEAD];
+    if (first >= 0 && first + N * kThreads * AHEAD <= row.vocab) {
 #pragma unroll
-    for (int e = 0; e < L::n; ++e)
-      if (in[e]) f(i + e, key_of(v[e]));
-  });
+      for (int j = 0; j < AHEAD; ++j) w[j] = *reinterpret_cast<const u32x4 *>(row.p + i + j * N * kThreads);
+    } else {
+      row.words(i, N * kThreads, w);
+    }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      uint32_t left = 0;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float v = L::value(w[j], e);
+        left |= v >= low && v <= high ? 1u << e : 0u;
+      }
+#pragma unroll 1
+      while (left) {
+        const int e = __ffs(left) - 1;
+        left &= left - 1;
+        f(i + j * N * kThreads + e, key_of(L::pick(w[j], e)));
+      }
+    }
+  }
 }
 
 template <typename L>
@@ -505,26 +511,11 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
     __syncthreads();
     if (tid == 0) sm.listed = 0;
     __syncthreads();
-    scan_words<64 / L::n>(row, key_at(hi), key_at(lo), [&](int i, const auto &v, const auto &in) INLINE {
-      // one addition a wave and word: lanes take their places by what the lanes before them have
-      u64 place[L::n], lanes[L::n];
-      int all = 0;
-#pragma unroll
-      for (int e = 0; e < L::n; ++e) {
-        place[e] = place_of(key_of(v[e]), i + e);
-        lanes[e] = __ballot(in[e] && place[e] >= lo && place[e] <= hi);
-        all += __popcll(lanes[e]);
-      }
-      const u64 before = (1ull << (tid & 63)) - 1;
-      int slot = 0;
-      if ((tid & 63) == 0) slot = atomicAdd(&sm.listed, all);
-      slot = uniform(slot);
-#pragma unroll
-      for (int e = 0; e < L::n; ++e) {
-        const int mine = slot + __popcll(lanes[e] & before);
-        if ((lanes[e] >> (tid & 63) & 1) && mine < kList) sm.list[mine] = place[e];
-        slot += __popcll(lanes[e]);
-      }
+    scan(row, key_at(hi), key_at(lo), [&](int i, uint32_t k) INLINE {
+      const u64 place = place_of(k, i);
+      if (place < lo || place > hi) return;
+      const int slot = atomicAdd(&sm.listed, 1);
+      if (slot < kList) sm.list[slot] = place;
     });
     __syncthreads();
     const int m = uniform(min(sm.listed, kList));
@@ -547,7 +538,7 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
       const int j = tid % kBins, group = tid / kBins;
       u64 m = 0;
       uint32_t c = 0;
-      constexpr int GROUPS = kThreads / kBins, AHEAD = 16;
+      constexpr int GROUPS = kThreads / kBins, AHEAD = 8;
       for (int i0 = group; i0 < count; i0 += GROUPS * AHEAD) {
         u64 mv[AHEAD];
         uint32_t cv[AHEAD];
@@ -700,19 +691,23 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
   const int slice = uniform((int)min(sm.at, (u64)count - 1));
   const u64 before = uniform(sm.before);
   __syncthreads();
-  // within the slice, entries side by side; their sum may miss the slice's by what was rounded: then its last one
+  // within the slice; its entries' sum may miss the slice's by what was rounded: then the last one that weighs something
   const int from = slice * s.size - row.off, to = min(from + s.size, a.vocab);
-  auto of_entry = [&](int i) INLINE {
-    if (from + i < 0) return 0ull;
-    const uint32_t k = row.key(from + i);
-    return k > kNegInf && place_of(k, from + i) <= last && heavy(place_of(k, from + i)) ? row.mass(k, top) : 0ull;
-  };
-  u64 behind = kNowhere;
-  for (int i = tid; i < to - from; i += kThreads)
-    if (of_entry(i)) behind = ~(u64)(from + i);
-  behind = all_min(sm, behind);
-  int id = from + locate(sm, to - from, before, target, of_entry);
-  if (uniform(sm.at) == kNowhere) id = behind == kNowhere ? index_at(first) : (int)~behind;
+#pragma unroll 4
+  for (int i = tid; i < to - from; i += kThreads) {
+    const uint32_t k = from + i < 0 ? 0u : row.key(from + i);
+    const u64 place = place_of(k, from + i);
+    sm.mass[i] = k > kNegInf && place <= last && heavy(place) ? row.mass(k, top) : 0;
+  }
+  __syncthreads();
+  int id = from + locate(sm, to - from, before, target, [&](int i) INLINE { return sm.mass[i]; });
+  if (uniform(sm.at) == kNowhere) {
+    u64 behind = kNowhere;
+    for (int i = tid; i < to - from; i += kThreads)
+      if (sm.mass[i]) behind = ~(u64)(from + i);
+    behind = all_min(sm, behind);
+    id = behind == kNowhere ? index_at(first) : (int)~behind;
+  }
   found(id, row.key(id), total);
 }
 
