@@ -407,30 +407,79 @@ __device__ INLINE inline u64 find(Shared &sm, int m, int by, u64 lo, u64 hi, u64
   }
 }
 
-// A pass over a row's entries: f(index, key) for those with keys in [from, to].  Comparing values tells the words without
-// such an entry apart; the others' entries are taken one a round.
+// the sum over a wave's lanes up to each, all of which are active: four shifts within rows of 16, two across them
+__device__ INLINE inline int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+  return v;
+}
+
+// A pass over a row's entries with places in [from, to].  A thread has a round of words, 32 entries, asked for together;
+// take(in, index, w) gets those to be taken as the bits of `in`, of which bit j * N + e is entry e of word j and has the
+// index index + j * N * kThreads + e.  The entries before the first and behind the last whole word come as a round of
+// their own, each as a word's first.  take is called by all lanes of a wave.
 template <typename L, typename F>
-__device__ INLINE inline void scan(const Row<L> &row, uint32_t from, uint32_t to, F f) {
-  constexpr int N = L::n, AHEAD = 8;
-  const float low = of_key(from), high = of_key(to);
+__device__ INLINE inline void scan(const Row<L> &row, u64 from, u64 to, F take) {
+  constexpr int N = L::n, AHEAD = 32 / N;
+  constexpr u64 index_mask = (1ull << kIndexBits) - 1;
+  constexpr uint32_t none = 0x7fffffffu;   // no value has the key of -0, which compares as 0
+  if (key_at(from) == none) from = place_of(none - 1, 0);
+  if (key_at(to) == none) to = place_of(none + 1, 0) | index_mask;
+  const float low = of_key(key_at(to)), high = of_key(key_at(from));
+  const int from_index = index_at(from), to_index = index_at(to);
+  const bool ragged = from_index != 0 || to_index != (int)index_mask;
+  const int head = min(row.off ? N - row.off : 0, row.vocab), whole = (row.vocab - head) / N, behind = head + whole * N;
+  const int rounds = (whole + kThreads * AHEAD - 1) / (kThreads * AHEAD), tid = threadIdx.x;
 #pragma unroll 1
-  for (int first = -row.off; first < row.vocab; first += N * kThreads * AHEAD) {
-    const int i = first + N * (int)threadIdx.x;
+  for (int r = 0; r <= rounds; ++r) {
+    const int word = r * kThreads * AHEAD + tid;   // the thread's first one
     u32x4 w[AHEAD];
-    if (first >= 0 && first + N * kThreads * AHEAD <= row.vocab) {
+    int i = head + word * N;
+    uint32_t mine = 0;   // which bits are of the row
+    if (r < rounds) {
 #pragma unroll
-      for (int j = 0; j < AHEAD; ++j) w[j] = *reinterpret_cast<const u32x4 *>(row.p + i + j * N * kThreads);
+      for (int j = 0; j < AHEAD; ++j) w[j] = *reinterpret_cast<const u32x4 *>(row.p + head + (int64_t)min(word + j * kThreads, whole - 1) * N);
+      const int words = (whole - word + kThreads - 1) / kThreads;
+      mine = words <= 0 ? 0u : words >= AHEAD ? ~0u : (1u << words * N) - 1;
     } else {
-      row.words(i, N * kThreads, w);
+      i = tid < head ? tid : behind + tid - head;
+      w[0] = u32x4{0, 0, 0, 0};
+      if (i < row.vocab) L::put(w[0], 0, row.p[i]), mine = 1;
     }
+    uint32_t in = 0;
 #pragma unroll
-    for (int j = 0; j < AHEAD; ++j) {
-      uint32_t left = 0;
+    for (int j = 0; j < AHEAD; ++j)
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         const float v = L::value(w[j], e);
-        left |= v >= low && v <= high ? 1u << e : 0u;
+        in |= v >= low && v <= high ? 1u << (j * N + e) : 0u;
       }
+    in &= mine;
+    if (ragged) {
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j)
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float v = L::value(w[j], e);
+          const int index = i + j * N * kThreads + e;
+          in &= ~((v == high && index < from_index) || (v == low && index > to_index) ? 1u << (j * N + e) : 0u);
+        }
+    }
+    if (__ballot(in != 0)) take(in, i, w);
+  }
+}
+// The same by entry: f(index, key).
+template <typename L, typename F>
+__device__ INLINE inline void scan_each(const Row<L> &row, u64 from, u64 to, F f) {
+  constexpr int N = L::n;
+  scan(row, from, to, [&](uint32_t in, int i, u32x4 (&w)[32 / N]) INLINE {
+#pragma unroll
+    for (int j = 0; j < 32 / N; ++j) {
+      uint32_t left = in >> (j * N) & ((1u << N) - 1);
 #pragma unroll 1
       while (left) {
         const int e = __ffs(left) - 1;
@@ -438,7 +487,7 @@ __device__ INLINE inline void scan(const Row<L> &row, uint32_t from, uint32_t to
         f(i + j * N * kThreads + e, key_of(L::pick(w[j], e)));
       }
     }
-  }
+  });
 }
 
 template <typename L>
@@ -463,7 +512,7 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
   row.heat(rules.t);
   const double top_bin = uniform(row.bin(top));
   const u64 end = place_of(kNegInf + 1, (1 << kIndexBits) - 1);   // the last place that counts
-  const u64 index_mask = (1ull << kIndexBits) - 1;
+  const u64 index_mask = (1ull << kIndexBits) - 1, start = first & ~index_mask;   // the largest logit's first place
   auto found = [&](int id, uint32_t k, u64 total) INLINE {
     if (tid != 0) return;
     const double z = top == kPosInf ? 0. : ((double)of_key(k) - (double)of_key(top)) * row.inv_t;
@@ -511,15 +560,26 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
     __syncthreads();
     if (tid == 0) sm.listed = 0;
     __syncthreads();
-    scan(row, key_at(hi), key_at(lo), [&](int i, uint32_t k) INLINE {
-      const u64 place = place_of(k, i);
-      if (place < lo || place > hi) return;
-      const int slot = atomicAdd(&sm.listed, 1);
-      if (slot < kList) sm.list[slot] = place;
+    scan(row, lo, hi, [&](uint32_t in, int i, u32x4 (&)[32 / L::n]) INLINE {
+      const int n = __popc(in), upto = wave_scan(n);
+      int slot = 0;
+      if ((tid & 63) == 63) slot = atomicAdd(&sm.listed, upto);
+      slot = __builtin_amdgcn_readlane(slot, 63) + upto - n;
+#pragma unroll 1
+      for (; in; in &= in - 1, ++slot) {
+        const int bit = __ffs(in) - 1;
+        if (slot < kList) sm.list[slot] = i + bit / L::n * (L::n * kThreads) + bit % L::n;
+      }
     });
     __syncthreads();
     const int m = uniform(min(sm.listed, kList));
-    for (int i = tid; i < m; i += kThreads) sm.mass[i] = row.mass(key_at(sm.list[i]), top);
+#pragma unroll 4
+    for (int i = tid; i < m; i += kThreads) {
+      const int index = (int)sm.list[i];
+      const uint32_t k = row.key(index);
+      sm.list[i] = place_of(k, index);
+      sm.mass[i] = row.mass(k, top);
+    }
     __syncthreads();
     return m;
   };
@@ -580,7 +640,7 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
       if (!(rules.by_k && rules.by_p)) upto = min(upto, min_bin);   // p takes its share of all that k leaves
     }
     if (all_sum(sm, tid <= upto && tid < kBins ? sm.row_number[tid] : 0) <= kList) {
-      const int m = gather(first, place_of(key_from(min(upto, kBins - 1)), index_mask));
+      const int m = gather(start, place_of(key_from(min(upto, kBins - 1)), index_mask));
       u64 total = all;
 #pragma unroll 1
       for (int by = rules.by_k ? BY_NUMBER : rules.by_p ? BY_WEIGHT : BY_INDEX;; ++by) {
@@ -612,9 +672,8 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
         __syncthreads();
         sm.bin[tid] = 0, sm.bin_number[tid] = 0;
         __syncthreads();
-        scan(row, key_at(hi), key_at(lo), [&](int i, uint32_t k) INLINE {
+        scan_each(row, lo, hi, [&](int i, uint32_t k) INLINE {
           const u64 place = place_of(k, i);
-          if (place < lo || place > hi) return;
           atomicAdd(&sm.bin_number[(place - lo) >> shift], 1u);
           if (!one) atomicAdd(&sm.bin[(place - lo) >> shift], row.mass(k, top));
         });
@@ -640,12 +699,12 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
         u64 sum = all;
         if (rules.by_k) {
           u64 v = 0;
-          scan(row, kNegInf + 1, top, [&](int i, uint32_t k) INLINE { v += place_of(k, i) <= last ? row.mass(k, top) : 0; });
+          scan_each(row, start, last, [&](int, uint32_t k) INLINE { v += row.mass(k, top); });
           sum = all_sum(sm, v);
         }
         target = by_p(sum);
       }
-      u64 lo = first, hi = last, before = 0, number = kNowhere;
+      u64 lo = start, hi = last, before = 0, number = kNowhere;
       if (one || masses) {
         const int bin = bin_of(!one, target);
         if (bin == kBins) continue;   // not reached: all stay
@@ -669,19 +728,35 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
     if (tid < count && sm.slice_share[tid] > 0.) sm.slice_mass[tid] = in_row(s.sum[at + tid], tid);
   } else {
     const int whole = masses ? edge : 0;
-    for (int u = tid; u < count * kBins; u += kThreads) {
-      const int i = u / kBins, from = u % kBins - sm.slice_shift[i];
-      const u64 v = from >= 0 && u % kBins < whole ? in_row(s.mass[(at + i) * kBins + from], i) : 0;
-      const u64 w = wave_sum(v);   // a wave's bins are of one slice
-      if ((tid & 63) == 0 && w) atomicAdd(&sm.slice_mass[i], w);
+    constexpr int AHEAD = 4;   // a wave takes a slice's bins, and asks for those of four slices together
+    for (int i0 = tid / 64; i0 < count && whole; i0 += kThreads / 64 * AHEAD) {
+      u64 v[AHEAD][kBins / 64];
+#pragma unroll
+      for (int b = 0; b < AHEAD; ++b)
+#pragma unroll
+        for (int c = 0; c < kBins / 64; ++c) {
+          const int i = i0 + kThreads / 64 * b, from = tid % 64 + 64 * c;
+          v[b][c] = i < count && from + sm.slice_shift[i] < whole ? s.mass[(at + i) * kBins + from] : 0;
+        }
+#pragma unroll
+      for (int b = 0; b < AHEAD; ++b) {
+        const int i = i0 + kThreads / 64 * b;
+        if (i >= count) break;   // the same for the whole wave
+        u64 sum = 0;
+#pragma unroll
+        for (int c = 0; c < kBins / 64; ++c) sum += v[b][c] ? in_row(v[b][c], i) : 0;
+        sum = wave_sum(sum);
+        if (tid % 64 == 0) sm.slice_mass[i] = sum;
+      }
     }
+    __syncthreads();
     if (masses && edge_listed >= 0) {
       for (int i = tid; i < edge_listed; i += kThreads)
         if (sm.list[i] <= last) atomicAdd(&sm.slice_mass[(index_at(sm.list[i]) + row.off) / s.size], sm.mass[i]);
     } else if (whole < kBins) {
       const uint32_t to = key_from(whole - 1) - 1;
-      if (to > kNegInf) scan(row, kNegInf + 1, to, [&](int i, uint32_t k) INLINE {
-        if (place_of(k, i) <= last && heavy(place_of(k, i))) atomicAdd(&sm.slice_mass[(i + row.off) / s.size], row.mass(k, top));
+      if (to > kNegInf) scan_each(row, place_of(to, 0), last, [&](int i, uint32_t k) INLINE {
+        if (heavy(place_of(k, i))) atomicAdd(&sm.slice_mass[(i + row.off) / s.size], row.mass(k, top));
       });
     }
   }
