@@ -89,6 +89,7 @@ struct Row {
   const typename L::elem *p;
   int vocab, off;      // entries; those of the first 16 bytes that stand before the row
   double inv_t, per;   // 1 / T, and what makes a difference of logits a power of 2
+  float bins;          // bins of a logit's 1: 8 / T
   __device__ INLINE Row(const SampleArgs &a, int t) {
     p = static_cast<const typename L::elem *>(a.logits) + t * a.row;
     vocab = a.vocab;
@@ -97,6 +98,7 @@ struct Row {
   __device__ INLINE void heat(float temperature) {
     inv_t = uniform(1. / (double)temperature);
     per = uniform(inv_t * 1.4426950408889634);
+    bins = uniform((float)fmin(inv_t * 8., (double)__FLT_MAX__));
   }
   __device__ INLINE uint32_t key(int i) const { return key_of(L::value(p[i])); }
   // The entries from i + j * step on, which are 16-byte aligned; NaN outside of the row.  All are asked for at once: the
@@ -122,8 +124,12 @@ struct Row {
         if (at + e >= 0 && at + e < vocab) L::put(w[j], e, p[at + e]);
     }
   }
-  // the bin's number as a whole number in fp64: exact however large, and ascending with the key
-  __device__ INLINE double bin(uint32_t k) const { return k == kPosInf ? 1e300 : floor((double)of_key(k) * inv_t * 8.); }
+  // The number of a value's bin, a whole number that ascends with the value.  Numbers whose difference is below kBins are
+  // subtracted without rounding, however large they are.
+  __device__ INLINE float bin(float v) const {
+    const float m = __FLT_MAX__;
+    return floorf(__builtin_amdgcn_fmed3f(__builtin_amdgcn_fmed3f(v, -m, m) * bins, -m, m));
+  }
   __device__ INLINE double weight(uint32_t k, uint32_t top) const {
     if (top == kPosInf || k <= kNegInf) return k == top && k > kNegInf ? 1. : 0.;
     const double y = ((double)of_key(k) - (double)of_key(top)) * per;
@@ -131,14 +137,17 @@ struct Row {
     const double s = exp2_parts(fmax(y, -45.), n);
     return y < -45. ? 0. : ldexp(s, n);
   }
-  // weight in units of 2^-43, to the nearest: 2^52 more, it is the low bits of its fp64
-  __device__ INLINE u64 mass(uint32_t k, uint32_t top) const {
-    const double y = ((double)of_key(k) - (double)of_key(top)) * per;
+  // the weight of v against the largest logit, which is finite, in units of 2^-43, to the nearest: 2^52 more, it is the
+  // low bits of its fp64; 0 for -inf, NaN and whatever is below 2^-44
+  __device__ INLINE u64 mass_of(float v, double top) const {
     int n;
-    const double s = exp2_parts(fmax(y, -45.), n);
-    const double v = fma(s, __builtin_bit_cast(double, (u64)(n + 43 + 1023) << 52), 0x1p52);
-    const u64 m = __builtin_bit_cast(u64, v) & ((1ull << 52) - 1);
-    return top == kPosInf || k <= kNegInf ? (k == top && k > kNegInf ? 1ull << 43 : 0) : y < -45. ? 0 : m;
+    const double s = exp2_parts(fmax(((double)v - top) * per, -45.), n);
+    const double m = fma(s, __builtin_bit_cast(double, (u64)(n + 43 + 1023) << 52), 0x1p52);
+    return __builtin_bit_cast(u64, m) & ((1ull << 52) - 1);
+  }
+  __device__ INLINE u64 mass(uint32_t k, uint32_t top) const {
+    const u64 m = mass_of(of_key(k), (double)of_key(top));
+    return top == kPosInf ? (k == top ? 1ull << 43 : 0) : m;
   }
 };
 
@@ -211,40 +220,52 @@ __global__ __launch_bounds__(T) void weigh_kernel(SampleArgs a, int count) {
   Row<L> row(a, t);
   constexpr int N = L::n, WORDS = kPer / N;
   const int from = slice * s.size - row.off + N * (int)threadIdx.x;
-  uint32_t key[WORDS][N];
   u32x4 w[WORDS];
   row.words(from, N * T, w);
   const Rules rules(a, t);
   row.heat(rules.t);
   const bool counts = rules.counts(), masses = rules.masses();
-  {
-#pragma unroll
-    for (int j = 0; j < WORDS; ++j)
-#pragma unroll
-      for (int e = 0; e < N; ++e) key[j][e] = key_of(L::value(w[j], e));
-  }
   if (counts)
     for (int i = threadIdx.x; i < kBins; i += T) mass[i] = 0, number[i] = 0;
-  u64 first = kNowhere;
+  float v[WORDS][N], largest = -INFINITY;
 #pragma unroll
   for (int j = 0; j < WORDS; ++j)
 #pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (key[j][e] > kNegInf) first = min(first, place_of(key[j][e], from + j * N * T + e));
+    for (int e = 0; e < N; ++e) {
+      v[j][e] = L::value(w[j], e);
+      largest = fmaxf(largest, v[j][e]);
+    }
+  // of the largest values the first one
+  u64 first = kNowhere;
+#pragma unroll
+  for (int j = WORDS - 1; j >= 0; --j)
+#pragma unroll
+    for (int e = N - 1; e >= 0; --e)
+      if (v[j][e] == largest) first = from + j * N * T + e;
+  first = largest > -INFINITY ? place_of(key_of(largest), (int)first) : kNowhere;
   first = wave_min(first);
   if (lane == 0) wave_first[wave] = first;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < T / 64; ++w) first = min(first, wave_first[w]);
+  first = uniform(first);
   if (threadIdx.x == 0) s.first[at] = first;
   if (first == kNowhere || rules.greedy()) return;   // the same for the whole workgroup
-  const uint32_t top = key_at(first);
+  float top = of_key(key_at(first));
+  if (top == INFINITY) {   // beside it nothing weighs
+    top = 0.f;
+#pragma unroll
+    for (int j = 0; j < WORDS; ++j)
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[j][e] = v[j][e] == INFINITY ? 0.f : -INFINITY;
+  }
+  const float top_bin = row.bin(top);
   if (!counts) {
     u64 total = 0;
 #pragma unroll
     for (int j = 0; j < WORDS; ++j)
 #pragma unroll
-      for (int e = 0; e < N; ++e) total += row.mass(key[j][e], top);
+      for (int e = 0; e < N; ++e) total += row.mass_of(v[j][e], (double)top);
     total = wave_sum(total);
     if (lane == 0) wave_total[wave] = total;
     __syncthreads();
@@ -254,14 +275,13 @@ __global__ __launch_bounds__(T) void weigh_kernel(SampleArgs a, int count) {
     }
     return;
   }
-  const double top_bin = row.bin(top);
 #pragma unroll
   for (int j = 0; j < WORDS; ++j)
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      const double d = key[j][e] > kNegInf ? top_bin - row.bin(key[j][e]) : 1e300;
-      const u64 m = masses ? row.mass(key[j][e], top) : 0;
-      if (d < kBins) {
+      const float d = top_bin - row.bin(v[j][e]);
+      const u64 m = masses ? row.mass_of(v[j][e], (double)top) : 0;
+      if (v[j][e] > -INFINITY && d < kBins) {
         atomicAdd(&number[(int)d], 1u);
         if (m) atomicAdd(&mass[(int)d], m);
       }
@@ -510,7 +530,8 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
   }
   Row<L> row(a, t);
   row.heat(rules.t);
-  const double top_bin = uniform(row.bin(top));
+  const float top_bin = row.bin(of_key(top));
+  auto bin_at = [&](uint32_t k) INLINE { return k >= top ? 0.f : top == kPosInf ? (float)kBins : top_bin - row.bin(of_key(k)); };
   const u64 end = place_of(kNegInf + 1, (1 << kIndexBits) - 1);   // the last place that counts
   const u64 index_mask = (1ull << kIndexBits) - 1, start = first & ~index_mask;   // the largest logit's first place
   auto found = [&](int id, uint32_t k, u64 total) INLINE {
@@ -526,8 +547,7 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
   auto by_p = [&](u64 total) INLINE { return rules.p > 0.f ? max(share(rules.p, total, true), 1ull) : 1ull; };
   if (tid < count) {
     const u64 f = of_mine;
-    double d = f == kNowhere ? kBins : top_bin - row.bin(key_at(f));
-    d = d < kBins ? d : kBins;
+    const float d = f == kNowhere ? (float)kBins : fminf(bin_at(key_at(f)), (float)kBins);
     sm.slice_shift[tid] = (int)d;
     sm.slice_share[tid] = d < kBins ? row.weight(key_at(f), top) : 0.;
   }
@@ -541,7 +561,7 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
       uint32_t lo = kNegInf + 1, hi = top;   // the answer is in [lo, hi]
       while (lo < hi) {
         const uint32_t step = (hi - lo + 63) / 64, mine = lo + step * tid;
-        const u64 in = __ballot(mine >= hi || top_bin - row.bin(mine) <= j);
+        const u64 in = __ballot(mine >= hi || bin_at(mine) <= (float)j);
         const int n = __ffsll(in) - 1;   // the first place that is in; -1: behind all of them
         const uint32_t below = n < 0 ? lo + step * 63 + 1 : n == 0 ? lo : lo + step * (n - 1) + 1;
         if (n >= 0) hi = min(hi, lo + step * n);
@@ -633,10 +653,12 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
       const u64 want = by_p(all);
       upto = bin_of(true, min(all, want + (want >> 36)));
     }
-    int min_bin = kBins;   // one bin further than the smallest weight's, which is off by less
+    int min_bin = kBins;   // one bin further than that of the smallest weight's logit, which is rounded
     if (rules.by_min) {
-      const double d = top == kPosInf ? 0. : top_bin - floor(((double)of_key(top) * row.inv_t + log((double)rules.least)) * 8.) + 1.;
-      min_bin = d < kBins ? (int)d : kBins;
+      const double z = (double)of_key(top) + log((double)rules.least) / row.inv_t;
+      float v = (float)z;
+      if ((double)v > z) v = of_key(key_of(v) - 1);
+      min_bin = (int)fminf(bin_at(key_of(v)) + 1.f, (float)kBins);
       if (!(rules.by_k && rules.by_p)) upto = min(upto, min_bin);   // p takes its share of all that k leaves
     }
     if (all_sum(sm, tid <= upto && tid < kBins ? sm.row_number[tid] : 0) <= kList) {
@@ -716,7 +738,7 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
       last = min(last, border(lo, hi, before, number, one, target));
       if (number > kList) edge_listed = -1;
     }
-    edge = last >= end ? kBins : (int)fmin(top_bin - row.bin(key_at(last)), (double)kBins);
+    edge = last >= end ? kBins : (int)fminf(bin_at(key_at(last)), (float)kBins);
     if (rules.by_min) edge = min(edge, max(0, min_bin - 2)), edge_listed = -1;
     // (the list is that of the smaller of two borders, or has been given up)
     if (rules.by_k && rules.by_p) edge_listed = -1;
