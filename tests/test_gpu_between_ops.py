@@ -400,6 +400,99 @@ def test_sample_extreme_spreads():
     _check_sample(torch.randn(n, V, generator=g).abs().neg() * 1e38, torch.rand(n, generator=g), 1e38, 0, 0.9)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_sample_of_the_largest_vocabulary(dtype):
+    g, V = _gen(33), 1 << 20
+    settings = [(1.0, 0, 1.0, 0.0), (1.0, 64, 0.95, 0.0), (0.7, 0, 0.9, 0.0), (1.5, 0, 0.99, 0.0), (1.0, 50000, 1.0, 0.0),
+                (1.0, 0, 1.0, 0.001)]
+    t, k, p, m = (list(v) for v in zip(*settings))
+    logits = _logits(g, len(settings), V, dtype)
+    _check_sample(logits, torch.rand(len(settings), generator=g), t, k, p, m)
+    wide = torch.empty(len(settings), V + 3, dtype=dtype, device=DEV)[:, 3:]   # an odd start, and one slice more
+    wide.copy_(logits)
+    _check_sample(wide, torch.rand(len(settings), generator=g), t, k, p, m)
+
+
+@pytest.mark.parametrize("n,V", [(100, 100003), (700, 12289), (2100, 4090)])
+def test_sample_of_many_slices(n, V):
+    """More than 2048 slices of 4096, which are then twice as long."""
+    g = _gen(n)
+    logits = _logits(g, n, V, F32)
+    few = [logits[i] for i in (0, n // 2, n - 1)]
+    u = torch.rand(n, generator=g)
+    for s in ((1.0, 0, 1.0, 0.0), (0.9, 40, 0.9, 0.0), (1.0, 0, 0.97, 0.0)):
+        ids, lp = _sample(logits, u, *s)
+        for i, row in zip((0, n // 2, n - 1), few):
+            token, want, margin = R.sample_row(row.numpy(), *s, u[i].item())
+            assert margin > 2.0 ** -36 and ids[i] == token and abs(lp[i].item() - want) <= 2.0 ** -24 * abs(want) + 1e-8
+        one, _ = _sample(logits[n - 1:], u[n - 1:], *s)      # as a call of its own
+        assert one[0] == ids[n - 1]
+
+
+@pytest.mark.parametrize("std", [1e-3, 0.05, 0.4])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_sample_crowded_logits(std, dtype):
+    """Far more entries within an eighth of a logit than are listed at a time, most of them different (in fp32)."""
+    g, V = _gen(17), 90001
+    settings = [(1.0, 0, 0.5, 0.0), (1.0, 30000, 0.7, 0.0), (1.0, 30000, 1.0, 0.0), (1.0, 0, 1.0, 0.9), (2.0, 20000, 0.9, 0.5),
+                (1.0, 5, 0.5, 0.0), (0.5, 0, 0.9, 0.01), (math.inf, 60000, 0.5, 0.0), (1.0, 2100, 0.9999, 0.0)]
+    t, k, p, m = (list(v) for v in zip(*settings))
+    logits = _randn(g, len(settings), V, std=std).to(dtype)
+    logits[:, ::11] = -math.inf
+    for i in range(2):
+        _check_sample(logits, torch.rand(len(settings), generator=g), t, k, p, m)
+
+
+@pytest.mark.parametrize("V", [40, 5000, 60000])
+def test_sample_infinite_logits_among_settings(V):
+    """Rows with one and several +inf under every rule and temperature: beside them nothing is chosen."""
+    g = _gen(V)
+    n = len(SETTINGS)
+    t, k, p, m = (list(v) for v in zip(*SETTINGS))
+    logits = _logits(g, n, V, F32)
+    logits[:, V // 3] = math.inf
+    logits[::2, V // 2:V // 2 + 9] = math.inf
+    logits[:, 0] = torch.finfo(F32).max
+    _check_sample(logits, torch.rand(n, generator=g), t, k, p, m)
+
+
+# ------------------------------------------------------------------ positions past 2^31
+def test_sample_rows_past_32_bits():
+    n, V, stride = 5, 20011, 1 << 30
+    g = _gen(3)
+    whole = torch.empty(stride * (n - 1) + V, device=DEV)
+    logits = whole.as_strided((n, V), (stride, 1))
+    logits.copy_(_logits(g, n, V, F32))
+    _check_sample(logits, torch.rand(n, generator=g), 1.0, 30, 0.9)
+    _check_sample(logits, torch.rand(n, generator=g), 1.0, 0, 0.999)
+
+
+def test_norm_rows_past_32_bits():
+    g, n, dim, stride = _gen(4), 5, 136, 1 << 29
+    x = _randn(g, n, dim).bfloat16()
+    whole = torch.empty(stride * (n - 1) + dim, dtype=BF16, device=DEV)
+    xv = whole.as_strided((n, dim), (stride, 1))
+    xv.copy_(x)
+    spec = _spec(g, "rms", dim, BF16)
+    y = torch.empty(n, dim, dtype=BF16, device=DEV)
+    oes.norm(xv, y, pre=spec[0])
+    want = R.normed(x.double(), torch.zeros(n, dim, dtype=torch.float64), spec[1])
+    _within(y, want[0], R.stored(*want, BF16), "x")
+    oes.norm(xv, xv, pre=spec[0])                      # in place, and rows of y as far apart
+    assert torch.equal(xv, y)
+
+
+def test_product_outputs_past_32_bits():
+    """n * N above 2^31: the last rows, and some between, against float64."""
+    g, n, N, K = _gen(6), 35000, 65537, 16
+    x, w = _randn(g, n, K).bfloat16(), _randn(g, N, K).bfloat16()
+    y = torch.empty(n, N, dtype=BF16, device=DEV)
+    oes.linear_bf16(x.to(DEV), w.to(DEV), y)
+    some = torch.tensor([0, 1, n // 2, n - 2, n - 1])
+    want, err = R.product(x[some], w, None, "none", 1.0, None)
+    _within(y[some.to(DEV)], want, R.stored(want, err, BF16), "rows")
+
+
 # ------------------------------------------------------------------ graphs, streams, repeats
 def _case(seed):
     g = _gen(seed)
