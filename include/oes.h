@@ -644,8 +644,9 @@ oes_status oes_norm(const oes_norm_args *args, void *stream);
  * their own row of y only, rows of W their own column.  K a multiple of 8 in [8,
  * 2^20], N in [1, 2^22], n in [0, 2^19]; x, W and their rows 16-byte aligned, bias
  * 2-byte, y and res aligned to their elements; x_row, w_row >= K, y_row, res_row >=
- * N; scale finite.  y may be res (then with the same stride), and must not overlap an
- * input otherwise.  Async. */
+ * N (the stride of a single row does not count); scale finite.  y may be res (then with
+ * the same stride), and must not overlap an input otherwise.  OES_ERR_UNSUPPORTED beyond
+ * these N and n.  Async. */
 enum { OES_ACT_NONE = 0, OES_ACT_SIGMOID = 1, OES_ACT_SILU = 2, OES_ACT_GELU = 3, OES_ACT_SWIGLU = 4 };
 oes_status oes_linear_bf16(const void *w, int64_t w_row, const void *bias, int32_t N, int32_t K, const void *x,
                            int64_t x_row, int32_t n, int32_t act, float scale, const void *res, int64_t res_row,
@@ -669,7 +670,7 @@ oes_status oes_linear_bf16(const void *w, int64_t w_row, const void *bias, int32
  *   temperature, top_p, min_p  fp32 [n] device or NULL (1, 1, 0); top_k int32 [n] device or NULL (0)
  *   u           fp32 [n] device
  *   ids         int32 [n] device out, logprob fp32 [n] device out or NULL
- *   workspace   device, 16-byte aligned, >= oes_sample_workspace bytes
+ *   workspace   device, 16-byte aligned, >= oes_sample_workspace bytes; one call's at a time
  * n in [0, 2^16], vocab in [1, 2^20] (OES_ERR_UNSUPPORTED beyond, and for n * vocab rounded
  * up to 8192s >= 2^36, from both calls); row >= vocab; pointers aligned to their elements.
  * Async. */

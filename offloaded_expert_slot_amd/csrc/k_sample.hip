@@ -8,9 +8,15 @@
 //           entries stand up to there, they are gathered in LDS and everything is decided among them;
 //           otherwise the entries of that bin alone are, and the token is looked for in the slice that the bins' sums
 //           name
+// A row is read twice at most (and more often only if one bin holds more than kList entries), nothing is sorted.
 // Weights are formed in fp64 and are integers of 2^-43 of the largest weight of the slice (or row), so that sums by
 // atomics do not depend on their order.  fp32 would not do: over 100000 entries its sums are off by more than the
 // share of many tokens.
+//
+// Measured, both launches replayed in a graph: one row of 100003 fp32 by k = 64 and p = 0.95 30 us, 4.6 of them weigh and
+// about 11 the gather (latency: what a workgroup's few instructions and trips to memory take one after the other); 48
+// rows of 100003 bf16, settings mixed, 60 us; 160 rows of 200003 fp32 by p 123 us: weigh 55 (2.3 TB/s; the
+// weights' fp64 and the bins' atomics), the gather about 30, the searches about 22.
 
 #include <algorithm>
 
