@@ -13,12 +13,13 @@
 // atomics do not depend on their order.  fp32 would not do: over 100000 entries its sums are off by more than the
 // share of many tokens.
 //
-// Measured, both launches replayed in a graph: one row of 100003 fp32 by k = 64 and p = 0.95 30 us, 4.6 of them weigh and
+// Measured, both launches replayed in a graph: one row of 100003 fp32 by k = 64 and p = 0.95 30 us, 4.0 of them weigh and
 // about 11 the gather (latency: what a workgroup's few instructions and trips to memory take one after the other); 48
-// rows of 100003 bf16, settings mixed, 60 us; 160 rows of 200003 fp32 by p 123 us: weigh 55 (2.3 TB/s; the
+// rows of 100003 bf16, settings mixed, 59 us; 160 rows of 200003 fp32 by p 120 us: weigh 49 (2.6 TB/s; the
 // weights' fp64 and the bins' atomics), the gather about 30, the searches about 22.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "layer_device.h"
 #include "oes_internal.h"
@@ -54,19 +55,33 @@ __device__ INLINE inline u64 place_of(uint32_t key, int index) { return (u64)~ke
 __device__ INLINE inline uint32_t key_at(u64 place) { return ~(uint32_t)(place >> kIndexBits); }
 __device__ INLINE inline int index_at(u64 place) { return (int)(place & ((1u << kIndexBits) - 1)); }
 
+// A constant in scalar registers, where an fma takes it as its third operand; as a literal it would be moved into vector
+// registers before each (18 of 70 instructions for an entry's weight and bin).
+__device__ INLINE inline double held(double v) {
+  asm("" : "+s"(v));
+  return v;
+}
 // 2^y for -45 <= y <= 0 as s 2^n, s within [0.7, 1.42]: y = n + f, and s = 2^f by a polynomial 1 + f q(f) whose q goes
 // through the values of (2^f - 1) / f at the nine Chebyshev nodes of [-1/2, 1/2]; off by 4e-14 at most, and 1 for f = 0.
-__device__ INLINE inline double exp2_parts(double y, int &n) {
-  const double magic = 0x1.8p52, t = y + magic;   // rounds y to a whole number, and leaves it in the low bits
-  n = (int)(uint32_t)__builtin_bit_cast(u64, t);
-  const double f = y - (t - magic);
-  const double c[] = {0.6931471805599453, 0.2402265069581299, 0.055504108664760424, 0.009618129159402558, 0.0013333558179043112,
-                      0.00015403455852453838, 1.525268684626772e-05, 1.3255224878668817e-06, 1.0203121063391729e-07};
-  double s = c[8];
+struct Exp2 {
+  double magic, c[9], unit, least;
+  __device__ INLINE Exp2() {
+    const double q[] = {0.6931471805599453, 0.2402265069581299, 0.055504108664760424, 0.009618129159402558, 0.0013333558179043112,
+                        0.00015403455852453838, 1.525268684626772e-05, 1.3255224878668817e-06, 1.0203121063391729e-07};
 #pragma unroll
-  for (int i = 7; i >= 0; --i) s = fma(s, f, c[i]);
-  return fma(s, f, 1.);
-}
+    for (int i = 0; i < 9; ++i) c[i] = held(q[i]);
+    magic = held(0x1.8p52), unit = held(0x1p52), least = held(-45.);
+  }
+  __device__ INLINE double parts(double y, int &n) const {
+    const double t = y + magic;   // rounds y to a whole number, and leaves it in the low bits
+    n = (int)(uint32_t)__builtin_bit_cast(u64, t);
+    const double f = y - (t - magic);
+    double s = fma(c[8], f, c[7]);
+#pragma unroll
+    for (int i = 6; i >= 0; --i) s = fma(s, f, c[i]);
+    return fma(s, f, 1.);
+  }
+};
 
 // Logits in memory: rows may start at any entry, whatever its alignment, and are read by 16 bytes that are aligned.
 struct F32 {
@@ -96,6 +111,7 @@ struct Row {
   int vocab, off;      // entries; those of the first 16 bytes that stand before the row
   double inv_t, per;   // 1 / T, and what makes a difference of logits a power of 2
   float bins;          // bins of a logit's 1: 8 / T
+  Exp2 exp2;
   __device__ INLINE Row(const SampleArgs &a, int t) {
     p = static_cast<const typename L::elem *>(a.logits) + t * a.row;
     vocab = a.vocab;
@@ -140,15 +156,15 @@ struct Row {
     if (top == kPosInf || k <= kNegInf) return k == top && k > kNegInf ? 1. : 0.;
     const double y = ((double)of_key(k) - (double)of_key(top)) * per;
     int n;
-    const double s = exp2_parts(fmax(y, -45.), n);
+    const double s = exp2.parts(fmax(y, exp2.least), n);
     return y < -45. ? 0. : ldexp(s, n);
   }
   // the weight of v against the largest logit, which is finite, in units of 2^-43, to the nearest: 2^52 more, it is the
   // low bits of its fp64; 0 for -inf, NaN and whatever is below 2^-44
   __device__ INLINE u64 mass_of(float v, double top) const {
     int n;
-    const double s = exp2_parts(fmax(((double)v - top) * per, -45.), n);
-    const double m = fma(s, __builtin_bit_cast(double, (u64)(n + 43 + 1023) << 52), 0x1p52);
+    const double s = exp2.parts(fmax(((double)v - top) * per, exp2.least), n);
+    const double m = fma(s, __builtin_bit_cast(double, (u64)(n + 43 + 1023) << 52), exp2.unit);
     return __builtin_bit_cast(u64, m) & ((1ull << 52) - 1);
   }
   __device__ INLINE u64 mass(uint32_t k, uint32_t top) const {
@@ -281,17 +297,27 @@ __global__ __launch_bounds__(T) void weigh_kernel(SampleArgs a, int count) {
     }
     return;
   }
+  auto put = [&](auto by_mass) INLINE {
 #pragma unroll
-  for (int j = 0; j < WORDS; ++j)
+    for (int j = 0; j < WORDS; ++j) {
+      u64 m[N];
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const float d = top_bin - row.bin(v[j][e]);
-      const u64 m = masses ? row.mass_of(v[j][e], (double)top) : 0;
-      if (v[j][e] > -INFINITY && d < kBins) {
-        atomicAdd(&number[(int)d], 1u);
-        if (m) atomicAdd(&mass[(int)d], m);
+      for (int e = 0; e < N; ++e)
+        if (by_mass) m[e] = row.mass_of(v[j][e], (double)top);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float d = top_bin - row.bin(v[j][e]);
+        if (v[j][e] > -INFINITY && d < kBins) {
+          atomicAdd(&number[(int)d], 1u);
+          if (by_mass && m[e]) atomicAdd(&mass[(int)d], m[e]);
+        }
       }
     }
+  };
+  if (masses)
+    put(std::true_type{});
+  else
+    put(std::false_type{});
   __syncthreads();
   for (int i = threadIdx.x; i < kBins; i += T) {
     s.number[at * kBins + i] = number[i];
