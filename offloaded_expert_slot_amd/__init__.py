@@ -593,7 +593,7 @@ class _Torch:
         self.e4m3 = (torch.float8_e4m3fn, torch.uint8)
         self.e8m0 = (torch.float8_e8m0fnu, torch.uint8)
         self.u8, self.i32, self.f32, self.f64 = (torch.uint8,), (torch.int32,), (torch.float32,), (torch.float64,)
-        self.device = torch.cuda.current_device
+        self.device = torch._C._cuda_getDevice   # asked with tensors on a GPU in hand: the runtime is up
         self.stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -872,29 +872,30 @@ class Norm:
         self.weight, self.bias = weight, bias
         self.dim = None if some is None else some.shape[0]
         self.device = None if some is None else some.device
+        self._index = None if some is None else some.get_device()
         self._spec = NormSpec(_ptr(weight), _ptr(bias), NORM_KINDS.get(kind, kind), ELEM_F32 if f32 else ELEM_BF16, eps,
                               offset)
         self._at = ctypes.addressof(self._spec)
 
 
-def _spec(name, s, dim, dev):
+def _spec(name, s, dim, index):
     if s is None:
         return 0
-    if s.dim is not None and (s.dim != dim or s.device != dev):
-        _bad(f"{name}: {s.dim} weights on {s.device}, not {dim} on {dev}")
+    if s.dim is not None and (s.dim != dim or s._index != index):
+        _bad(f"{name}: {s.dim} weights on {s.device}, not {dim} on those of x")
     return s._at
 
 
-def _norm_rows(name, t, shape, dev):
-    """(address, row stride, head stride) of [n, dim] or [n, heads, dim] rows."""
+def _norm_rows(name, t, x, shape, index):
+    """(address, row stride, head stride) of [n, dim] or [n, heads, dim] rows beside x."""
+    st = t.stride()
+    if t.shape == shape and t.get_device() == index and st[-1] == 1:
+        return t.data_ptr(), st[0], st[1] if len(st) == 3 else 0
     if t.shape != shape:
         _bad(f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}")
-    if t.device != dev:
-        _bad(f"{name}: on {t.device}, not {dev}")
-    st = t.stride()
-    if st[-1] != 1:
-        _bad(f"{name}: the values of a row must be adjacent")
-    return t.data_ptr(), st[0], st[1] if len(st) == 3 else 0
+    if t.device != x.device:
+        _bad(f"{name}: on {t.device}, not {x.device}")
+    _bad(f"{name}: the values of a row must be adjacent")
 
 
 def norm(x, y=None, pre=None, post=None, gate=None, gate_act="plain", scale=1.0, res=None, res_out=None, stream=None):
@@ -904,14 +905,15 @@ def norm(x, y=None, pre=None, post=None, gate=None, gate_act="plain", scale=1.0,
     pre, post   Norm objects;  res, res_out like x, both bf16 or both float32 (res_out may be res)
     gate   bf16 that broadcasts to x's shape
     """
-    th, dev, shape = _th(), x.device, x.shape
+    th, shape, index = _th(), x.shape, x.get_device()
     if len(shape) not in (2, 3):
         _bad(f"x: [n, dim] or [n, heads, dim], not {tuple(shape)}")
     n, heads, dim = shape[0], shape[1] if len(shape) == 3 else 1, shape[-1]
     kind = x.dtype
-    if kind not in th.bf16 and kind != th.torch.float32:
+    x32 = kind == th.torch.float32
+    if not x32 and kind not in th.bf16:
         _bad(f"x: element type {kind}, not bfloat16 (or its bits as int16) or float32")
-    xp, xr, xh = _norm_rows("x", x, shape, dev)
+    xp, xr, xh = _norm_rows("x", x, x, shape, index)
     rp = rr = rh = op = orow = oh = yp = yr = yh = gp = gr = gh = gc = rkind = 0
     if res is not None or res_out is not None:
         some = res if res is not None else res_out
@@ -919,18 +921,18 @@ def norm(x, y=None, pre=None, post=None, gate=None, gate_act="plain", scale=1.0,
         if rkind == ELEM_BF16 and some.dtype not in th.bf16:
             _bad(f"res and res_out: element type {some.dtype}, not bfloat16 (or its bits as int16) or float32")
         if res is not None:
-            rp, rr, rh = _norm_rows("res", res, shape, dev)
+            rp, rr, rh = _norm_rows("res", res, x, shape, index)
         if res_out is not None:
             if res_out.dtype != some.dtype:
                 _bad(f"res_out: element type {res_out.dtype}, not {some.dtype}")
-            op, orow, oh = _norm_rows("res_out", res_out, shape, dev)
+            op, orow, oh = _norm_rows("res_out", res_out, x, shape, index)
     if y is not None:
         if y.dtype not in th.bf16:
             _bad(f"y: element type {y.dtype}, not bfloat16 (or its bits as int16)")
-        yp, yr, yh = _norm_rows("y", y, shape, dev)
+        yp, yr, yh = _norm_rows("y", y, x, shape, index)
     if gate is not None:
-        if gate.dtype not in th.bf16 or gate.device != dev:
-            _bad(f"gate: {gate.dtype} on {gate.device}, not bfloat16 (or its bits as int16) on {dev}")
+        if gate.dtype not in th.bf16 or gate.get_device() != index:
+            _bad(f"gate: {gate.dtype} on {gate.device}, not bfloat16 (or its bits as int16) on {x.device}")
         if gate.shape != shape:
             try:
                 gate = gate.expand(shape)
@@ -940,10 +942,10 @@ def norm(x, y=None, pre=None, post=None, gate=None, gate_act="plain", scale=1.0,
         gp, gr, gh, gc = gate.data_ptr(), gs[0], gs[1] if len(gs) == 3 else 0, gs[-1]
         if gc not in (0, 1):
             _bad("gate: the values of a row must be adjacent, or one")
-    args = _NORM_ARGS.pack(_spec("post", post, dim, dev), _spec("pre", pre, dim, dev), xp, gp, rp, op, yp, xr, xh, gr, gh,
-                           gc, rr, rh, orow, oh, yr, yh, n, heads, dim, ELEM_F32 if kind == th.torch.float32 else ELEM_BF16,
+    args = _NORM_ARGS.pack(_spec("post", post, dim, index), _spec("pre", pre, dim, index), xp, gp, rp, op, yp, xr, xh, gr, gh,
+                           gc, rr, rh, orow, oh, yr, yh, n, heads, dim, ELEM_F32 if x32 else ELEM_BF16,
                            rkind, GATE_ACTS.get(gate_act, gate_act), scale, 0)
-    _enqueue(dev, lib().oes_norm, args, stream=stream)
+    _enqueue(x.device, lib().oes_norm, args, stream=stream)
 
 
 def linear_bf16(x, w, y, bias=None, act="none", scale=1.0, res=None, stream=None):
@@ -953,7 +955,8 @@ def linear_bf16(x, w, y, bias=None, act="none", scale=1.0, res=None, stream=None
     y and res: bf16 or float32 alike; y may be res.
     """
     th, a = _th(), ACTS.get(act, act)
-    if x.dim() != 2 or w.dim() != 2 or y.dim() != 2:
+    xs, ws, ys = x.stride(), w.stride(), y.stride()
+    if len(xs) != 2 or len(ws) != 2 or len(ys) != 2:
         _bad("x [n, K], w [N, K] and y [n, N]")
     (n, K), (rows, wk), (yn, N), dev = x.shape, w.shape, y.shape, x.device
     if x.dtype not in th.bf16 or w.dtype not in th.bf16:
@@ -963,9 +966,9 @@ def linear_bf16(x, w, y, bias=None, act="none", scale=1.0, res=None, stream=None
         _bad(f"y: element type {y.dtype}, not bfloat16 (or its bits as int16) or float32")
     if wk != K or yn != n or rows != (2 * N if a == 4 else N):
         _bad(f"x {tuple(x.shape)}, w {tuple(w.shape)} and y {tuple(y.shape)} do not belong together (act {act})")
-    if w.device != dev or y.device != dev:
+    index = x.get_device()
+    if w.get_device() != index or y.get_device() != index:
         _bad(f"w on {w.device} and y on {y.device}, not {dev}")
-    xs, ws, ys = x.stride(), w.stride(), y.stride()
     if (xs[1] != 1 and K > 1) or (ws[1] != 1 and K > 1) or (ys[1] != 1 and N > 1):
         _bad("the values of a row of x, w or y must be adjacent")
     bp = None if bias is None else _typed("bias", bias, th.bf16, (rows,), dev)
