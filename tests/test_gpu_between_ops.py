@@ -456,6 +456,20 @@ def test_sample_infinite_logits_among_settings(V):
     _check_sample(logits, torch.rand(n, generator=g), t, k, p, m)
 
 
+@pytest.mark.parametrize("T", [1e-45, 1e-40, 1e-37, 1e30, 3e38])
+@pytest.mark.parametrize("V", [300, 20011, 60000])
+def test_sample_extreme_temperatures(T, V):
+    """Temperatures whose inverse passes fp32, and such that all weights are equal; logits of both signs and zeros."""
+    g = _gen(V)
+    settings = [(0, 1.0, 0.0), (9, 1.0, 0.0), (0, 0.9, 0.0), (40, 0.9, 0.0), (0, 1.0, 0.5), (V - 20, 0.5, 0.1)]
+    k, p, m = (list(v) for v in zip(*settings))
+    logits = _logits(g, len(settings), V, BF16).float()
+    logits[:, 5] = 0.0
+    logits[1::2] = -logits[1::2].abs()
+    logits[:, ::37] = -math.inf
+    _check_sample(logits, torch.rand(len(settings), generator=g), T, k, p, m)
+
+
 # ------------------------------------------------------------------ positions past 2^31
 def test_sample_rows_past_32_bits():
     n, V, stride = 5, 20011, 1 << 30
