@@ -694,7 +694,8 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
       if (!(rules.by_k && rules.by_p)) upto = min(upto, min_bin);   // p takes its share of all that k leaves
     }
     if (all_sum(sm, tid <= upto && tid < kBins ? sm.row_number[tid] : 0) <= kList) {
-      const int m = gather(start, place_of(key_from(min(upto, kBins - 1)), index_mask));
+      last = place_of(key_from(min(upto, kBins - 1)), index_mask);   // of the list: the searches' ranges end with it
+      const int m = gather(start, last);
       u64 total = all;
 #pragma unroll 1
       for (int by = rules.by_k ? BY_NUMBER : rules.by_p ? BY_WEIGHT : BY_INDEX;; ++by) {
