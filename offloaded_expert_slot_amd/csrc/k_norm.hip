@@ -137,6 +137,7 @@ __global__ __launch_bounds__(MANY ? (P == 1 ? 256 : 1024) : 256) void norm_kerne
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const int c = 8 * (me + i * step);
+      gate[i].w[0] = u32x4{0, 0, 0, 0};   // behind the row's end it opens to a number: v stays 0 there
       if (!in[i]) continue;
       x[i].load(a.x, x0 + c, xf);
       if (a.res) res[i].load(a.res, r0 + c, rf);
