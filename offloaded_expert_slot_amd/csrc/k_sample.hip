@@ -573,7 +573,7 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
     if (a.logprob) a.logprob[t] = (float)(z - log((double)total * 0x1p-43));
   };
   auto aim = [&](u64 total) INLINE {   // the running sum that the token's must reach
-    const float u = rules.u >= 0.f ? rules.u : 0.f;   // NaN too
+    const float u = rules.u > 0.f ? rules.u : 0.f;   // NaN and -0 too: `share` takes no sign
     return u < 1.f ? share(u, total, false) + 1 : total;
   };
   auto by_p = [&](u64 total) INLINE { return rules.p > 0.f ? max(share(rules.p, total, true), 1ull) : 1ull; };
