@@ -581,7 +581,8 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
     const u64 f = of_mine;
     const float d = f == kNowhere ? (float)kBins : fminf(bin_at(key_at(f)), (float)kBins);
     sm.slice_shift[tid] = (int)d;
-    sm.slice_share[tid] = d < kBins ? row.weight(key_at(f), top) : 0.;
+    // a slice whose largest entry counts as 0 has nothing to choose, whatever its entries add up to
+    sm.slice_share[tid] = d < kBins && row.mass(key_at(f), top) ? row.weight(key_at(f), top) : 0.;
   }
   if (tid < kBins) sm.row_mass[tid] = 0, sm.row_number[tid] = 0;
   if (tid <= kBins) sm.slice_mass[tid] = 0;
@@ -821,7 +822,8 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
   const int slice = uniform((int)min(sm.at, (u64)count - 1));
   const u64 before = uniform(sm.before);
   __syncthreads();
-  // within the slice; its entries' sum may miss the slice's by what was rounded: then the last one that weighs something
+  // Within the slice; its entries' sum may miss the slice's by what was rounded: then the last one that weighs something
+  // (there is one: the slice's largest is kept where any of its entries is), which is the one that u >= 1 asks for anyway.
   const int from = slice * s.size - row.off, to = min(from + s.size, a.vocab);
 #pragma unroll 4
   for (int i = tid; i < to - from; i += kThreads) {
@@ -830,7 +832,7 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SampleArgs a, int coun
     sm.mass[i] = k > kNegInf && place <= last && heavy(place) ? row.mass(k, top) : 0;
   }
   __syncthreads();
-  int id = from + locate(sm, to - from, before, target, [&](int i) INLINE { return sm.mass[i]; });
+  int id = from + locate(sm, to - from, before, rules.u >= 1.f ? kNowhere : target, [&](int i) INLINE { return sm.mass[i]; });
   if (uniform(sm.at) == kNowhere) {
     u64 behind = kNowhere;
     for (int i = tid; i < to - from; i += kThreads)
