@@ -670,7 +670,8 @@ oes_status oes_linear_bf16(const void *w, int64_t w_row, const void *bias, int32
  *   temperature, top_p, min_p  fp32 [n] device or NULL (1, 1, 0); top_k int32 [n] device or NULL (0)
  *   u           fp32 [n] device
  *   ids         int32 [n] device out, logprob fp32 [n] device out or NULL
- *   workspace   device, 16-byte aligned, >= oes_sample_workspace bytes; one call's at a time
+ *   workspace   device, 16-byte aligned, >= oes_sample_workspace bytes (which never fall as n or vocab
+ *               grows: that of the largest call serves every smaller one); one call's at a time
  * n in [0, 2^16], vocab in [1, 2^20] (OES_ERR_UNSUPPORTED beyond, and for n * vocab rounded
  * up to 8192s >= 2^36, from both calls); row >= vocab; pointers aligned to their elements.
  * Async. */

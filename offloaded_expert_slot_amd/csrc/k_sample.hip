@@ -215,8 +215,9 @@ __device__ INLINE inline Slices slices_of(const SampleArgs &a, int count, int si
 }
 // Slices of 4096, or of 8192 entries where there would be more than 2048 of them; a row may begin with up to 7 entries of
 // another one's.
+constexpr int kShortSlices = 2048;
 inline int slice_threads(int n, int vocab) {
-  return (int64_t)n * ((vocab + 7 + 256 * kPer - 1) / (256 * kPer)) > 2048 ? 512 : 256;
+  return (int64_t)n * ((vocab + 7 + 256 * kPer - 1) / (256 * kPer)) > kShortSlices ? 512 : 256;
 }
 inline int slice_count(int threads, int vocab) { return (vocab + 7 + threads * kPer - 1) / (threads * kPer); }
 
@@ -864,8 +865,10 @@ bool sample_fits(int n, int vocab) {
   return launch_fits((int64_t)n * slice_count(threads, vocab), threads) && launch_fits(n, kThreads);
 }
 
+// Beyond kShortSlices at least what they take, so that a call's workspace is enough for every smaller one.
 int64_t sample_workspace_bytes(int n, int vocab) {
-  const int64_t all = (int64_t)n * slice_count(slice_threads(n, vocab), vocab);
+  const int threads = slice_threads(n, vocab);
+  const int64_t count = (int64_t)n * slice_count(threads, vocab), all = threads == 256 ? count : std::max<int64_t>(count, kShortSlices);
   return (all * (16 + kBins * 12) + 15) / 16 * 16;
 }
 

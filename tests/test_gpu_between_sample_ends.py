@@ -1,9 +1,11 @@
-"""Sampling at the ends of its range: uniform numbers of 0, -0 and from 1 on."""
+"""Sampling at the ends of its range: uniform numbers of 0, -0 and from 1 on, entries that weigh nothing, and batches
+that shrink."""
 import math
 
 import pytest
 import torch
 
+import offloaded_expert_slot_amd as oes
 from tests.test_gpu_between_ops import BF16, F32, _check_sample, _gen, _logits, _sample
 
 pytestmark = pytest.mark.gpu
@@ -49,3 +51,17 @@ def test_entries_that_weigh_nothing(settings, first, dtype):
         # a smallest weight that everything which counts passes: weighed by another way, the same tokens
         again, lp2 = _sample(wide[:, first:], [u] * 4, t_, k, p, 1e-20)
         assert torch.equal(ids, again) and ((lp - lp2).abs() <= 2.0 ** -23 * lp.abs() + 1e-8).all()
+
+
+@pytest.mark.parametrize("V", [100003, 128256])
+def test_a_batch_that_shrinks_keeps_its_workspace(V):
+    """The workspace of the largest batch, made once, through batches around the change of the slices' length."""
+    g, most = _gen(V), 96
+    logits, u = _logits(g, most, V, BF16).to("cuda:0"), torch.rand(most, generator=g).to("cuda:0")
+    held = torch.empty(oes.sample_workspace_bytes(most, V), dtype=torch.uint8, device="cuda:0")
+    k, p = torch.full((most,), 64, dtype=torch.int32, device="cuda:0"), torch.full((most,), 0.95, device="cuda:0")
+    for n in (96, 82, 81, 80, 65, 64, 63, 1):
+        ids = torch.full((most,), -7, dtype=torch.int32, device="cuda:0")
+        oes.sample(logits[:n], u[:n], ids[:n], held, top_k=k[:n], top_p=p[:n])
+        want, _ = _sample(logits[:n], u[:n].cpu(), None, 64, 0.95)
+        assert torch.equal(ids[:n].cpu(), want) and (ids[n:] == -7).all(), n
