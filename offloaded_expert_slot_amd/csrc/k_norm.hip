@@ -86,16 +86,19 @@ __global__ __launch_bounds__(MANY ? (P == 1 ? 256 : 1024) : 256) void norm_kerne
         if (s.b) b[i].load(s.b, 8 * (me + i * step), gf);
       }
     if (s.layer) {
+      // Half the mean, which does not overflow for finite values; the mean and the differences end at the largest number
+      // then, so that their squares are infinite, not NaN times 0.
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum += v[i][e];
-      const float mean = row_sum(sum) * share;
+        for (int e = 0; e < 8; ++e) sum = fmaf(v[i][e], 0.5f * share, sum);
+      const float half = row_sum(sum), most = fabsf(half) <= __FLT_MAX__ ? __FLT_MAX__ : INFINITY;
+      const float mean = fminf(fmaxf(2.f * half, -most), most);
 #pragma unroll
       for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = in[i] ? v[i][e] - mean : 0.f;
+        for (int e = 0; e < 8; ++e) v[i][e] = in[i] ? fminf(fmaxf(v[i][e] - mean, -most), most) : 0.f;
     }
     float sq = 0.f;
 #pragma unroll
