@@ -613,8 +613,8 @@ typedef struct {
  *          act: OES_GATE_PLAIN, OES_GATE_SIGMOID, OES_GATE_SILU (v / (1 + exp(-v)))
  *   res    as x, of type res_elem; res_out may be res (then with the same strides)
  *   y      as x, bf16; y may be x if x is bf16 (then with the same strides)
- * Otherwise outputs must not overlap inputs or each other.  n >= 0, heads >= 1, n *
- * heads < 2^31, dim a multiple of 8 in [8, 16384]; rows of x, res, res_out and y
+ * Otherwise outputs must not overlap inputs or each other, and two rows of res_out or
+ * of y share no element.  n >= 0, heads >= 1, n * heads < 2^31, dim a multiple of 8 in [8, 16384]; rows of x, res, res_out and y
  * 16-byte aligned, of gate too where gate_col is 1 (else 2-byte); strides >= 0; scale
  * finite.  A row whose squares (layer: of its differences from the mean) add up to more
  * than 3.4e38 has a norm of 0, before b: NaN where it is infinite, and for a layer norm

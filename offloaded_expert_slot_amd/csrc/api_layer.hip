@@ -8,6 +8,7 @@
 #include <stdio.h>
 
 #include <algorithm>
+#include <utility>
 
 #include "kv_pages.h"
 #include "oes_internal.h"
@@ -378,6 +379,19 @@ oes_status check_spec(const char *what, const oes_norm_spec *s, NormSpec &out) {
   return OES_OK;
 }
 
+// Whether two of n x heads rows of dim elements, at t * row + h * head, share an element
+bool rows_overlap(int64_t n, int64_t row, int64_t heads, int64_t head, int64_t dim) {
+  if ((n > 1 && row < dim) || (heads > 1 && head < dim)) return true;
+  if (n == 1 || heads == 1) return false;
+  if (n > heads) std::swap(n, heads), std::swap(row, head);
+  if (head >= dim && row - dim >= head && (row - dim) / head >= heads - 1) return false;   // one after the other
+  for (int64_t t = 1; t < n; ++t) {   // fewer than 2^16; the heads next to a row t further on
+    const __int128 at = (__int128)t * row, h = at / head, past = at - h * head;
+    if ((h < heads && past < dim) || (h + 1 < heads && head - past < dim)) return true;
+  }
+  return false;
+}
+
 // [n, heads, dim] rows of elements of `size` bytes; the stride over a single row or head counts as 0
 oes_status check_norm_rows(const char *what, const void *p, int64_t &row, int64_t &head, const oes_norm_args *a, int size, bool written) {
   const int64_t per = 16 / size;
@@ -385,7 +399,7 @@ oes_status check_norm_rows(const char *what, const void *p, int64_t &row, int64_
   if (a->heads == 1) head = 0;
   if (!aligned(p, 16) || row < 0 || head < 0 || row % per || head % per)
     return fail(OES_ERR_ARG, "%s: rows must be 16-byte aligned, strides >= 0", what);
-  if (written && ((a->n > 1 && row < a->dim) || (a->heads > 1 && head < a->dim)))
+  if (written && rows_overlap(a->n, row, a->heads, head, a->dim))
     return fail(OES_ERR_ARG, "%s: rows that are written must not overlap", what);
   return OES_OK;
 }
