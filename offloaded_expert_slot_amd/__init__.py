@@ -31,6 +31,7 @@ and between the blocks:
     sample(logits, u, ids, workspace, temperature, top_k, top_p, min_p, logprob)
 """
 import ctypes
+import math
 import os
 import re
 import struct
@@ -854,6 +855,30 @@ def kv_evict(kv, acc, budget, kept, new_len, workspace, first=0, last=0, stream=
 
 
 # ---------------------------------------------------------------- between the blocks
+def _named(what, value, names):
+    """The C value of one of `names`, given by its name or itself."""
+    try:
+        return names[value]
+    except (KeyError, TypeError):   # TypeError: not hashable
+        pass
+    if isinstance(value, int) and value in names.values():
+        return int(value)
+    _bad(f"{what}: {value!r}, not {', '.join(names)}")
+
+
+def _number(what, value):
+    """A finite float of float32's range."""
+    if type(value) is float and value == 1.0:
+        return value
+    try:
+        v = math.nan if isinstance(value, str) else float(value)
+    except (TypeError, ValueError, OverflowError, RuntimeError):   # RuntimeError: a tensor of several values
+        v = math.nan
+    if not abs(v) < 3.4028235677973366e38:   # what rounds to float32's largest number, or less
+        _bad(f"{what}: {value!r} is not a finite number of float32")
+    return v
+
+
 class Norm:
     """A norm's weights and kind (oes_norm_spec): gain = offset + weight, or 1 without a weight; then + bias.
 
@@ -873,8 +898,8 @@ class Norm:
         self.dim = None if some is None else some.shape[0]
         self.device = None if some is None else some.device
         self._index = None if some is None else some.get_device()
-        self._spec = NormSpec(_ptr(weight), _ptr(bias), NORM_KINDS.get(kind, kind), ELEM_F32 if f32 else ELEM_BF16, eps,
-                              offset)
+        self._spec = NormSpec(_ptr(weight), _ptr(bias), _named("kind", kind, NORM_KINDS), ELEM_F32 if f32 else ELEM_BF16,
+                              _number("eps", eps), _number("offset", offset))
         self._at = ctypes.addressof(self._spec)
 
 
@@ -942,9 +967,13 @@ def norm(x, y=None, pre=None, post=None, gate=None, gate_act="plain", scale=1.0,
         gp, gr, gh, gc = gate.data_ptr(), gs[0], gs[1] if len(gs) == 3 else 0, gs[-1]
         if gc not in (0, 1):
             _bad("gate: the values of a row must be adjacent, or one")
-    args = _NORM_ARGS.pack(_spec("post", post, dim, index), _spec("pre", pre, dim, index), xp, gp, rp, op, yp, xr, xh, gr, gh,
-                           gc, rr, rh, orow, oh, yr, yh, n, heads, dim, ELEM_F32 if x32 else ELEM_BF16,
-                           rkind, GATE_ACTS.get(gate_act, gate_act), scale, 0)
+    act, scale = _named("gate_act", gate_act, GATE_ACTS), _number("scale", scale)
+    try:
+        args = _NORM_ARGS.pack(_spec("post", post, dim, index), _spec("pre", pre, dim, index), xp, gp, rp, op, yp, xr, xh, gr,
+                               gh, gc, rr, rh, orow, oh, yr, yh, n, heads, dim, ELEM_F32 if x32 else ELEM_BF16, rkind, act,
+                               scale, 0)
+    except struct.error:
+        _bad(f"x: {tuple(shape)} is too large")
     _enqueue(x.device, lib().oes_norm, args, stream=stream)
 
 
@@ -954,7 +983,7 @@ def linear_bf16(x, w, y, bias=None, act="none", scale=1.0, res=None, stream=None
     act: none, sigmoid, silu, gelu (its tanh form), or swiglu (w and bias have 2 N rows: gate, then up).
     y and res: bf16 or float32 alike; y may be res.
     """
-    th, a = _th(), ACTS.get(act, act)
+    th, a, scale = _th(), _named("act", act, ACTS), _number("scale", scale)
     xs, ws, ys = x.stride(), w.stride(), y.stride()
     if len(xs) != 2 or len(ws) != 2 or len(ys) != 2:
         _bad("x [n, K], w [N, K] and y [n, N]")
