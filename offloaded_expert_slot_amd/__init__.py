@@ -855,12 +855,13 @@ def kv_evict(kv, acc, budget, kept, new_len, workspace, first=0, last=0, stream=
 
 
 # ---------------------------------------------------------------- between the blocks
+_F32_END = 3.4028235677973366e38   # what is below rounds to a number of float32
+
+
 def _named(what, value, names):
     """The C value of one of `names`, given by its name or itself."""
-    try:
+    if isinstance(value, str) and value in names:
         return names[value]
-    except (KeyError, TypeError):   # TypeError: not hashable
-        pass
     if isinstance(value, int) and value in names.values():
         return int(value)
     _bad(f"{what}: {value!r}, not {', '.join(names)}")
@@ -868,15 +869,20 @@ def _named(what, value, names):
 
 def _number(what, value):
     """A finite float of float32's range."""
-    if type(value) is float and value == 1.0:
+    if type(value) is float and -_F32_END < value < _F32_END:
         return value
     try:
         v = math.nan if isinstance(value, str) else float(value)
     except (TypeError, ValueError, OverflowError, RuntimeError):   # RuntimeError: a tensor of several values
         v = math.nan
-    if not abs(v) < 3.4028235677973366e38:   # what rounds to float32's largest number, or less
+    if not abs(v) < _F32_END:
         _bad(f"{what}: {value!r} is not a finite number of float32")
     return v
+
+
+def _too_large(what, *sizes):
+    """Of sizes that the library's int32 arguments would cut to their low bits."""
+    raise OesError(ERR_UNSUPPORTED, f"OES_ERR_UNSUPPORTED: {what}: {' x '.join(map(str, sizes))} is too large")
 
 
 class Norm:
@@ -967,7 +973,12 @@ def norm(x, y=None, pre=None, post=None, gate=None, gate_act="plain", scale=1.0,
         gp, gr, gh, gc = gate.data_ptr(), gs[0], gs[1] if len(gs) == 3 else 0, gs[-1]
         if gc not in (0, 1):
             _bad("gate: the values of a row must be adjacent, or one")
-    act, scale = _named("gate_act", gate_act, GATE_ACTS), _number("scale", scale)
+    try:
+        act = GATE_ACTS[gate_act]
+    except (KeyError, TypeError):
+        act = _named("gate_act", gate_act, GATE_ACTS)
+    if type(scale) is not float or scale != 1.0:
+        scale = _number("scale", scale)
     try:
         args = _NORM_ARGS.pack(_spec("post", post, dim, index), _spec("pre", pre, dim, index), xp, gp, rp, op, yp, xr, xh, gr,
                                gh, gc, rr, rh, orow, oh, yr, yh, n, heads, dim, ELEM_F32 if x32 else ELEM_BF16, rkind, act,
@@ -983,11 +994,19 @@ def linear_bf16(x, w, y, bias=None, act="none", scale=1.0, res=None, stream=None
     act: none, sigmoid, silu, gelu (its tanh form), or swiglu (w and bias have 2 N rows: gate, then up).
     y and res: bf16 or float32 alike; y may be res.
     """
-    th, a, scale = _th(), _named("act", act, ACTS), _number("scale", scale)
+    th = _th()
+    try:
+        a = ACTS[act]
+    except (KeyError, TypeError):
+        a = _named("act", act, ACTS)
+    if type(scale) is not float or scale != 1.0:
+        scale = _number("scale", scale)
     xs, ws, ys = x.stride(), w.stride(), y.stride()
     if len(xs) != 2 or len(ws) != 2 or len(ys) != 2:
         _bad("x [n, K], w [N, K] and y [n, N]")
     (n, K), (rows, wk), (yn, N), dev = x.shape, w.shape, y.shape, x.device
+    if rows > 0x7fffffff or n > 0x7fffffff or K > 0x7fffffff:
+        _too_large("n x N x K", n, rows, K)
     if x.dtype not in th.bf16 or w.dtype not in th.bf16:
         _bad(f"x and w: element types {x.dtype} and {w.dtype}, not bfloat16 (or its bits as int16)")
     f32 = y.dtype == th.torch.float32
@@ -1014,6 +1033,8 @@ def linear_bf16(x, w, y, bias=None, act="none", scale=1.0, res=None, stream=None
 
 
 def sample_workspace_bytes(n, vocab):
+    if not (abs(n) <= 0x7fffffff and abs(vocab) <= 0x7fffffff):
+        _too_large("n x vocab", n, vocab)
     b = _I64()
     _check(lib().oes_sample_workspace(n, vocab, ctypes.byref(b)))
     return b.value
@@ -1028,6 +1049,8 @@ def sample(logits, u, ids, workspace, temperature=None, top_k=None, top_p=None, 
     if logits.dim() != 2:
         _bad(f"logits: [n, vocab], not {tuple(logits.shape)}")
     n, vocab = logits.shape
+    if n > 0x7fffffff or vocab > 0x7fffffff:
+        _too_large("n x vocab", n, vocab)
     f32 = logits.dtype == th.torch.float32
     if not f32 and logits.dtype not in th.bf16:
         _bad(f"logits: element type {logits.dtype}, not bfloat16 (or its bits as int16) or float32")

@@ -7,10 +7,10 @@ import torch
 import offloaded_expert_slot_amd as oes
 
 
-def refused(call, *words):
+def refused(call, *words, status=oes.ERR_ARG):
     with pytest.raises(oes.OesError) as e:
         call()
-    assert e.value.status == oes.ERR_ARG
+    assert e.value.status == status
     assert all(w in str(e.value) for w in words), str(e.value)
 
 
@@ -52,3 +52,27 @@ def test_values_that_stay():
         refused(lambda: oes.linear_bf16(x, bf(10, 64), bf(3, 10), act=a, scale=torch.tensor(0.5)), "not on a GPU")
     refused(lambda: oes.linear_bf16(x, bf(20, 64), bf(3, 10), act=4), "not on a GPU")
     assert oes.Norm(bf(64), kind=1)._spec.kind == 1 and oes.Norm(bf(64), eps=0)._spec.eps == 0
+
+
+def test_sizes_beyond_the_c_interface():
+    """Sizes that an int32 does not hold are refused as such, not cut to their low bits (rows of stride 0 take no memory)."""
+    def rows(n, cols, kind=torch.bfloat16):
+        return torch.zeros(1, cols, dtype=kind).expand(n, cols)
+
+    def wide(n, cols, kind=torch.bfloat16):
+        return torch.zeros(1, 1, dtype=kind).expand(n, cols)
+
+    def beyond(call):
+        refused(call, "too large", status=oes.ERR_UNSUPPORTED)
+
+    for n in (1 << 31, (1 << 32) + 1):
+        refused(lambda: oes.norm(rows(n, 64), rows(n, 64)), "too large")
+        beyond(lambda: oes.linear_bf16(rows(n, 64), bf(10, 64), rows(n, 10)))
+        beyond(lambda: oes.linear_bf16(bf(3, 64), rows(n, 64), wide(3, n)))
+        beyond(lambda: oes.linear_bf16(wide(3, n), wide(10, n), bf(3, 10)))
+        beyond(lambda: oes.sample(rows(n, 50), wide(1, n, torch.float32)[0], wide(1, n, torch.int32)[0], bf(0)))
+        beyond(lambda: oes.sample(wide(3, n), torch.zeros(3), torch.zeros(3, dtype=torch.int32), bf(0)))
+        beyond(lambda: oes.sample_workspace_bytes(n, 100))
+        beyond(lambda: oes.sample_workspace_bytes(3, n))
+    beyond(lambda: oes.sample_workspace_bytes(-(1 << 32) + 3, 100))
+    beyond(lambda: oes.linear_bf16(bf(1, 64), rows(1 << 32, 64), wide(1, 1 << 31), act="swiglu"))
