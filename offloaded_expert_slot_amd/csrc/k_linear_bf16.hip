@@ -431,17 +431,17 @@ __global__ __launch_bounds__(256) void row_kernel(DenseArgs a) {
 }
 
 template <typename P>
-Tiles tiles_of(const DenseArgs &a, int band = 4) {
+Tiles tiles_of(const DenseArgs &a) {
   Tiles t;
   t.tiles_n = (int)(((a.act == OES_ACT_SWIGLU ? 2ll : 1ll) * a.N + P::BN - 1) / P::BN);
   t.tiles_m = (a.n + P::BM - 1) / P::BM;
-  t.band = std::min(band, t.tiles_m);
+  t.band = std::min(4, t.tiles_m);
   return t;
 }
 
 template <typename P>
-hipError_t launch_shape(const DenseArgs &a, hipStream_t s, int band = 4) {
-  const Tiles t = tiles_of<P>(a, band);
+hipError_t launch_shape(const DenseArgs &a, hipStream_t s) {
+  const Tiles t = tiles_of<P>(a);
   const dim3 g((uint32_t)t.tiles_n * (uint32_t)t.tiles_m), b(P::threads);
   const bool swiglu = a.act == OES_ACT_SWIGLU;
   if constexpr (P::BM <= 64) {
@@ -499,7 +499,6 @@ auto with_shape(const DenseArgs &a, F f) {
 
 }  // namespace
 
-#ifndef DENSE_TUNE
 bool linear_bf16_fits(const DenseArgs &a) {
   if (a.n == 1) return true;   // 2^21 workgroups at most
   return with_shape(a, [&](auto p) {
@@ -519,6 +518,5 @@ hipError_t launch_linear_bf16(const DenseArgs &a, hipStream_t s) {
   }
   return with_shape(a, [&](auto p) { return launch_shape<decltype(p)>(a, s); });
 }
-#endif
 
 }  // namespace oes
