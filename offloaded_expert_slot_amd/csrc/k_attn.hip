@@ -69,22 +69,9 @@ __device__ inline int swizzle(int row) {
   return DP == 64 ? ((row >> 1) & 1) << 2 | ((row >> 2) & 3) : (row & 3) << 2 | ((row >> 2) & 3);
 }
 
-// 16 bytes per lane from global memory to LDS base + 16 * lane; counted by vmcnt only
-__device__ inline void load_to_lds(const void *src, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");
-}
-// the same with a wave-uniform base and a 32-bit offset per lane
-__device__ inline void load_to_lds(const void *base, uint32_t off, uint32_t lds) {
-  const uint64_t b = (uint64_t)base;
-  const uint64_t u = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(b >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)b);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(u) : "memory");
-}
 template <int N>
 __device__ inline void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-__device__ inline uint32_t lds_addr(const void *p) {
-  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
 }
 // the value of the lane's other half (lane ^ 32) joined with its own
 __device__ inline float max_halves(float v) {

@@ -32,15 +32,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __attribute__((aligned(16))) const uint32_t nothing[4] = {0, 0, 0, 0};
 
-// 16 bytes per lane from src + OFF to LDS base + 16 * lane; counted by vmcnt only.  (The instruction's offset counts
-// for both addresses.)  ONCE: what no other workgroup will read.
-template <int OFF, bool ONCE = false>
-__device__ inline void load_to_lds(const void *src, uint32_t lds) {
-  if (ONCE)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2 nt" ::"s"(lds - OFF), "v"(src), "n"(OFF) : "memory");
-  else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2" ::"s"(lds - OFF), "v"(src), "n"(OFF) : "memory");
-}
 // Until all but N loads have arrived and the wave's reads of LDS are done; then, BARRIER, until every wave has come here.
 template <int N, bool BARRIER>
 __device__ inline void wait_loads() {
@@ -49,12 +40,6 @@ __device__ inline void wait_loads() {
   else
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
-__device__ inline uint32_t lds_addr(const void *p) {
-  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
-}
-
-// 1 / (1 + exp(-v)); exp2 of a rounded argument is off by |v| half steps
-__device__ inline float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * v)); }
 __device__ inline float activate(int act, float v) {
   switch (act) {
     case OES_ACT_SIGMOID: return sigmoid(v);

@@ -34,10 +34,9 @@ __device__ inline u32x4 packed(const float (&v)[8]) {
   return u32x4{f2bf16_pair(v[0], v[1]), f2bf16_pair(v[2], v[3]), f2bf16_pair(v[4], v[5]), f2bf16_pair(v[6], v[7])};
 }
 
-// act(g): 1 / (1 + exp(-g)) by exp2, whose rounded argument is off by |g| half steps
-__device__ inline float opened(int act, float g) {
+__device__ inline float opened(int act, float g) {   // act(g)
   if (act == OES_GATE_PLAIN) return g;
-  const float p = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * g));
+  const float p = sigmoid(g);
   return act == OES_GATE_SIGMOID ? p : g * p;
 }
 

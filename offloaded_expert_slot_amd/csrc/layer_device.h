@@ -44,6 +44,28 @@ __device__ inline f32x2 e4m3_pair(uint32_t w) {
   return __builtin_amdgcn_cvt_pk_f32_fp8(w, HI);
 }
 
+// 1 / (1 + exp(-v)); exp2 of a rounded argument is off by |v| half steps
+__device__ inline float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * v)); }
+
+// 16 bytes per lane from src + OFF to LDS base + 16 * lane; counted by vmcnt only.  (The instruction's offset counts
+// for both addresses.)  ONCE: what no other workgroup will read.
+template <int OFF = 0, bool ONCE = false>
+__device__ inline void load_to_lds(const void *src, uint32_t lds) {
+  if (ONCE)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2 nt" ::"s"(lds - OFF), "v"(src), "n"(OFF) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2" ::"s"(lds - OFF), "v"(src), "n"(OFF) : "memory");
+}
+// the same with a wave-uniform base and a 32-bit offset per lane
+__device__ inline void load_to_lds(const void *base, uint32_t off, uint32_t lds) {
+  const uint64_t b = (uint64_t)base;
+  const uint64_t u = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(b >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)b);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(u) : "memory");
+}
+__device__ inline uint32_t lds_addr(const void *p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
+}
+
 __device__ inline void raise_status(const oes_kv &kv) {
   if (kv.status) *kv.status = OES_ERR_ARG;
 }
