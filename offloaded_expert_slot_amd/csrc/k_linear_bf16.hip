@@ -429,7 +429,8 @@ hipError_t launch_shape(const DenseArgs &a, hipStream_t s) {
   const Tiles t = tiles_of<P>(a);
   const dim3 g((uint32_t)t.tiles_n * (uint32_t)t.tiles_m), b(P::threads);
   const bool swiglu = a.act == OES_ACT_SWIGLU;
-  if constexpr (P::BM <= 64) {
+  // (32 x 16 is not taken for one tile of tokens: 16 x 32 makes as many workgroups then, and theirs cost less.)
+  if constexpr (P::BM <= 64 && !(P::BM == 32 && P::BN == 16)) {
     if (t.tiles_m == 1) {
       if (swiglu)
         hipLaunchKernelGGL((dense_kernel<P, true, true>), g, b, P::lds, s, a, t);
