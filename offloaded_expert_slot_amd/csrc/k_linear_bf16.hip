@@ -447,8 +447,10 @@ hipError_t launch_shape(const DenseArgs &a, hipStream_t s) {
 }
 
 // The shapes, and what a round of 256 workgroups of each costs, in us at K = 7168 (4096 rows of W, or as many tokens as
-// make 224 - 256 tiles; the smallest read W from memory).  A call takes the shape whose rounds cost least: over 136 sizes
-// (512 ... 20000 rows, K 2048 ... 7168, 1 ... 4096 tokens) that is within a few per cent of the fastest of 28 shapes.
+// make 224 - 256 tiles; the smallest read W from memory).  A call takes the shape whose rounds cost least.  Over 146 sizes
+// (512 ... 20000 rows, K 2048 ... 7168, 4 ... 4096 tokens) that takes 0.9 % more than the fastest of fifteen shapes, in the
+// geometric mean; 5 % more at nine of them, and the most where shapes of other proportions would need fewer rounds: 384 x
+// 20000 x 4096 84 us (128 x 256: 71), 192 x 7168 x 7168 54 (128 x 64: 46), 192 x 2 * 2880 x 2880 23.5 (128 x 64: 20.5).
 template <typename F>
 auto with_shape(const DenseArgs &a, F f) {
   const int cost[] = {130, 145, 155, 190, 245, 360, 515, 690, 1040, 1750};
