@@ -8,7 +8,11 @@
 //           entries stand up to there, they are gathered in LDS and everything is decided among them;
 //           otherwise the entries of that bin alone are, and the token is looked for in the slice that the bins' sums
 //           name
-// A row is read twice at most (and more often only if one bin holds more than kList entries), nothing is sorted.
+// Nothing is sorted.  A row is read twice where at most kList entries stand up to the last one's bin (and with no rule
+// but u, once and one slice of it again).  Where more do, further passes read it: one for the list of each border, k's and then
+// p's, and one before for every 2^-9 of a bin that holds more than kList entries; one for the weight of what k left; one for the last
+// bin's entries where two rules meet in it.  Of one row of 100003 that takes 148 us for k = 30000 and p = 0.7 of logits spread by
+// 2, 184 us for p = 0.9 of logits spread by 0.05, and 310 us where all are equal.
 // Weights are formed in fp64 and are integers of 2^-43 of the largest weight of the slice (or row), so that sums by
 // atomics do not depend on their order.  fp32 would not do: over 100000 entries its sums are off by more than the
 // share of many tokens.
