@@ -616,9 +616,9 @@ typedef struct {
  * Otherwise outputs must not overlap inputs or each other, and two rows of res_out or
  * of y share no element.  n >= 0, heads >= 1, n * heads < 2^31, dim a multiple of 8 in [8, 16384]; rows of x, res, res_out and y
  * 16-byte aligned, of gate too where gate_col is 1 (else 2-byte); strides >= 0; scale
- * finite.  A row whose squares (layer: of its differences from the mean) add up to more
- * than 3.4e38 has a norm of 0, before b: NaN where it is infinite, and for a layer norm
- * with an infinity in every place; NaN gives NaN.  Async. */
+ * finite.  A row whose squares (layer: of half its differences from the mean) add up to
+ * more than 3.4e38 has a norm of 0, before b: NaN where it is infinite, and for a layer
+ * norm with an infinity in every place; NaN gives NaN.  Async. */
 enum { OES_GATE_PLAIN = 0, OES_GATE_SIGMOID = 1, OES_GATE_SILU = 2 };
 typedef struct {
   const oes_norm_spec *post, *pre;

@@ -375,7 +375,8 @@ oes_status check_spec(const char *what, const oes_norm_spec *s, NormSpec &out) {
   if (s->elem != OES_ELEM_BF16 && s->elem != OES_ELEM_F32) return fail(OES_ERR_UNSUPPORTED, "%s: w and b are bf16 or fp32", what);
   if (!(s->eps >= 0) || !isfinite(s->eps) || !isfinite(s->offset)) return fail(OES_ERR_ARG, "%s: eps must be finite and >= 0, offset finite", what);
   if (!aligned(s->w, 16) || !aligned(s->b, 16)) return fail(OES_ERR_ARG, "%s: w and b must be 16-byte aligned", what);
-  out = NormSpec{s->w, s->b, 1, s->kind == OES_NORM_LAYER, s->elem == OES_ELEM_F32, s->eps, s->offset};
+  const bool layer = s->kind == OES_NORM_LAYER;
+  out = NormSpec{s->w, s->b, 1, layer, s->elem == OES_ELEM_F32, layer ? 0.25f * s->eps : s->eps, s->offset};
   return OES_OK;
 }
 

@@ -85,19 +85,19 @@ __global__ __launch_bounds__(MANY ? (P == 1 ? 256 : 1024) : 256) void norm_kerne
         if (s.b) b[i].load(s.b, 8 * (me + i * step), gf);
       }
     if (s.layer) {
-      // Half the mean, which does not overflow for finite values; the mean and the differences end at the largest number
-      // then, so that their squares are infinite, not NaN times 0.
+      // Half the mean and half the differences, neither of which overflows for finite values (an infinite difference times
+      // an inverse of 0 would be NaN): v - m over the root of its mean square and eps is (v / 2 - m / 2) over the root of
+      // its own and eps / 4, which s.eps is here.
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < P; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum = fmaf(v[i][e], 0.5f * share, sum);
-      const float half = row_sum(sum), most = fabsf(half) <= __FLT_MAX__ ? __FLT_MAX__ : INFINITY;
-      const float mean = fminf(fmaxf(2.f * half, -most), most);
+      const float half = row_sum(sum);
 #pragma unroll
       for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = in[i] ? fminf(fmaxf(v[i][e] - mean, -most), most) : 0.f;
+        for (int e = 0; e < 8; ++e) v[i][e] = in[i] ? fmaf(v[i][e], 0.5f, -half) : 0.f;
     }
     float sq = 0.f;
 #pragma unroll
@@ -139,12 +139,15 @@ __global__ __launch_bounds__(MANY ? (P == 1 ? 256 : 1024) : 256) void norm_kerne
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const int c = 8 * (me + i * step);
-      gate[i].w[0] = u32x4{0, 0, 0, 0};   // behind the row's end it opens to a number: v stays 0 there
+      if (MANY) gate[i].w[0] = u32x4{0, 0, 0, 0};
       if (!in[i]) continue;
       x[i].load(a.x, x0 + c, xf);
       if (a.res) res[i].load(a.res, r0 + c, rf);
       if (a.gate && a.gate_col) gate[i].load(a.gate, g0 + c, false);
     }
+    // Behind the row's end a gate must open to a number, so that v stays 0 there: registers of 0, or 0 where it is used.  us,
+    // the first and the second way: 8192 x 32 heads of 128 without a gate 31.9 and 29.4; 4096 x 2880 with one 28.7 and 29.1;
+    // 8192 x 4096 with fp32 gains and no gate 70.3 and 78.9.
     const uint32_t one = a.gate && !a.gate_col ? static_cast<const uint16_t *>(a.gate)[g0] : 0u;
 #pragma unroll
     for (int i = 0; i < P; ++i)
@@ -155,7 +158,7 @@ __global__ __launch_bounds__(MANY ? (P == 1 ? 256 : 1024) : 256) void norm_kerne
 #pragma unroll
       for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] *= a.scale * opened(a.gate_act, gate[i].value(e, false));
+        for (int e = 0; e < 8; ++e) v[i][e] *= a.scale * opened(a.gate_act, MANY || in[i] ? gate[i].value(e, false) : 0.f);
     } else {
       const float s = a.gate ? a.scale * opened(a.gate_act, bf16f(one)) : a.scale;
 #pragma unroll

@@ -192,7 +192,7 @@ hipError_t launch_evict(const EvictArgs &a, hipStream_t s);
 struct NormSpec {         // a norm, by value
   const void *w, *b;
   int32_t on, layer, f32;  // on: 0 = the identity; f32: w and b are fp32
-  float eps, offset;
+  float eps, offset;       // eps: a quarter of it for a layer norm, which goes by half its differences
 };
 struct NormArgs {
   NormSpec post, pre;
