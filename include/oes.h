@@ -641,7 +641,8 @@ oes_status oes_norm(const oes_norm_args *args, void *stream);
  *   OES_ACT_GELU     v / 2 * (1 + tanh(sqrt(2 / pi) * (v + 0.044715 v^3)))
  *   OES_ACT_SWIGLU   silu(g) * u: W and bias have 2 N rows, [0, N) for g and [N, 2 N) for u,
  *                    as in the gate_up banks
- * Sums and the epilogue are fp32, y is rounded to nearest even once.  Rows of x reach
+ * Sums and the epilogue are fp32, y is rounded to nearest even once; 1 / (1 + exp(-v))
+ * below 2^-126 (v < -87.3) counts as 0, here and in gates.  Rows of x reach
  * their own row of y only, rows of W their own column.  K a multiple of 8 in [8,
  * 2^20], N in [1, 2^22], n in [0, 2^19]; x, W and their rows 16-byte aligned, bias
  * 2-byte, y and res aligned to their elements; x_row, w_row >= K, y_row, res_row >=
