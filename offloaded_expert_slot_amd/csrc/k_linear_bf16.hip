@@ -6,11 +6,12 @@
 // ahead.  A group of one wave waits for its own loads alone; others meet at a barrier a step.  The groups' sums
 // are joined in LDS, in order.
 //
-// Few tokens are bound by reading W: 16 tokens of 100003 x 4096 126 us, 6.5 TB/s; 24 tokens of SwiGLU 2 x 2048 x 7168 11
-// us (5.3 TB/s).  Small tiles with K cut over a workgroup's waves then keep all CUs reading.  Many are bound by the matrix
-// units: 4096 tokens of 7168 x 7168 366 us, 1.15 PFLOP/s, by tiles of 256 x 256, each of whose operand values in LDS feeds 8
-// or 4 products a wave.  Between them (333 tokens of 2880 x 2880 17.5 us) there are as few tiles as CUs, and the time is that of
-// one tile's 45 steps.
+// Few tokens are bound by reading W: 16 tokens of 100003 x 4096 128 us, 6.5 TB/s; 24 tokens of SwiGLU 2 x 2048 x 7168 16.4
+// us (3.6 TB/s; 11.4 where W is still in the memory-side cache).  Small tiles with K cut over a workgroup's waves then keep
+// all CUs reading.  Many are bound by the matrix units: 4096 tokens of 7168 x 7168 364 us in a graph, 1.15 PFLOP/s (368 - 386 by
+// calls and traces), by tiles of 256 x 256, each of whose operand values in LDS feeds 8 or 4 products a wave.  Between them
+// (333 tokens of 2880 x 2880 18.4 us, 23.2 from memory) there are fewer tiles than CUs, and the time is that of one tile's 45
+// steps.
 //
 // In LDS a row of a step is 8 pieces of 16 bytes, piece c at c ^ f(row), f such that the 16 rows that a read takes
 // spread over all banks.  Where a wave has 32 rows of W, block i = 2 p + b takes rows 32 p + 8 (r / 4) + 4 b + r % 4, so

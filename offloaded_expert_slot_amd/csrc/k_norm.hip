@@ -1,7 +1,7 @@
 // Norms between the blocks: r = res + scale * act(gate) * post(x), y = pre(r).
 //
-// Bound by memory (8192 x 4096 with a bf16 residual 49.9 us, 5.4 TB/s; 3001 x 7168 with both norms, a gate and an fp32
-// residual 54.7 us, 4.7 TB/s; one row of 2048 3.1 us, latency): a row is read once into registers, 8 values a piece
+// Bound by memory (8192 x 4096 with a bf16 residual 50.5 us, 5.3 TB/s; 3001 x 7168 with both norms, a gate and an fp32
+// residual 55.5 us, 4.7 TB/s; one row of 2048 2.7 us in a graph, latency): a row is read once into registers, 8 values a piece
 // of 16 (fp32: 32) bytes, and stays there through both norms.  Up to 64 lanes of a wave have a row, whose sums meet by lane
 // exchanges, or a workgroup of just as many waves as it takes, whose sums meet in LDS (in order, so that a row's result
 // depends on nothing else).  Squares are taken of differences from the mean, which a sum of squares less the

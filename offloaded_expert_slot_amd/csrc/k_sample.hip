@@ -17,9 +17,9 @@
 // atomics do not depend on their order.  fp32 would not do: over 100000 entries its sums are off by more than the
 // share of many tokens.
 //
-// Measured, both launches replayed in a graph: one row of 100003 fp32 by k = 64 and p = 0.95 28.6 us, 4.0 of them weigh and
+// Measured, both launches replayed in a graph: one row of 100003 fp32 by k = 64 and p = 0.95 28.5 us, 4.0 of them weigh and
 // about 11 the gather (latency: what a workgroup's few instructions and trips to memory take one after the other); 48
-// rows of 100003 bf16, settings mixed, 56 us; 160 rows of 200003 fp32 by p 106 us: weigh 46 (2.8 TB/s; the weights'
+// rows of 100003 bf16, settings mixed, 56 us; 160 rows of 200003 fp32 by p 107 us: weigh 46 (2.8 TB/s; the weights'
 // fp64 and the bins' atomics, vector units busy for 0.8 of it), the gather about 30, the searches about 20.
 
 #include <algorithm>
