@@ -1033,6 +1033,7 @@ def linear_bf16(x, w, y, bias=None, act="none", scale=1.0, res=None, stream=None
 
 
 def sample_workspace_bytes(n, vocab):
+    """Bytes that `sample` needs for n rows of vocab logits, or fewer of them (oes_sample_workspace)."""
     if not (abs(n) <= 0x7fffffff and abs(vocab) <= 0x7fffffff):
         _too_large("n x vocab", n, vocab)
     b = _I64()
