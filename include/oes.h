@@ -614,11 +614,12 @@ typedef struct {
  *   res    as x, of type res_elem; res_out may be res (then with the same strides)
  *   y      as x, bf16; y may be x if x is bf16 (then with the same strides)
  * Otherwise outputs must not overlap inputs or each other, and two rows of res_out or
- * of y share no element.  n >= 0, heads >= 1, n * heads < 2^31, dim a multiple of 8 in [8, 16384]; rows of x, res, res_out and y
- * 16-byte aligned, of gate too where gate_col is 1 (else 2-byte); strides >= 0; scale
- * finite.  A row whose squares (layer: of half its differences from the mean) add up to
- * more than 3.4e38 has a norm of 0, before b: NaN where it is infinite, and for a layer
- * norm with an infinity in every place; NaN gives NaN.  Async. */
+ * of y share no element.  n >= 0, heads >= 1, n * heads < 2^31, dim a multiple of 8 in
+ * [8, 16384]; rows of x, res, res_out and y 16-byte aligned, of gate too where gate_col
+ * is 1 (else 2-byte); strides >= 0; scale finite.  A row whose squares (layer: of half
+ * its differences from the mean) add up to more than 3.4e38 has a norm of 0, before b:
+ * NaN where it is infinite, and for a layer norm with an infinity in every place; NaN
+ * gives NaN.  Async. */
 enum { OES_GATE_PLAIN = 0, OES_GATE_SIGMOID = 1, OES_GATE_SILU = 2 };
 typedef struct {
   const oes_norm_spec *post, *pre;
@@ -642,13 +643,13 @@ oes_status oes_norm(const oes_norm_args *args, void *stream);
  *   OES_ACT_SWIGLU   silu(g) * u: W and bias have 2 N rows, [0, N) for g and [N, 2 N) for u,
  *                    as in the gate_up banks
  * Sums and the epilogue are fp32, y is rounded to nearest even once; 1 / (1 + exp(-v))
- * below 2^-126 (v < -87.3) counts as 0, here and in gates.  Rows of x reach
- * their own row of y only, rows of W their own column.  K a multiple of 8 in [8,
- * 2^20], N in [1, 2^22], n in [0, 2^19]; x, W and their rows 16-byte aligned, bias
- * 2-byte, y and res aligned to their elements; x_row, w_row >= K, y_row, res_row >=
- * N (the stride of a single row does not count); scale finite.  y may be res (then with
- * the same stride), and must not overlap an input otherwise.  OES_ERR_UNSUPPORTED beyond
- * these N and n.  Async. */
+ * below 2^-126 (v < -87.3) counts as 0, here and in gates.  Rows of x reach their own
+ * row of y only, rows of W their own column.  K a multiple of 8 in [8, 2^20], N in [1,
+ * 2^22], n in [0, 2^19]; x, W and their rows 16-byte aligned, bias 2-byte, y and res
+ * aligned to their elements; x_row, w_row >= K, y_row, res_row >= N (the stride of a
+ * single row does not count); scale finite.  y may be res (then with the same stride),
+ * and must not overlap an input otherwise.  OES_ERR_UNSUPPORTED beyond these N and n.
+ * Async. */
 enum { OES_ACT_NONE = 0, OES_ACT_SIGMOID = 1, OES_ACT_SILU = 2, OES_ACT_GELU = 3, OES_ACT_SWIGLU = 4 };
 oes_status oes_linear_bf16(const void *w, int64_t w_row, const void *bias, int32_t N, int32_t K, const void *x,
                            int64_t x_row, int32_t n, int32_t act, float scale, const void *res, int64_t res_row,

@@ -384,8 +384,9 @@ oes_status check_spec(const char *what, const oes_norm_spec *s, NormSpec &out) {
 bool rows_overlap(int64_t n, int64_t row, int64_t heads, int64_t head, int64_t dim) {
   if ((n > 1 && row < dim) || (heads > 1 && head < dim)) return true;
   if (n == 1 || heads == 1) return false;
+  const auto in_turn = [&](int64_t outer, int64_t inner, int64_t count) { return (outer - dim) / inner >= count - 1; };
+  if (in_turn(row, head, heads) || in_turn(head, row, n)) return false;   // all of a token behind the one before, or of a head
   if (n > heads) std::swap(n, heads), std::swap(row, head);
-  if (head >= dim && row - dim >= head && (row - dim) / head >= heads - 1) return false;   // one after the other
   for (int64_t t = 1; t < n; ++t) {   // fewer than 2^16; the heads next to a row t further on
     const __int128 at = (__int128)t * row, h = at / head, past = at - h * head;
     if ((h < heads && past < dim) || (h + 1 < heads && head - past < dim)) return true;
